@@ -455,6 +455,217 @@ int salr_moe_forward(const salr_moe_layer_t* G, const uint16_t* X, int64_t T,
                      const int32_t* expert_offsets, int64_t m_cap, uint16_t* Y,
                      void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * Around the grouped experts: the router, the way of the tokens to their
+ * experts' rows and back, and the gradients of each (the grouped layer
+ * itself takes rows that are already grouped by expert).
+ *
+ * A "slot" is one token's j-th choice: slot t * k + j of token t, k choices a
+ * token (1 <= k <= SALR_MOE_MAX_TOPK), n = T * k slots in all (n < 2^31 -
+ * 65536).  ids[slot] is its expert; an id outside [0, E) routes the slot
+ * nowhere (a padded token, a choice that was not filled): it takes no row and
+ * adds nothing.  rows[slot] is the slot's row among the rows grouped by
+ * expert, or -1.  Types: SALR_TYPE_BF16 or SALR_TYPE_F32 where a call names
+ * one; ids, rows and offsets are int32, router weights and their gradients
+ * float, token rows bf16.  Sums are held in fp32 and rounded once to bf16.
+ * T == 0 is allowed everywhere.  Results do not depend on timing: no call
+ * here sums with floating-point atomics.
+ */
+#define SALR_TYPE_BF16 0
+#define SALR_TYPE_F32 1
+#define SALR_MOE_MAX_TOPK 32
+
+/*
+ * salr_moe_route - each token's k experts and their weights.
+ *   ids[t][0..k)     the experts of the k largest logits of row t, largest
+ *                    first, equal logits by ascending expert;
+ *   weights[t][j]    p_j = softmax(logits[t])[ids[t][j]], or with renorm != 0
+ *                    p_j / (p_0 + ... + p_{k-1}).
+ * A logit of -inf is never chosen: a row with fewer than k others gets ids -1
+ * and weights 0 in the remaining places (a row of only -inf: all of them).
+ * A NaN logit is never chosen either; with renorm == 0 it makes the chosen
+ * experts' weights of its row NaN, and a +inf logit does so always.
+ * logits  device bf16 or float [T][E] (logits_type), 1 <= k <= E <= 4096.
+ * ids     device int32 [T][k]; weights device float [T][k].
+ * Asynchronous on `stream`.  Errors: INVALID_ARG (dimensions, nulls,
+ * alignment, type), HIP.
+ */
+int salr_moe_route(const void* logits, int32_t logits_type, int64_t T,
+                   int32_t E, int32_t k, int32_t renorm, int32_t* ids,
+                   float* weights, void* stream);
+
+/*
+ * salr_moe_route_backward - dL/dlogits from dL/dweights for the choice `ids`
+ * that salr_moe_route made of the same logits (the choice itself has no
+ * gradient).  With p the softmax of the row and dw_e the sum of dweights over
+ * the slots of expert e:
+ *   renorm == 0   dlogits_e = p_e (dw_e - sum_i p_i dw_i)        (all e)
+ *   renorm != 0   the same with p the softmax over the chosen experts only,
+ *                 0 elsewhere.
+ * ids outside [0, E) and their dweights are ignored (their dweights may be
+ * NaN); a row without any id gets zeros.  dlogits has the logits' type and is
+ * overwritten; it may be the logits' own buffer.  Asynchronous on `stream`.
+ * Errors: as salr_moe_route.
+ */
+int salr_moe_route_backward(const void* logits, int32_t logits_type, int64_t T,
+                            int32_t E, int32_t k, int32_t renorm,
+                            const int32_t* ids, const float* dweights,
+                            void* dlogits, void* stream);
+
+/* Workspace bytes of salr_moe_dispatch for at most T_max tokens of k slots
+ * over E experts (`out` host; 1 <= E <= 4096).  Errors: INVALID_ARG. */
+int salr_moe_dispatch_ws_bytes(int64_t T_max, int32_t k, int32_t E, size_t* out);
+
+/*
+ * salr_moe_dispatch - the slots sorted by expert (stable: by expert, then by
+ * slot) and the tokens' rows copied there, ready for salr_moe_forward:
+ *   expert_offsets  device int32 [E + 1]: off[e] = slots with an id below e
+ *                   (off[E]: routed slots).
+ *   rows            device int32 [T][k]: the slot's row, -1 where it has none.
+ *   slots           device int32 [T * k] or NULL: the slot of each row (the
+ *                   inverse of rows); entries from off[E] on are not written.
+ *   Xs              device bf16 [T * k][D]: Xs[rows[t][j]] = X[t]; rows from
+ *                   off[E] on are not written.  X and Xs both NULL: sort only.
+ * ids  device int32 [T][k], any values (see above), also the same expert
+ *      twice for one token.
+ * X    device bf16 [T][D], 1 <= D <= 2^20 (Xs may not alias it).
+ * ws   device, salr_moe_dispatch_ws_bytes long for some T_max >= T with this
+ *      k and E; contents on entry do not matter.  Calls that share it (or
+ *      captured graphs of such calls) must be ordered.
+ * The gradient of the copy is salr_moe_combine(dXs, rows, weights = NULL).
+ * Asynchronous on `stream`.  Errors: INVALID_ARG, WORKSPACE, HIP.
+ */
+int salr_moe_dispatch(const int32_t* ids, int64_t T, int32_t k, int32_t E,
+                      const uint16_t* X, int64_t D, int32_t* expert_offsets,
+                      int32_t* rows, int32_t* slots, uint16_t* Xs, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * salr_moe_combine - the experts' outputs back to their tokens, weighted:
+ *   Y[t] = base[t] + sum_j weights[t][j] Ys[rows[t][j]]
+ * Ys       device bf16 [R][D] (R rows; 1 <= D <= 2^20, any D).
+ * rows     device int32 [T][k]; an entry outside [0, R) adds nothing: its
+ *          weight and its row are not used (they may be NaN).
+ * weights  device float [T][k], or NULL: ones.
+ * base     device bf16 [T][D] (a shared expert's output, the residual
+ *          stream; may be Y itself), or NULL: zeros.
+ * Y        device bf16 [T][D] (may not alias Ys).  A token without any row gets
+ *          base, or zeros.
+ * Asynchronous on `stream`.  Errors: INVALID_ARG, HIP.
+ */
+int salr_moe_combine(const uint16_t* Ys, int64_t R, const int32_t* rows,
+                     const float* weights, const uint16_t* base, int64_t T,
+                     int32_t k, int64_t D, uint16_t* Y, void* stream);
+
+/*
+ * salr_moe_combine_backward - the gradients of salr_moe_combine in one pass
+ * (that of base is dY itself):
+ *   dYs[rows[t][j]]  = weights[t][j] dY[t]             (bf16)
+ *   dweights[t][j]   = sum_d dY[t][d] Ys[rows[t][j]][d]  (float)
+ * rows      as for salr_moe_combine, no row named by two slots (as
+ *           salr_moe_dispatch writes them); a slot whose entry is outside
+ *           [0, R) gets dweights 0.
+ * weights   device float [T][k], or NULL: ones.
+ * dYs       device bf16 [R][D] or NULL to skip; rows that no slot names are
+ *           left as they were.  May be Ys's own buffer, not dY's.
+ * dweights  device float [T][k] or NULL to skip (Ys is then not read and may
+ *           be NULL).
+ * Asynchronous on `stream`.  Errors: INVALID_ARG, HIP.
+ */
+int salr_moe_combine_backward(const uint16_t* dY, const uint16_t* Ys, int64_t R,
+                              const int32_t* rows, const float* weights,
+                              int64_t T, int32_t k, int64_t D, uint16_t* dYs,
+                              float* dweights, void* stream);
+
+/*
+ * AdamW over many tensors in one launch: the step that follows
+ * salr_linear_backward for the adapters of any number of layers and experts.
+ * For every element, with g = grad * grad_scale and step t (from 1):
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, p rounded to its type at the end (a bf16 parameter loses updates
+ * below half its last place; give it a float master copy, which is then
+ * what the step updates, p being its rounding).
+ *
+ * States are float, or 8 bits (SALR_STATE_8BIT): m and s = sqrt(v) of each
+ * run of SALR_ADAMW_BLOCK elements of a tensor (the last may be shorter) as
+ * e4m3 codes (OCP FP8: 4 exponent, 3 mantissa bits) times one float scale a
+ * run, scale = largest |value| / 448, nearest code, ties to even; an s above
+ * zero takes at least the smallest code (else a small v would vanish before
+ * its m).  A run whose largest |value| is below 2^-100 is stored as zeros.
+ * The step uses the new m and v before they are rounded for storage.
+ * States of zero bytes are zeros in both forms: the start of training.
+ * A NaN gradient makes its own element NaN; an infinite one its element, and
+ * in 8 bits its whole run.
+ */
+#define SALR_STATE_F32 0
+#define SALR_STATE_8BIT 1
+#define SALR_ADAMW_BLOCK 256
+
+/* One tensor of n elements: plain device pointers. */
+typedef struct salr_adamw_tensor {
+  void* p;          /* parameters (p_type)                                  */
+  const void* g;    /* gradients (g_type)                                   */
+  void* m;          /* float [n], or e4m3 codes uint8 [n]                   */
+  void* v;          /* float [n], or the codes of sqrt(v) uint8 [n]         */
+  float* m_scale;   /* 8-bit states: float [ceil(n/SALR_ADAMW_BLOCK)]       */
+  float* v_scale;   /* 8-bit states: float [ceil(n/SALR_ADAMW_BLOCK)]       */
+  float* master;    /* float [n] of a bf16 parameter, or NULL in all        */
+  int64_t n;        /* elements, 0 <= n < 2^40                              */
+} salr_adamw_tensor_t;
+
+/* A plan: the tensors of one parameter group laid out for the step. */
+typedef struct salr_adamw_plan {
+  void* table;        /* device, the caller's buffer                        */
+  int64_t chunks;     /* the entries below are salr_adamw_plan's            */
+  int32_t count;
+  int32_t p_type, g_type, state_type, has_master;
+} salr_adamw_plan_t;
+
+/* What one step uses.  step >= 1; lr, eps, weight_decay >= 0 and finite, 0 <=
+ * beta1, beta2 < 1. */
+typedef struct salr_adamw_step_args {
+  int64_t step;
+  double lr, beta1, beta2, eps, weight_decay, grad_scale;
+} salr_adamw_step_args_t;
+
+/* Bytes of the plan's device buffer for `count` tensors of n[i] elements (`n`
+ * and `out` host; count <= 2^20, at most 2^24 - 1 runs of 2048 elements in
+ * all).  Errors: INVALID_ARG. */
+int salr_adamw_plan_bytes(const int64_t* n, int32_t count, size_t* out);
+
+/*
+ * salr_adamw_plan - build a plan: once, for tensors that stay where they are.
+ * tensors  host array of `count` records (all with a master, or none;
+ *          masters only for bf16 parameters).  Everything that a step writes
+ *          (p, m, v, scales, master) must be disjoint, over all tensors.
+ * table    device buffer of at least salr_adamw_plan_bytes; it belongs to
+ *          the plan until its last step.
+ * out      host.
+ * SYNCHRONOUS on `stream` (the table is copied from host memory); not under
+ * graph capture (UNSUPPORTED).  Errors: INVALID_ARG (nulls, alignment,
+ * types, overlaps), WORKSPACE, UNSUPPORTED (also: host memory ran out), HIP.
+ */
+int salr_adamw_plan(const salr_adamw_tensor_t* tensors, int32_t count,
+                    int32_t p_type, int32_t g_type, int32_t state_type,
+                    void* table, size_t table_bytes, salr_adamw_plan_t* out,
+                    void* stream);
+
+/*
+ * salr_adamw_step - one step over every tensor of the plan, in place.
+ * args  host.
+ * dyn   NULL, or device float [4] that replaces args' step, lr and grad_scale
+ *       (for steps in a captured graph, whose host arguments are fixed):
+ *       {lr, grad_scale, 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)}, read
+ *       when the step runs.
+ * Asynchronous on `stream`, capturable.  Errors: INVALID_ARG, HIP.
+ */
+int salr_adamw_step(const salr_adamw_plan_t* plan,
+                    const salr_adamw_step_args_t* args, const float* dyn,
+                    void* stream);
+
 /* Static English text for a status code (never NULL). */
 const char* salr_status_string(int status);
 

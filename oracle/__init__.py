@@ -34,8 +34,20 @@ Parity status of each function (what pins it, see tests/test_oracle_*.py):
   moe.grouped_forward              pinned: per-token brute force from the
                                    original weights, planted boundary shift
                                    and expert swap
+  routing.route / route_backward
+                                   pinned: hand cases, finite differences of
+                                   the weights, planted missing terms
+  routing.dispatch / combine / combine_backward
+                                   pinned: a stable argsort, finite
+                                   differences, planted swaps
+  adamw.step                       pinned: torch.optim.AdamW in float64, a
+                                   first step in closed form
+  adamw.code_values / encode / decode
+                                   pinned: torch's e4m3 conversion over all
+                                   codes, exact round trips, the half-step
+                                   bound, planted mistakes
   The pages print no worked example and no intermediate values, so no
   function is pinned to a number printed on the pages.
 """
 
-from . import backward, bf16, moe, nf4, salr  # noqa: F401
+from . import adamw, backward, bf16, moe, nf4, routing, salr  # noqa: F401

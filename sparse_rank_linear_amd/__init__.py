@@ -10,13 +10,20 @@ arguments (binding.py) and draws synthetic inputs (synth.py).
 """
 
 from .binding import (  # noqa: F401
+    ADAMW_BLOCK,
     EXPORTS,
     LIB_PATH,
+    MOE_MAX_TOPK,
     NOALLOC_SCRATCH_BYTES,
+    AdamWPlan,
     SalrError,
     SalrLayer,
     SalrMoE,
     WaitTimeout,
+    adamw_dyn,
+    adamw_plan,
+    adamw_states,
+    adamw_step,
     backward_workspace,
     backward_ws_bytes,
     encode,
@@ -26,9 +33,17 @@ from .binding import (  # noqa: F401
     linear_backward,
     linear_forward,
     linear_forward_noalloc,
+    moe_combine,
+    moe_combine_backward,
+    moe_dispatch,
+    moe_dispatch_backward,
+    moe_dispatch_workspace,
+    moe_dispatch_ws_bytes,
     moe_encode_expert,
     moe_forward,
     moe_query_sizes,
+    moe_route,
+    moe_route_backward,
     moe_workspace,
     nf4_levels,
     probe_mfma,
@@ -43,8 +58,12 @@ from .binding import (  # noqa: F401
 )
 
 __all__ = [
-    "EXPORTS", "LIB_PATH", "NOALLOC_SCRATCH_BYTES", "SalrError", "SalrLayer", "SalrMoE", "WaitTimeout", "backward_workspace",
-    "backward_ws_bytes", "encode", "forward_workspace", "fuse", "lib", "linear_backward", "linear_forward",
-    "linear_forward_noalloc", "moe_encode_expert", "moe_forward", "moe_query_sizes", "moe_workspace", "nf4_levels", "probe_mfma", "probe_stream_read", "quantize_nf4", "query_sizes",
-    "transpose_count", "transpose_layer", "transpose_ws_bytes", "wait_error", "workspace",
+    "ADAMW_BLOCK", "AdamWPlan", "EXPORTS", "LIB_PATH", "MOE_MAX_TOPK", "NOALLOC_SCRATCH_BYTES", "SalrError",
+    "SalrLayer", "SalrMoE", "WaitTimeout", "adamw_dyn", "adamw_plan", "adamw_states", "adamw_step",
+    "backward_workspace", "backward_ws_bytes", "encode", "forward_workspace", "fuse", "lib", "linear_backward",
+    "linear_forward", "linear_forward_noalloc", "moe_combine", "moe_combine_backward", "moe_dispatch",
+    "moe_dispatch_backward", "moe_dispatch_workspace", "moe_dispatch_ws_bytes", "moe_encode_expert", "moe_forward",
+    "moe_query_sizes", "moe_route", "moe_route_backward", "moe_workspace", "nf4_levels", "probe_mfma",
+    "probe_stream_read", "quantize_nf4", "query_sizes", "transpose_count", "transpose_layer", "transpose_ws_bytes",
+    "wait_error", "workspace",
 ]

@@ -44,6 +44,15 @@ EXPORTS = (
     "salr_moe_query_sizes",
     "salr_moe_expert",
     "salr_moe_forward",
+    "salr_moe_route",
+    "salr_moe_route_backward",
+    "salr_moe_dispatch_ws_bytes",
+    "salr_moe_dispatch",
+    "salr_moe_combine",
+    "salr_moe_combine_backward",
+    "salr_adamw_plan_bytes",
+    "salr_adamw_plan",
+    "salr_adamw_step",
     # include/salr_probe.h
     "salr_probe_stream_read",
     "salr_probe_mfma",
@@ -121,6 +130,27 @@ class salr_encode_opts_t(C.Structure):
     _fields_ = [("oversample", C.c_int32), ("iters", C.c_int32), ("seed", C.c_uint64)]
 
 
+class salr_adamw_tensor_t(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("p", "g", "m", "v", "m_scale", "v_scale", "master")] + [("n", C.c_int64)]
+
+
+class salr_adamw_plan_t(C.Structure):
+    _fields_ = [
+        ("table", C.c_void_p),
+        ("chunks", C.c_int64),
+        ("count", C.c_int32),
+        ("p_type", C.c_int32),
+        ("g_type", C.c_int32),
+        ("state_type", C.c_int32),
+        ("has_master", C.c_int32),
+    ]
+
+
+class salr_adamw_step_args_t(C.Structure):
+    _fields_ = [("step", C.c_int64)] + [(n, C.c_double) for n in (
+        "lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")]
+
+
 _LIB = None
 
 
@@ -178,6 +208,32 @@ def _lib():
         lib.salr_moe_forward.argtypes = [C.POINTER(salr_moe_layer_t), C.c_void_p, C.c_int64, C.c_void_p,
                                          C.c_int64, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
         lib.salr_moe_forward.restype = C.c_int
+        lib.salr_moe_route.argtypes = [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
+                                       C.c_void_p, C.c_void_p]
+        lib.salr_moe_route.restype = C.c_int
+        lib.salr_moe_route_backward.argtypes = [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int32, C.c_int32,
+                                                C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]
+        lib.salr_moe_route_backward.restype = C.c_int
+        lib.salr_moe_dispatch_ws_bytes.argtypes = [C.c_int64, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]
+        lib.salr_moe_dispatch_ws_bytes.restype = C.c_int
+        lib.salr_moe_dispatch.argtypes = [C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.c_void_p, C.c_int64,
+                                          C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
+                                          C.c_void_p]
+        lib.salr_moe_dispatch.restype = C.c_int
+        lib.salr_moe_combine.argtypes = [C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+                                         C.c_int32, C.c_int64, C.c_void_p, C.c_void_p]
+        lib.salr_moe_combine.restype = C.c_int
+        lib.salr_moe_combine_backward.argtypes = [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                                  C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p]
+        lib.salr_moe_combine_backward.restype = C.c_int
+        lib.salr_adamw_plan_bytes.argtypes = [C.POINTER(C.c_int64), C.c_int32, C.POINTER(C.c_size_t)]
+        lib.salr_adamw_plan_bytes.restype = C.c_int
+        lib.salr_adamw_plan.argtypes = [C.POINTER(salr_adamw_tensor_t), C.c_int32, C.c_int32, C.c_int32, C.c_int32,
+                                        C.c_void_p, C.c_size_t, C.POINTER(salr_adamw_plan_t), C.c_void_p]
+        lib.salr_adamw_plan.restype = C.c_int
+        lib.salr_adamw_step.argtypes = [C.POINTER(salr_adamw_plan_t), C.POINTER(salr_adamw_step_args_t), C.c_void_p,
+                                        C.c_void_p]
+        lib.salr_adamw_step.restype = C.c_int
         lib.salr_probe_stream_read.argtypes = [C.c_void_p, C.c_size_t, C.c_void_p, C.c_int32, C.c_void_p]
         lib.salr_probe_stream_read.restype = C.c_int
         lib.salr_probe_mfma.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]
@@ -693,6 +749,330 @@ def moe_forward(moe: SalrMoE, X, expert_offsets, Y=None, m_cap: int = 0, ws=None
                                  ws.numel() * ws.element_size(), _stream_ptr(stream))
     _check(st, "salr_moe_forward")
     return Y
+
+
+# ----------------------------------------------------------------------------
+# Around the grouped experts, and the optimizer.
+#
+# These calls run on the device of their tensors (also when another one is
+# current), on `stream` or that device's current stream; what they allocate
+# belongs to that stream.
+TYPE_BF16, TYPE_F32 = 0, 1
+STATE_F32, STATE_8BIT = 0, 1
+MOE_MAX_TOPK = 32
+ADAMW_BLOCK = 256
+
+
+class _Place:
+    """The device and stream of one call."""
+
+    __slots__ = ("dev", "stream", "_dev_ctx", "_stream_ctx")
+
+    def __init__(self, dev, stream):
+        import torch
+
+        if dev.type != "cuda":
+            raise ValueError("device tensors are needed")
+        self.dev = dev
+        self._dev_ctx = self._stream_ctx = None
+        if dev.index != torch.cuda.current_device():
+            self._dev_ctx = torch.cuda.device(dev)
+        if stream is not None:
+            if stream.device_index != dev.index:
+                raise ValueError("stream and tensors are on different devices")
+            self._stream_ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        import torch
+
+        if self._dev_ctx is not None:
+            self._dev_ctx.__enter__()
+        if self._stream_ctx is not None:
+            self._stream_ctx.__enter__()
+        self.stream = torch.cuda.current_stream(self.dev).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self._stream_ctx is not None:
+            self._stream_ctx.__exit__(*exc)
+        if self._dev_ctx is not None:
+            self._dev_ctx.__exit__(*exc)
+        return False
+
+
+def _ptr(t, name, dtype, shape, dev):
+    """The address of tensor t after checking it (an empty one: None)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev} (is on {t.device})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() or None
+
+
+def _float_type(t, name):
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return TYPE_BF16
+    if t.dtype == torch.float32:
+        return TYPE_F32
+    raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+
+
+def moe_route(logits, k: int, renorm: bool = True, ids=None, weights=None, stream=None):
+    """Each token's k experts (int32 [T][k], largest logit first) and their
+    softmax weights (float [T][k]; renorm: over the chosen experts) from
+    router logits, bf16 or float [T][E] (salr_moe_route).  -inf logits are
+    never chosen: id -1, weight 0 where too few others are left."""
+    import torch
+
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T][E]")
+    T, E = logits.shape
+    dev, shape = logits.device, (T, k)
+    with _Place(dev, stream) as at:
+        if ids is None:
+            ids = torch.empty(shape, dtype=torch.int32, device=dev)
+        if weights is None:
+            weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        _check(_lib().salr_moe_route(_ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"),
+                                     T, E, k, bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
+                                     _ptr(weights, "weights", torch.float32, shape, dev), at.stream),
+               "salr_moe_route")
+    return ids, weights
+
+
+def moe_route_backward(logits, ids, dweights, renorm: bool = True, dlogits=None, stream=None):
+    """dL/dlogits (the logits' type, [T][E]) from dL/dweights for the choice
+    moe_route made (salr_moe_route_backward)."""
+    import torch
+
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise ValueError("logits must be [T][E] and ids [T][k]")
+    T, E = logits.shape
+    dev, shape = logits.device, (T, ids.shape[1])
+    with _Place(dev, stream) as at:
+        if dlogits is None:
+            dlogits = torch.empty_like(logits)
+        _check(_lib().salr_moe_route_backward(
+            _ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"), T, E, shape[1],
+            bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
+            _ptr(dweights, "dweights", torch.float32, shape, dev),
+            _ptr(dlogits, "dlogits", logits.dtype, (T, E), dev), at.stream), "salr_moe_route_backward")
+    return dlogits
+
+
+def moe_dispatch_ws_bytes(T_max: int, k: int, E: int) -> int:
+    out = C.c_size_t()
+    _check(_lib().salr_moe_dispatch_ws_bytes(T_max, k, E, C.byref(out)), "salr_moe_dispatch_ws_bytes")
+    return out.value
+
+
+def moe_dispatch_workspace(T_max: int, k: int, E: int, device="cuda"):
+    return workspace(moe_dispatch_ws_bytes(T_max, k, E), device)
+
+
+def moe_dispatch(ids, E: int, X=None, Xs=None, offsets=None, rows=None, slots=None, ws=None, stream=None):
+    """The slots (token, choice) of ids (int32 [T][k]) sorted by expert, and
+    the tokens' rows X (bf16 [T][D]) copied there for moe_forward
+    (salr_moe_dispatch).  Returns (Xs bf16 [T * k][D] or None, offsets int32
+    [E + 1], rows int32 [T][k], slots int32 [T * k]); ids outside [0, E) get
+    row -1, and Xs and slots are not written from row offsets[E] on."""
+    import torch
+
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T][k]")
+    T, k = ids.shape
+    n, D, dev = T * k, 0, ids.device
+    with _Place(dev, stream) as at:
+        if offsets is None:
+            offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        if rows is None:
+            rows = torch.empty((T, k), dtype=torch.int32, device=dev)
+        if slots is None:
+            slots = torch.empty(n, dtype=torch.int32, device=dev)
+        x = xs = None
+        if X is not None:
+            if X.dim() != 2:
+                raise ValueError("X must be [T][D]")
+            D = X.shape[1]
+            if Xs is None:
+                Xs = torch.empty((n, D), dtype=torch.bfloat16, device=dev)
+            x = _ptr(X, "X", torch.bfloat16, (T, D), dev)
+            xs = _ptr(Xs, "Xs", torch.bfloat16, (n, D), dev)
+        elif Xs is not None:
+            raise ValueError("Xs needs X")
+        if ws is None:
+            ws = torch.empty(moe_dispatch_ws_bytes(T, k, E), dtype=torch.uint8, device=dev)
+        elif ws.device != dev:
+            raise ValueError(f"ws must be on {dev} (is on {ws.device})")
+        _check(_lib().salr_moe_dispatch(_ptr(ids, "ids", torch.int32, (T, k), dev), T, k, E, x, D,
+                                        _ptr(offsets, "offsets", torch.int32, (E + 1,), dev),
+                                        _ptr(rows, "rows", torch.int32, (T, k), dev),
+                                        _ptr(slots, "slots", torch.int32, (n,), dev), xs, ws.data_ptr(),
+                                        ws.numel() * ws.element_size(), at.stream), "salr_moe_dispatch")
+    return Xs, offsets, rows, slots
+
+
+def _combine(Ys, rows, weights, base, Y, stream):
+    import torch
+
+    if Ys.dim() != 2 or rows.dim() != 2:
+        raise ValueError("the rows' values must be [R][D] and rows [T][k]")
+    (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
+    bf16 = torch.bfloat16
+    with _Place(dev, stream) as at:
+        if Y is None:
+            Y = torch.empty((T, D), dtype=bf16, device=dev)
+        _check(_lib().salr_moe_combine(
+            _ptr(Ys, "the rows' values", bf16, (R, D), dev), R, _ptr(rows, "rows", torch.int32, (T, k), dev),
+            None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev),
+            None if base is None else _ptr(base, "base", bf16, (T, D), dev), T, k, D,
+            _ptr(Y, "the output", bf16, (T, D), dev), at.stream), "salr_moe_combine")
+    return Y
+
+
+def moe_combine(Ys, rows, weights=None, base=None, Y=None, stream=None):
+    """Y[t] = base[t] + sum_j weights[t][j] Ys[rows[t][j]] (bf16 [T][D]; fp32
+    sum): the experts' outputs Ys (bf16 [R][D]) back at their tokens
+    (salr_moe_combine).  rows are moe_dispatch's; -1 adds nothing."""
+    return _combine(Ys, rows, weights, base, Y, stream)
+
+
+def moe_dispatch_backward(dXs, rows, dX=None, stream=None):
+    """The gradient of moe_dispatch's copy: dX[t] = sum_j dXs[rows[t][j]]
+    (bf16 [T][D]; salr_moe_combine with unit weights)."""
+    return _combine(dXs, rows, None, None, dX, stream)
+
+
+def moe_combine_backward(dY, Ys, rows, weights=None, dYs=None, dweights=None, stream=None):
+    """The gradients of moe_combine: (dYs bf16 [R][D], dYs[rows[t][j]] =
+    weights[t][j] dY[t]; dweights float [T][k], the products <dY[t],
+    Ys[rows[t][j]]>).  A dYs made here is zero in the rows that no slot
+    names; a given one keeps them (salr_moe_combine_backward)."""
+    import torch
+
+    if Ys.dim() != 2 or rows.dim() != 2:
+        raise ValueError("Ys must be [R][D] and rows [T][k]")
+    (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
+    bf16 = torch.bfloat16
+    with _Place(dev, stream) as at:
+        if dYs is None:
+            dYs = torch.zeros((R, D), dtype=bf16, device=dev)
+        if dweights is None:
+            dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        _check(_lib().salr_moe_combine_backward(
+            _ptr(dY, "dY", bf16, (T, D), dev), _ptr(Ys, "Ys", bf16, (R, D), dev), R,
+            _ptr(rows, "rows", torch.int32, (T, k), dev),
+            None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev), T, k, D,
+            _ptr(dYs, "dYs", bf16, (R, D), dev), _ptr(dweights, "dweights", torch.float32, (T, k), dev), at.stream),
+            "salr_moe_combine_backward")
+    return dYs, dweights
+
+
+def adamw_states(params, bits: int = 32, master: bool = False) -> dict:
+    """Fresh AdamW states of the tensors in `params`: the lists m and v
+    (float, or with bits = 8 e4m3 codes with the lists m_scale and v_scale)
+    and, with master, float copies of bf16 parameters; keywords of
+    adamw_plan."""
+    import torch
+
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+    zeros = lambda n, dtype: [torch.zeros(n(p), dtype=dtype, device=p.device) for p in params]
+    params = list(params)
+    dtype = torch.float8_e4m3fn if bits == 8 else torch.float32
+    size, runs = (lambda p: p.numel()), (lambda p: -(-p.numel() // ADAMW_BLOCK))
+    return {"m": zeros(size, dtype), "v": zeros(size, dtype),
+            "m_scale": zeros(runs, torch.float32) if bits == 8 else None,
+            "v_scale": zeros(runs, torch.float32) if bits == 8 else None,
+            "master": [p.detach().float() for p in params] if master else None}
+
+
+@dataclass
+class AdamWPlan:
+    """Tensors laid out for adamw_step (include/salr.h, salr_adamw_plan_t).
+    Holds on to them: they and the plan outlive every step and captured
+    graph that uses them."""
+
+    desc: salr_adamw_plan_t
+    table: object
+    tensors: list
+    device: object
+
+
+def adamw_plan(params, grads, m, v, m_scale=None, v_scale=None, master=None, stream=None) -> AdamWPlan:
+    """A plan for adamw_step over the tensors in `params` (all bf16 or all
+    float) with their gradients (all bf16 or all float) and states (see
+    adamw_states), element i of every list belonging together; all tensors
+    contiguous and 16-byte aligned, written ones disjoint.  Synchronous."""
+    import torch
+
+    lists = {"params": params, "grads": grads, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale,
+             "master": master}
+    lists = {name: list(ts) for name, ts in lists.items() if ts is not None}
+    params, count = lists["params"], len(lists["params"])
+    if count == 0:
+        raise ValueError("adamw_plan needs at least one tensor")
+    for name, ts in lists.items():
+        if len(ts) != count:
+            raise ValueError(f"{name} has {len(ts)} tensors for {count} parameters")
+    dev = params[0].device
+    bits8 = lists["m"][0].dtype != torch.float32
+    state_dtypes = (torch.float8_e4m3fn, torch.uint8) if bits8 else (torch.float32,)
+    if ("m_scale" in lists, "v_scale" in lists) != (bits8, bits8):
+        raise ValueError("m_scale and v_scale belong to 8-bit states, and only to them")
+    dtypes = {"params": (params[0].dtype,), "grads": (lists["grads"][0].dtype,), "m": state_dtypes,
+              "v": state_dtypes, "m_scale": (torch.float32,), "v_scale": (torch.float32,),
+              "master": (torch.float32,)}
+    field = {"params": "p", "grads": "g"}
+    recs = (salr_adamw_tensor_t * count)()
+    for name, ts in lists.items():
+        for i, t in enumerate(ts):
+            n = params[i].numel()
+            want = -(-n // ADAMW_BLOCK) if name.endswith("_scale") else n
+            if t.dtype not in dtypes[name]:
+                raise TypeError(f"{name}[{i}] must be {dtypes[name][0]} (got {t.dtype})")
+            if t.numel() != want:
+                raise ValueError(f"{name}[{i}] must have {want} elements (got {t.numel()})")
+            if t.device != dev:
+                raise ValueError(f"{name}[{i}] must be on {dev} (is on {t.device})")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be contiguous")
+            setattr(recs[i], field.get(name, name), t.data_ptr() or None)
+            recs[i].n = n
+    desc, nbytes = salr_adamw_plan_t(), C.c_size_t()
+    sizes = (C.c_int64 * count)(*[r.n for r in recs])
+    _check(_lib().salr_adamw_plan_bytes(sizes, count, C.byref(nbytes)), "salr_adamw_plan_bytes")
+    p_type, g_type = _float_type(params[0], "params"), _float_type(lists["grads"][0], "grads")
+    with _Place(dev, stream) as at:
+        table = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+        _check(_lib().salr_adamw_plan(recs, count, p_type, g_type, STATE_8BIT if bits8 else STATE_F32,
+                                      table.data_ptr(), nbytes.value, C.byref(desc), at.stream), "salr_adamw_plan")
+    return AdamWPlan(desc, table, [t for ts in lists.values() for t in ts], dev)
+
+
+def adamw_dyn(step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, grad_scale: float = 1.0) -> list:
+    """The four floats of adamw_step's `dyn` tensor for one step."""
+    return [lr, grad_scale, 1.0 / (1.0 - beta1 ** step), (1.0 - beta2 ** step) ** -0.5]
+
+
+def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.01, grad_scale: float = 1.0, dyn=None, stream=None):
+    """One AdamW step (number `step`, from 1) over every tensor of the plan,
+    in place and in one launch (salr_adamw_step).  dyn: a device float
+    tensor [4] with adamw_dyn's values, read when the step runs instead of
+    step, lr and grad_scale (for captured graphs)."""
+    import torch
+
+    args = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale)
+    with _Place(plan.device, stream) as at:
+        d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (4,), plan.device)
+        _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, at.stream), "salr_adamw_step")
 
 
 def probe_stream_read(src, sink, workgroups: int, stream=None):

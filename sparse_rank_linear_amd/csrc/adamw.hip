@@ -1,0 +1,221 @@
+// AdamW over many tensors in one launch (include/salr.h, salr_adamw_step).
+//
+// Per element, in fp32:  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+// p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
+// 8-bit states hold m and s = sqrt(v) of 256 elements as e4m3 codes times
+// largest / 448 (v spans twice the exponents of its root, which the format's
+// 2^-9 .. 448 would not hold).
+//
+// One workgroup per 2048 elements of a tensor, found in the plan's chunk
+// list; 8 consecutive elements a thread, so a float array moves 32 bytes and
+// the codes 8 bytes a thread, and an 8-bit run is 32 lanes of one wave.
+// Bound by HBM: 24 bytes an element with float states, 12 with 8-bit ones
+// (bf16 parameters, float gradients, no master).
+#include <hip/hip_runtime.h>
+
+#include "salr_device.hpp"
+#include "salr_kernels.hpp"
+
+namespace salr {
+namespace {
+
+constexpr int kAdamwThreads = 256;
+constexpr int kPer = 8;  // elements a thread
+static_assert(kAdamwThreads * kPer == kAdamwChunk, "one chunk per workgroup");
+constexpr int kRunLanes = 256 / kPer;
+constexpr float kTiny = 0x1p-100f;
+
+// 8 elements from i on, those at or past n read as 0 and are not written.
+// Pointers are 16-byte aligned and i is a multiple of 8, so whole groups move
+// as 16-byte vectors.
+__device__ __forceinline__ void load8(const float* p, int64_t i, int64_t n, float* x) {
+  if (i + kPer <= n) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p + i), b = *reinterpret_cast<const f32x4_t*>(p + i + 4);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      x[c] = a[c];
+      x[c + 4] = b[c];
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) x[c] = i + c < n ? p[i + c] : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, int64_t i, int64_t n, float* x) {
+  if (i + kPer <= n) {
+    const u32x4_t a = load16(p + i);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      x[2 * c] = bf16_to_f32((uint16_t)a[c]);
+      x[2 * c + 1] = bf16_to_f32((uint16_t)(a[c] >> 16));
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) x[c] = i + c < n ? bf16_to_f32(p[i + c]) : 0.f;
+  }
+}
+__device__ __forceinline__ void store8(float* p, int64_t i, int64_t n, const float* x) {
+  if (i + kPer <= n) {
+    *reinterpret_cast<f32x4_t*>(p + i) = f32x4_t{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4_t*>(p + i + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
+  } else {
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+      if (i + c < n) p[i + c] = x[c];
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, int64_t i, int64_t n, const float* x) {
+  if (i + kPer <= n) {
+    u32x4_t w;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[c] = (uint32_t)f32_to_bf16(x[2 * c]) | ((uint32_t)f32_to_bf16(x[2 * c + 1]) << 16);
+    *reinterpret_cast<u32x4_t*>(p + i) = w;
+  } else {
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+      if (i + c < n) p[i + c] = f32_to_bf16(x[c]);
+  }
+}
+
+// 8 codes as two words (the codes past n as 0).
+__device__ __forceinline__ u32x2_t load_codes(const uint8_t* p, int64_t i, int64_t n) {
+  if (i + kPer <= n) return *reinterpret_cast<const u32x2_t*>(p + i);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int c = 0; c < kPer; ++c)
+    if (i + c < n) w[c / 4] |= (uint32_t)p[i + c] << (8 * (c % 4));
+  return u32x2_t{w[0], w[1]};
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, u32x2_t w) {
+  if (i + kPer <= n) {
+    *reinterpret_cast<u32x2_t*>(p + i) = w;
+  } else {
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+      if (i + c < n) p[i + c] = (uint8_t)((c < 4 ? w.x : w.y) >> (8 * (c % 4)));
+  }
+}
+__device__ __forceinline__ void decode8(u32x2_t w, float scale, float* x) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int word = (int)(h ? w.y : w.x);
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(word, false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(word, true);
+    x[4 * h] = lo[0] * scale;
+    x[4 * h + 1] = lo[1] * scale;
+    x[4 * h + 2] = hi[0] * scale;
+    x[4 * h + 3] = hi[1] * scale;
+  }
+}
+__device__ __forceinline__ u32x2_t encode8(const float* x) {
+  int w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    w[h] = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h], x[4 * h + 1], 0, false);
+    w[h] = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h + 2], x[4 * h + 3], w[h], true);
+  }
+  return u32x2_t{(uint32_t)w[0], (uint32_t)w[1]};
+}
+
+// The largest |x| of a run (32 lanes; NaN left aside), the run's scale and
+// its inverse (0 and 0 for a run of zeros).
+__device__ __forceinline__ void run_scale(const float* x, float* scale, float* inv) {
+  float top = 0.f;
+#pragma unroll
+  for (int c = 0; c < kPer; ++c) top = fmaxf(top, fabsf(x[c]));
+#pragma unroll
+  for (int d = kRunLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kRunLanes));
+  const bool live = top >= kTiny;
+  *scale = live ? top / 448.f : 0.f;
+  *inv = live ? 448.f / top : 0.f;
+}
+
+template <class P, class G, bool S8, bool MASTER>
+__global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwArgs a) {
+#pragma clang fp contract(off)
+  const AdamwChunk ch = a.chunks[blockIdx.x];
+  const AdamwTensor t = a.tensors[ch.tensor];
+  const int64_t i = (int64_t)ch.chunk * kAdamwChunk + threadIdx.x * kPer;
+  float decay = a.decay, rate = a.rate, gs = a.grad_scale, isb2 = a.inv_sqrt_bias2;
+  if (a.dyn) {
+    const float lr = a.dyn[0];
+    gs = a.dyn[1];
+    decay = 1.f - lr * a.weight_decay;
+    rate = lr * a.dyn[2];
+    isb2 = a.dyn[3];
+  }
+  float g[kPer], m[kPer], v[kPer], p[kPer], s[kPer];
+  load8(static_cast<const G*>(t.g), i, t.n, g);
+  const int64_t run = i / 256;
+  if constexpr (S8) {
+    const bool in = i < t.n;
+    const u32x2_t mc = load_codes(static_cast<const uint8_t*>(t.m), i, t.n);
+    const u32x2_t vc = load_codes(static_cast<const uint8_t*>(t.v), i, t.n);
+    decode8(mc, in ? t.ms[run] : 0.f, m);
+    decode8(vc, in ? t.vs[run] : 0.f, s);
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) v[c] = s[c] * s[c];
+  } else {
+    load8(static_cast<const float*>(t.m), i, t.n, m);
+    load8(static_cast<const float*>(t.v), i, t.n, v);
+  }
+  if constexpr (MASTER) load8(t.master, i, t.n, p);
+  else load8(static_cast<const P*>(t.p), i, t.n, p);
+#pragma unroll
+  for (int c = 0; c < kPer; ++c) {
+    g[c] *= gs;
+    m[c] = m[c] * a.beta1 + g[c] * a.rest1;
+    v[c] = v[c] * a.beta2 + (g[c] * g[c]) * a.rest2;
+    s[c] = sqrtf(v[c]);
+    p[c] = p[c] * decay - (m[c] / (s[c] * isb2 + a.eps)) * rate;
+  }
+  if constexpr (MASTER) store8(t.master, i, t.n, p);
+  store8(static_cast<P*>(t.p), i, t.n, p);
+  if constexpr (S8) {
+    float scale_m, inv_m, scale_s, inv_s;
+    run_scale(m, &scale_m, &inv_m);
+    run_scale(s, &scale_s, &inv_s);
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) {
+      m[c] *= inv_m;
+      s[c] *= inv_s;
+      s[c] = s[c] > 0.f ? fmaxf(s[c], 0x1p-9f) : s[c];  // (the smallest code)
+    }
+    if (i < t.n) {
+      store_codes(static_cast<uint8_t*>(t.m), i, t.n, encode8(m));
+      store_codes(static_cast<uint8_t*>(t.v), i, t.n, encode8(s));
+      if ((threadIdx.x & (kRunLanes - 1)) == 0) {
+        t.ms[run] = scale_m;
+        t.vs[run] = scale_s;
+      }
+    }
+  } else {
+    store8(static_cast<float*>(t.m), i, t.n, m);
+    store8(static_cast<float*>(t.v), i, t.n, v);
+  }
+}
+
+template <class P, class G, bool S8, bool MASTER>
+void launch(const AdamwArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((adamw_kernel<P, G, S8, MASTER>), dim3((unsigned)a.n_chunks), dim3(kAdamwThreads), 0, s, a);
+}
+
+template <class P, bool MASTER>
+void launch_p(const AdamwArgs& a, bool g_f32, bool state8, hipStream_t s) {
+  if (g_f32)
+    state8 ? launch<P, float, true, MASTER>(a, s) : launch<P, float, false, MASTER>(a, s);
+  else
+    state8 ? launch<P, uint16_t, true, MASTER>(a, s) : launch<P, uint16_t, false, MASTER>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwArgs& a, bool p_f32, bool g_f32, bool state8, bool master, hipStream_t s) {
+  if (a.n_chunks == 0) return hipSuccess;
+  if (p_f32) launch_p<float, false>(a, g_f32, state8, s);
+  else if (master) launch_p<uint16_t, true>(a, g_f32, state8, s);
+  else launch_p<uint16_t, false>(a, g_f32, state8, s);
+  return hipGetLastError();
+}
+
+}  // namespace salr

@@ -235,6 +235,74 @@ size_t moe_lowrank_part_bytes(int64_t T, int64_t K, int r_pad);
 hipError_t launch_moe_forward(const MoeArgs& a, int32_t m_cap, hipStream_t s);
 
 // ----------------------------------------------------------------------------
+// Around the grouped experts (include/salr.h, salr_moe_route and on).
+// ----------------------------------------------------------------------------
+// Logit rows [T][E] (bf16 or float by `f32`) to k experts and weights a row.
+hipError_t launch_moe_route(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renorm, int32_t* ids,
+                            float* weights, hipStream_t s);
+hipError_t launch_moe_route_backward(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renorm,
+                                     const int32_t* ids, const float* dweights, void* dlogits, hipStream_t s);
+
+struct MoeDispatchArgs {
+  const int32_t* ids;      // [T * k]
+  const uint16_t* X;       // [T][D], or null: sort only
+  uint16_t* Xs;            // [T * k][D]
+  int32_t* off;            // [E + 1]
+  int32_t* rows;           // [T * k]
+  int32_t* slots;          // [T * k] or null
+  uint32_t* hist;          // [chunks][E]
+  int64_t D;
+  int32_t n, k, E;         // n = T * k
+  int32_t chunk, chunks;   // slots per histogram row (of the several-launch form)
+};
+// Slots per histogram row for n slots: at most kMoeSortChunks rows.
+int32_t moe_sort_chunk(int64_t n);
+constexpr int kMoeSortChunks = 64;
+hipError_t launch_moe_dispatch(const MoeDispatchArgs& a, hipStream_t s);
+
+struct MoeCombineArgs {
+  const uint16_t* Ys;      // [R][D]
+  const int32_t* rows;     // [T][k]
+  const float* weights;    // [T][k] or null
+  const uint16_t* base;    // [T][D] or null
+  const uint16_t* dY;      // [T][D] (backward)
+  uint16_t* out;           // Y [T][D]; backward: dYs [R][D] or null
+  float* dweights;         // [T][k] or null (backward)
+  int64_t R, T, D;
+  int32_t k;
+};
+hipError_t launch_moe_combine(const MoeCombineArgs& a, hipStream_t s);
+hipError_t launch_moe_combine_backward(const MoeCombineArgs& a, hipStream_t s);
+
+// ----------------------------------------------------------------------------
+// AdamW over many tensors (include/salr.h).  The plan's table: `count` tensor
+// records, then one {tensor, chunk of the tensor} pair per kAdamwChunk
+// elements of each tensor.
+// ----------------------------------------------------------------------------
+constexpr int kAdamwChunk = 2048;  // elements per workgroup: a multiple of the 8-bit block
+struct AdamwTensor {
+  void* p;
+  const void* g;
+  void *m, *v;
+  float *ms, *vs, *master;
+  int64_t n;
+};
+struct AdamwChunk {
+  int32_t tensor, chunk;
+};
+struct AdamwArgs {
+  const AdamwTensor* tensors;
+  const AdamwChunk* chunks;
+  const float* dyn;        // {lr, grad_scale, 1 / (1 - b1^t), 1 / sqrt(1 - b2^t)} or null
+  float beta1, beta2, rest1, rest2;  // rest = 1 - beta
+  float eps, weight_decay;
+  // where dyn is null: 1 - lr weight_decay, lr / (1 - b1^t), and as in dyn
+  float decay, rate, grad_scale, inv_sqrt_bias2;
+  int64_t n_chunks;
+};
+hipError_t launch_adamw(const AdamwArgs& a, bool p_f32, bool g_f32, bool state8, bool master, hipStream_t s);
+
+// ----------------------------------------------------------------------------
 // Encode kernels.
 // ----------------------------------------------------------------------------
 struct PrunePackArgs {
