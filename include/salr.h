@@ -604,7 +604,8 @@ int salr_moe_combine_backward(const uint16_t* dY, const uint16_t* Ys, int64_t R,
 #define SALR_STATE_8BIT 1
 #define SALR_ADAMW_BLOCK 256
 
-/* One tensor of n elements: plain device pointers. */
+/* One tensor of n elements: plain device pointers (scales: 4-byte aligned, so
+ * that the runs of many tensors may lie in one array). */
 typedef struct salr_adamw_tensor {
   void* p;          /* parameters (p_type)                                  */
   const void* g;    /* gradients (g_type)                                   */

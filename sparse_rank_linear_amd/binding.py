@@ -763,41 +763,42 @@ MOE_MAX_TOPK = 32
 ADAMW_BLOCK = 256
 
 
-class _Place:
-    """The device and stream of one call."""
+def _elsewhere(dev, stream) -> bool:
+    """Whether a call on `dev` has to change the current device or stream
+    (or cannot run at all): the calls then run themselves inside _Place."""
+    import torch
 
-    __slots__ = ("dev", "stream", "_dev_ctx", "_stream_ctx")
+    return stream is not None or dev.index != torch.cuda.current_device() if dev.type == "cuda" else True
+
+
+class _Place:
+    """Makes a call's device, and its stream where one is given, current."""
 
     def __init__(self, dev, stream):
         import torch
 
         if dev.type != "cuda":
             raise ValueError("device tensors are needed")
-        self.dev = dev
-        self._dev_ctx = self._stream_ctx = None
-        if dev.index != torch.cuda.current_device():
-            self._dev_ctx = torch.cuda.device(dev)
-        if stream is not None:
-            if stream.device_index != dev.index:
-                raise ValueError("stream and tensors are on different devices")
-            self._stream_ctx = torch.cuda.stream(stream)
+        if stream is not None and stream.device_index != dev.index:
+            raise ValueError("stream and tensors are on different devices")
+        self._contexts = [torch.cuda.device(dev)] + ([torch.cuda.stream(stream)] if stream is not None else [])
 
     def __enter__(self):
-        import torch
-
-        if self._dev_ctx is not None:
-            self._dev_ctx.__enter__()
-        if self._stream_ctx is not None:
-            self._stream_ctx.__enter__()
-        self.stream = torch.cuda.current_stream(self.dev).cuda_stream
-        return self
+        for c in self._contexts:
+            c.__enter__()
 
     def __exit__(self, *exc):
-        if self._stream_ctx is not None:
-            self._stream_ctx.__exit__(*exc)
-        if self._dev_ctx is not None:
-            self._dev_ctx.__exit__(*exc)
+        for c in reversed(self._contexts):
+            c.__exit__(*exc)
         return False
+
+
+def _raw_stream(dev):
+    """The current stream of `dev` as an address.  (torch.cuda.current_stream
+    builds a stream object each time, 1.9 us of a 9 us call.)"""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _ptr(t, name, dtype, shape, dev):
@@ -834,15 +835,17 @@ def moe_route(logits, k: int, renorm: bool = True, ids=None, weights=None, strea
         raise ValueError("logits must be [T][E]")
     T, E = logits.shape
     dev, shape = logits.device, (T, k)
-    with _Place(dev, stream) as at:
-        if ids is None:
-            ids = torch.empty(shape, dtype=torch.int32, device=dev)
-        if weights is None:
-            weights = torch.empty(shape, dtype=torch.float32, device=dev)
-        _check(_lib().salr_moe_route(_ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"),
-                                     T, E, k, bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
-                                     _ptr(weights, "weights", torch.float32, shape, dev), at.stream),
-               "salr_moe_route")
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return moe_route(logits, k, renorm, ids, weights)
+    if ids is None:
+        ids = torch.empty(shape, dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    _check(_lib().salr_moe_route(_ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"),
+                                 T, E, k, bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
+                                 _ptr(weights, "weights", torch.float32, shape, dev), _raw_stream(dev)),
+           "salr_moe_route")
     return ids, weights
 
 
@@ -855,14 +858,16 @@ def moe_route_backward(logits, ids, dweights, renorm: bool = True, dlogits=None,
         raise ValueError("logits must be [T][E] and ids [T][k]")
     T, E = logits.shape
     dev, shape = logits.device, (T, ids.shape[1])
-    with _Place(dev, stream) as at:
-        if dlogits is None:
-            dlogits = torch.empty_like(logits)
-        _check(_lib().salr_moe_route_backward(
-            _ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"), T, E, shape[1],
-            bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
-            _ptr(dweights, "dweights", torch.float32, shape, dev),
-            _ptr(dlogits, "dlogits", logits.dtype, (T, E), dev), at.stream), "salr_moe_route_backward")
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return moe_route_backward(logits, ids, dweights, renorm, dlogits)
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _check(_lib().salr_moe_route_backward(
+        _ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"), T, E, shape[1],
+        bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
+        _ptr(dweights, "dweights", torch.float32, shape, dev),
+        _ptr(dlogits, "dlogits", logits.dtype, (T, E), dev), _raw_stream(dev)), "salr_moe_route_backward")
     return dlogits
 
 
@@ -888,33 +893,35 @@ def moe_dispatch(ids, E: int, X=None, Xs=None, offsets=None, rows=None, slots=No
         raise ValueError("ids must be [T][k]")
     T, k = ids.shape
     n, D, dev = T * k, 0, ids.device
-    with _Place(dev, stream) as at:
-        if offsets is None:
-            offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        if rows is None:
-            rows = torch.empty((T, k), dtype=torch.int32, device=dev)
-        if slots is None:
-            slots = torch.empty(n, dtype=torch.int32, device=dev)
-        x = xs = None
-        if X is not None:
-            if X.dim() != 2:
-                raise ValueError("X must be [T][D]")
-            D = X.shape[1]
-            if Xs is None:
-                Xs = torch.empty((n, D), dtype=torch.bfloat16, device=dev)
-            x = _ptr(X, "X", torch.bfloat16, (T, D), dev)
-            xs = _ptr(Xs, "Xs", torch.bfloat16, (n, D), dev)
-        elif Xs is not None:
-            raise ValueError("Xs needs X")
-        if ws is None:
-            ws = torch.empty(moe_dispatch_ws_bytes(T, k, E), dtype=torch.uint8, device=dev)
-        elif ws.device != dev:
-            raise ValueError(f"ws must be on {dev} (is on {ws.device})")
-        _check(_lib().salr_moe_dispatch(_ptr(ids, "ids", torch.int32, (T, k), dev), T, k, E, x, D,
-                                        _ptr(offsets, "offsets", torch.int32, (E + 1,), dev),
-                                        _ptr(rows, "rows", torch.int32, (T, k), dev),
-                                        _ptr(slots, "slots", torch.int32, (n,), dev), xs, ws.data_ptr(),
-                                        ws.numel() * ws.element_size(), at.stream), "salr_moe_dispatch")
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return moe_dispatch(ids, E, X, Xs, offsets, rows, slots, ws)
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    if rows is None:
+        rows = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty(n, dtype=torch.int32, device=dev)
+    x = xs = None
+    if X is not None:
+        if X.dim() != 2:
+            raise ValueError("X must be [T][D]")
+        D = X.shape[1]
+        if Xs is None:
+            Xs = torch.empty((n, D), dtype=torch.bfloat16, device=dev)
+        x = _ptr(X, "X", torch.bfloat16, (T, D), dev)
+        xs = _ptr(Xs, "Xs", torch.bfloat16, (n, D), dev)
+    elif Xs is not None:
+        raise ValueError("Xs needs X")
+    if ws is None:
+        ws = torch.empty(moe_dispatch_ws_bytes(T, k, E), dtype=torch.uint8, device=dev)
+    elif ws.device != dev:
+        raise ValueError(f"ws must be on {dev} (is on {ws.device})")
+    _check(_lib().salr_moe_dispatch(_ptr(ids, "ids", torch.int32, (T, k), dev), T, k, E, x, D,
+                                    _ptr(offsets, "offsets", torch.int32, (E + 1,), dev),
+                                    _ptr(rows, "rows", torch.int32, (T, k), dev),
+                                    _ptr(slots, "slots", torch.int32, (n,), dev), xs, ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), _raw_stream(dev)), "salr_moe_dispatch")
     return Xs, offsets, rows, slots
 
 
@@ -925,14 +932,16 @@ def _combine(Ys, rows, weights, base, Y, stream):
         raise ValueError("the rows' values must be [R][D] and rows [T][k]")
     (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
     bf16 = torch.bfloat16
-    with _Place(dev, stream) as at:
-        if Y is None:
-            Y = torch.empty((T, D), dtype=bf16, device=dev)
-        _check(_lib().salr_moe_combine(
-            _ptr(Ys, "the rows' values", bf16, (R, D), dev), R, _ptr(rows, "rows", torch.int32, (T, k), dev),
-            None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev),
-            None if base is None else _ptr(base, "base", bf16, (T, D), dev), T, k, D,
-            _ptr(Y, "the output", bf16, (T, D), dev), at.stream), "salr_moe_combine")
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return _combine(Ys, rows, weights, base, Y, None)
+    if Y is None:
+        Y = torch.empty((T, D), dtype=bf16, device=dev)
+    _check(_lib().salr_moe_combine(
+        _ptr(Ys, "the rows' values", bf16, (R, D), dev), R, _ptr(rows, "rows", torch.int32, (T, k), dev),
+        None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev),
+        None if base is None else _ptr(base, "base", bf16, (T, D), dev), T, k, D,
+        _ptr(Y, "the output", bf16, (T, D), dev), _raw_stream(dev)), "salr_moe_combine")
     return Y
 
 
@@ -960,17 +969,19 @@ def moe_combine_backward(dY, Ys, rows, weights=None, dYs=None, dweights=None, st
         raise ValueError("Ys must be [R][D] and rows [T][k]")
     (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
     bf16 = torch.bfloat16
-    with _Place(dev, stream) as at:
-        if dYs is None:
-            dYs = torch.zeros((R, D), dtype=bf16, device=dev)
-        if dweights is None:
-            dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
-        _check(_lib().salr_moe_combine_backward(
-            _ptr(dY, "dY", bf16, (T, D), dev), _ptr(Ys, "Ys", bf16, (R, D), dev), R,
-            _ptr(rows, "rows", torch.int32, (T, k), dev),
-            None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev), T, k, D,
-            _ptr(dYs, "dYs", bf16, (R, D), dev), _ptr(dweights, "dweights", torch.float32, (T, k), dev), at.stream),
-            "salr_moe_combine_backward")
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return moe_combine_backward(dY, Ys, rows, weights, dYs, dweights)
+    if dYs is None:
+        dYs = torch.zeros((R, D), dtype=bf16, device=dev)
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _check(_lib().salr_moe_combine_backward(
+        _ptr(dY, "dY", bf16, (T, D), dev), _ptr(Ys, "Ys", bf16, (R, D), dev), R,
+        _ptr(rows, "rows", torch.int32, (T, k), dev),
+        None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev), T, k, D,
+        _ptr(dYs, "dYs", bf16, (R, D), dev), _ptr(dweights, "dweights", torch.float32, (T, k), dev), _raw_stream(dev)),
+        "salr_moe_combine_backward")
     return dYs, dweights
 
 
@@ -1009,7 +1020,8 @@ def adamw_plan(params, grads, m, v, m_scale=None, v_scale=None, master=None, str
     """A plan for adamw_step over the tensors in `params` (all bf16 or all
     float) with their gradients (all bf16 or all float) and states (see
     adamw_states), element i of every list belonging together; all tensors
-    contiguous and 16-byte aligned, written ones disjoint.  Synchronous."""
+    contiguous and 16-byte aligned (scales: 4-byte), written ones disjoint.
+    Synchronous."""
     import torch
 
     lists = {"params": params, "grads": grads, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale,
@@ -1049,10 +1061,12 @@ def adamw_plan(params, grads, m, v, m_scale=None, v_scale=None, master=None, str
     sizes = (C.c_int64 * count)(*[r.n for r in recs])
     _check(_lib().salr_adamw_plan_bytes(sizes, count, C.byref(nbytes)), "salr_adamw_plan_bytes")
     p_type, g_type = _float_type(params[0], "params"), _float_type(lists["grads"][0], "grads")
-    with _Place(dev, stream) as at:
-        table = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
-        _check(_lib().salr_adamw_plan(recs, count, p_type, g_type, STATE_8BIT if bits8 else STATE_F32,
-                                      table.data_ptr(), nbytes.value, C.byref(desc), at.stream), "salr_adamw_plan")
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return adamw_plan(**lists)
+    table = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+    _check(_lib().salr_adamw_plan(recs, count, p_type, g_type, STATE_8BIT if bits8 else STATE_F32,
+                                  table.data_ptr(), nbytes.value, C.byref(desc), _raw_stream(dev)), "salr_adamw_plan")
     return AdamWPlan(desc, table, [t for ts in lists.values() for t in ts], dev)
 
 
@@ -1069,10 +1083,12 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     step, lr and grad_scale (for captured graphs)."""
     import torch
 
-    args = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale)
-    with _Place(plan.device, stream) as at:
-        d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (4,), plan.device)
-        _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, at.stream), "salr_adamw_step")
+    args, dev = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale), plan.device
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, dyn)
+    d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (4,), dev)
+    _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, _raw_stream(dev)), "salr_adamw_step")
 
 
 def probe_stream_read(src, sink, workgroups: int, stream=None):

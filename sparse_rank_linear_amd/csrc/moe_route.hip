@@ -7,13 +7,16 @@
 // exp(l - max) over all experts, or over the chosen ones (renorm).  Backward,
 // with p the same softmax and c = sum_i p_{e_i} dw_i:  dl_e = p_e (dw_e - c).
 //
-// One wave per row, PER logits a lane in registers (logit q * 64 + lane), so
-// a row is read once.  The k largest are taken one after the other: a
-// wave-wide maximum, then the lowest expert that holds it.
+// A group of LANES lanes per row (16 up to 256 experts: four rows a wave),
+// PER logits a lane in registers (logit q * LANES + lane), so a row is read
+// once.  The k largest are taken one after the other: a maximum over the
+// group, then the lowest expert that holds it; within 16 lanes both run on
+// DPP row rotations, without the LDS round trips of a shuffle.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 
+#include "salr.h"
 #include "salr_device.hpp"
 #include "salr_kernels.hpp"
 
@@ -28,104 +31,131 @@ __device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = f32_to_bf16(v); }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+// v combined over the row's lanes, in every one of them.
+template <int N>
+__device__ __forceinline__ int row_ror(int v) {  // lane i of 16 from lane (i - N) mod 16
+  return __builtin_amdgcn_update_dpp(v, v, 0x120 + N, 0xF, 0xF, false);
+}
+template <int LANES, class F>
+__device__ __forceinline__ int group_all(int v, F f) {
+  v = f(v, row_ror<8>(v));
+  v = f(v, row_ror<4>(v));
+  v = f(v, row_ror<2>(v));
+  v = f(v, row_ror<1>(v));
+  if constexpr (LANES == 64) {
+    v = f(v, __shfl_xor(v, 16, 64));
+    v = f(v, __shfl_xor(v, 32, 64));
+  }
   return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {  // (NaN left aside)
+  return __int_as_float(group_all<LANES>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+  }));
 }
-__device__ __forceinline__ int wave_min(int v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = min(v, __shfl_xor(v, d, 64));
-  return v;
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+  return __int_as_float(group_all<LANES>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  }));
+}
+template <int LANES>
+__device__ __forceinline__ int group_min(int v) {
+  return group_all<LANES>(v, [](int a, int b) { return min(a, b); });
 }
 
-template <class Tl, int PER>
+template <class Tl, int LANES, int PER>
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const Tl* logits, int64_t T, int32_t E, int32_t k,
                                                                   int32_t renorm, int32_t* ids, float* weights) {
-  const int lane = threadIdx.x & 63;
-  const int64_t waves = (int64_t)gridDim.x * (kRouteThreads / 64);
-  for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 64) + (threadIdx.x >> 6); t < T; t += waves) {
+  constexpr int SLOTS = SALR_MOE_MAX_TOPK > LANES ? SALR_MOE_MAX_TOPK / LANES : 1;  // choices kept per lane
+  const int lane = threadIdx.x % LANES;
+  const int64_t groups = (int64_t)gridDim.x * (kRouteThreads / LANES);
+  for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES; t < T; t += groups) {
     float l[PER];
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      const int e = q * 64 + lane;
+      const int e = q * LANES + lane;
       l[q] = e < E ? load_logit(logits + t * E + e) : kNegInf;
     }
-    float top = kNegInf;  // (fmaxf leaves NaN aside)
+    float top = kNegInf;
 #pragma unroll
     for (int q = 0; q < PER; ++q) top = fmaxf(top, l[q]);
-    top = wave_max(top);
+    top = group_max<LANES>(top);
     float total = 0.f;
     if (!renorm) {
 #pragma unroll
-      for (int q = 0; q < PER; ++q) total += q * 64 + lane < E ? expf(l[q] - top) : 0.f;
-      total = wave_sum(total);
+      for (int q = 0; q < PER; ++q) total += q * LANES + lane < E ? expf(l[q] - top) : 0.f;
+      total = group_sum<LANES>(total);
     }
-    // lane j keeps the j-th choice
-    float mine = 0.f;
-    int my_id = -1;
+    // lane j % LANES keeps the j-th choice
+    float val[SLOTS];
+    int id[SLOTS];
+#pragma unroll
+    for (int c = 0; c < SLOTS; ++c) {
+      val[c] = kNegInf;
+      id[c] = -1;
+    }
     float best = top;
     for (int j = 0; j < k; ++j) {
-      if (!(best > kNegInf)) break;
       int at = 1 << 30;
 #pragma unroll
-      for (int q = PER - 1; q >= 0; --q) at = l[q] == best ? q * 64 + lane : at;
-      at = wave_min(at);
-      const float w = expf(best - top);
-      if (renorm) total += w;
-      if (lane == j) {
-        mine = w;
-        my_id = at;
-      }
+      for (int q = PER - 1; q >= 0; --q) at = l[q] == best ? q * LANES + lane : at;
+      at = group_min<LANES>(at);
+      const bool keep = lane == j % LANES && best > kNegInf;
+#pragma unroll
+      for (int c = 0; c < SLOTS; ++c)
+        if (keep && j / LANES == c) {
+          val[c] = best;
+          id[c] = at;
+        }
       float next = kNegInf;
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
-        if (q * 64 + lane == at) l[q] = kNegInf;
+        l[q] = q * LANES + lane == at ? kNegInf : l[q];
         next = fmaxf(next, l[q]);
       }
-      best = wave_max(next);
+      best = group_max<LANES>(next);
     }
-    if (lane < k) {
-      ids[t * k + lane] = my_id;
-      weights[t * k + lane] = my_id >= 0 ? mine / total : 0.f;
+    float w[SLOTS], sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < SLOTS; ++c) {
+      w[c] = id[c] >= 0 ? expf(val[c] - top) : 0.f;
+      sum += w[c];
     }
+    if (renorm) total = group_sum<LANES>(sum);
+#pragma unroll
+    for (int c = 0; c < SLOTS; ++c)
+      if (c * LANES + lane < k) {
+        ids[t * k + c * LANES + lane] = id[c];
+        weights[t * k + c * LANES + lane] = id[c] >= 0 ? w[c] / total : 0.f;
+      }
   }
 }
 
-template <class Tl, int PER>
+template <class Tl, int LANES, int PER>
 __global__ __launch_bounds__(kRouteThreads) void moe_route_backward_kernel(const Tl* logits, int64_t T, int32_t E,
                                                                            int32_t k, int32_t renorm,
                                                                            const int32_t* ids, const float* dweights,
                                                                            Tl* dlogits) {
-  const int lane = threadIdx.x & 63;
-  const int64_t waves = (int64_t)gridDim.x * (kRouteThreads / 64);
-  for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 64) + (threadIdx.x >> 6); t < T; t += waves) {
+  const int lane = threadIdx.x % LANES;
+  const int64_t groups = (int64_t)gridDim.x * (kRouteThreads / LANES);
+  for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES; t < T; t += groups) {
     float l[PER], up[PER];  // logit, gradient that reaches its probability
     bool chosen[PER];
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      const int e = q * 64 + lane;
+      const int e = q * LANES + lane;
       l[q] = e < E ? load_logit(logits + t * E + e) : kNegInf;
       up[q] = 0.f;
       chosen[q] = false;
     }
-    int id = -1;
-    float dw = 0.f;
-    if (lane < k) {
-      id = ids[t * k + lane];
-      dw = dweights[t * k + lane];
-    }
-    for (int j = 0; j < k; ++j) {
-      const int e = __shfl(id, j, 64);
-      const float d = __shfl(dw, j, 64);
+    for (int j = 0; j < k; ++j) {  // (one address a group)
+      const int e = ids[t * k + j];
+      const float d = dweights[t * k + j];
 #pragma unroll
       for (int q = 0; q < PER; ++q)
-        if (e == q * 64 + lane && e < E) {
+        if (e == q * LANES + lane && e < E) {
           up[q] += d;
           chosen[q] = true;
         }
@@ -133,47 +163,50 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_backward_kernel(const
     float top = kNegInf;
 #pragma unroll
     for (int q = 0; q < PER; ++q) top = fmaxf(top, !renorm || chosen[q] ? l[q] : kNegInf);
-    top = wave_max(top);
+    top = group_max<LANES>(top);
     float total = 0.f, c = 0.f;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      const bool in = q * 64 + lane < E && (!renorm || chosen[q]);
+      const bool in = q * LANES + lane < E && (!renorm || chosen[q]);
       l[q] = in && top > kNegInf ? expf(l[q] - top) : 0.f;
       total += l[q];
       c += l[q] * up[q];
     }
-    total = wave_sum(total);
-    c = wave_sum(c);
+    total = group_sum<LANES>(total);
+    c = group_sum<LANES>(c);
     const float inv = total != 0.f ? 1.f / total : 0.f;
     c *= inv;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      const int e = q * 64 + lane;
+      const int e = q * LANES + lane;
       if (e < E) store_logit(dlogits + t * E + e, l[q] * inv * (up[q] - c));
     }
   }
 }
 
-// f(std::integral_constant<int, PER>) for the least PER with 64 PER >= E.
+// f(lanes, per) for the first form that holds E logits.
 template <int N>
 struct Int {
   static constexpr int value = N;
 };
 template <class F>
-void with_per(int32_t E, F f) {
-  if (E <= 64) f(Int<1>{});
-  else if (E <= 128) f(Int<2>{});
-  else if (E <= 256) f(Int<4>{});
-  else if (E <= 512) f(Int<8>{});
-  else if (E <= 1024) f(Int<16>{});
-  else if (E <= 2048) f(Int<32>{});
-  else f(Int<64>{});
+void with_form(int32_t E, F f) {
+  if (E <= 16) f(Int<16>{}, Int<1>{});
+  else if (E <= 32) f(Int<16>{}, Int<2>{});
+  else if (E <= 64) f(Int<16>{}, Int<4>{});
+  else if (E <= 128) f(Int<16>{}, Int<8>{});
+  else if (E <= 256) f(Int<16>{}, Int<16>{});
+  else if (E <= 512) f(Int<64>{}, Int<8>{});
+  else if (E <= 1024) f(Int<64>{}, Int<16>{});
+  else if (E <= 2048) f(Int<64>{}, Int<32>{});
+  else f(Int<64>{}, Int<64>{});
 }
 
-// Workgroups for T rows, a wave a row (more than kMaxBlocks: they loop).
+// Workgroups for T rows (more than kMaxBlocks: they loop).
 constexpr int64_t kMaxBlocks = int64_t(1) << 22;
-unsigned route_blocks(int64_t T) {
-  return (unsigned)std::min(kMaxBlocks, (T + kRouteThreads / 64 - 1) / (kRouteThreads / 64));
+dim3 route_grid(int64_t T, int lanes) {
+  const int64_t rows = kRouteThreads / lanes;
+  return dim3((unsigned)std::min(kMaxBlocks, (T + rows - 1) / rows));
 }
 
 }  // namespace
@@ -181,14 +214,14 @@ unsigned route_blocks(int64_t T) {
 hipError_t launch_moe_route(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renorm, int32_t* ids,
                             float* weights, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const dim3 grid(route_blocks(T));
-  with_per(E, [&](auto per) {
-    constexpr int PER = decltype(per)::value;
+  with_form(E, [&](auto lanes, auto per) {
+    constexpr int LANES = decltype(lanes)::value, PER = decltype(per)::value;
+    const dim3 grid = route_grid(T, LANES);
     if (f32)
-      hipLaunchKernelGGL((moe_route_kernel<float, PER>), grid, dim3(kRouteThreads), 0, s,
+      hipLaunchKernelGGL((moe_route_kernel<float, LANES, PER>), grid, dim3(kRouteThreads), 0, s,
                          static_cast<const float*>(logits), T, E, k, (int32_t)renorm, ids, weights);
     else
-      hipLaunchKernelGGL((moe_route_kernel<uint16_t, PER>), grid, dim3(kRouteThreads), 0, s,
+      hipLaunchKernelGGL((moe_route_kernel<uint16_t, LANES, PER>), grid, dim3(kRouteThreads), 0, s,
                          static_cast<const uint16_t*>(logits), T, E, k, (int32_t)renorm, ids, weights);
   });
   return hipGetLastError();
@@ -197,15 +230,15 @@ hipError_t launch_moe_route(const void* logits, bool f32, int64_t T, int32_t E, 
 hipError_t launch_moe_route_backward(const void* logits, bool f32, int64_t T, int32_t E, int32_t k, bool renorm,
                                      const int32_t* ids, const float* dweights, void* dlogits, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const dim3 grid(route_blocks(T));
-  with_per(E, [&](auto per) {
-    constexpr int PER = decltype(per)::value;
+  with_form(E, [&](auto lanes, auto per) {
+    constexpr int LANES = decltype(lanes)::value, PER = decltype(per)::value;
+    const dim3 grid = route_grid(T, LANES);
     if (f32)
-      hipLaunchKernelGGL((moe_route_backward_kernel<float, PER>), grid, dim3(kRouteThreads), 0, s,
+      hipLaunchKernelGGL((moe_route_backward_kernel<float, LANES, PER>), grid, dim3(kRouteThreads), 0, s,
                          static_cast<const float*>(logits), T, E, k, (int32_t)renorm, ids, dweights,
                          static_cast<float*>(dlogits));
     else
-      hipLaunchKernelGGL((moe_route_backward_kernel<uint16_t, PER>), grid, dim3(kRouteThreads), 0, s,
+      hipLaunchKernelGGL((moe_route_backward_kernel<uint16_t, LANES, PER>), grid, dim3(kRouteThreads), 0, s,
                          static_cast<const uint16_t*>(logits), T, E, k, (int32_t)renorm, ids, dweights,
                          static_cast<uint16_t*>(dlogits));
   });

@@ -24,6 +24,7 @@ constexpr int64_t kMaxChunks = (int64_t(1) << 24) - 1;  // workgroups of one lau
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline int status(hipError_t e) { return e == hipSuccess ? SALR_OK : SALR_ERR_HIP; }
 
 bool type_ok(int32_t t) { return t == SALR_TYPE_BF16 || t == SALR_TYPE_F32; }
@@ -193,7 +194,7 @@ int adamw_fill(const salr_adamw_tensor_t* t, int32_t count, int32_t p_type, int3
     rec[i] = salr::AdamwTensor{q.p, q.g, q.m, q.v, q.m_scale, q.v_scale, q.master, q.n};
     if (q.n == 0) continue;
     if (!all_given({q.p, q.g, q.m, q.v})) return SALR_ERR_INVALID_ARG;
-    if (state8 && !all_given({q.m_scale, q.v_scale})) return SALR_ERR_INVALID_ARG;
+    if (state8 && (!q.m_scale || !q.v_scale || !aligned4(q.m_scale) || !aligned4(q.v_scale))) return SALR_ERR_INVALID_ARG;
     if ((q.master != nullptr) != master || !aligned16(q.master)) return SALR_ERR_INVALID_ARG;
     const auto add = [](Range* to, size_t& n, const void* p, size_t bytes) {
       to[n++] = Range{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes};
@@ -291,7 +292,7 @@ int salr_adamw_step(const salr_adamw_plan_t* plan, const salr_adamw_step_args_t*
   if (!nonneg(args->eps) || !nonneg(args->weight_decay)) return SALR_ERR_INVALID_ARG;
   if (!(args->beta1 >= 0 && args->beta1 < 1) || !(args->beta2 >= 0 && args->beta2 < 1)) return SALR_ERR_INVALID_ARG;
   if (!dyn && (args->step < 1 || !nonneg(args->lr))) return SALR_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(dyn) & 3u) return SALR_ERR_INVALID_ARG;
+  if (!aligned4(dyn)) return SALR_ERR_INVALID_ARG;
   salr::AdamwArgs a{};
   a.tensors = static_cast<const salr::AdamwTensor*>(plan->table);
   a.chunks = reinterpret_cast<const salr::AdamwChunk*>(static_cast<const char*>(plan->table) +

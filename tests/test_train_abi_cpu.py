@@ -101,7 +101,8 @@ def test_adamw_plan_refusals():
     assert _plan([a], s=1) == -1                                        # 8-bit states without scales
     s8 = dict(m_scale=P + 0x40000, v_scale=P + 0x50000)
     assert _plan([_tensor(1, **s8)], s=1, nbytes=0) == -3
-    assert _plan([_tensor(1, m_scale=P + 0x40004, v_scale=P + 0x50000)], s=1) == -1
+    assert _plan([_tensor(1, m_scale=P + 0x40002, v_scale=P + 0x50000)], s=1) == -1
+    assert _plan([_tensor(1, m_scale=P + 0x40004, v_scale=P + 0x5000C)], s=1, nbytes=0) == -3
     # masters: all or none, bf16 parameters only
     m1, m2 = _tensor(1, master=P + 0x60000 + 0x100000), _tensor(2, master=P + 0x60000 + 0x200000)
     assert _plan([m1, m2], nbytes=0) == -3 and _plan([m1, b]) == -1 and _plan([b, m1]) == -1
