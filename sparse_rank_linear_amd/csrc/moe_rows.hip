@@ -2,12 +2,17 @@
 // salr_moe_dispatch, salr_moe_combine and its gradient).
 //
 // Slot s = t * k + j is token t's j-th choice.  The sort is a stable counting
-// sort:  rows[s] = #{s' : id_s' < id_s} + #{s' < s : id_s' = id_s},  counted
-// per chunk of slots (moe_count_kernel), then placed (moe_place_kernel: each
-// workgroup adds up the chunks before its own, so no scan launch sits
-// between).  The copies run token-major: a token's row is read once and
-// written to its k rows (or its k rows are read and one written), 16 bytes a
-// thread; they are bound by HBM.
+// sort:  rows[s] = #{s' : id_s' < id_s} + #{s' < s : id_s' = id_s}.
+//
+// moe_dispatch_kernel sorts and copies in one launch: every workgroup counts
+// the ids for itself (all of them, and those before its own few tokens),
+// places its slots and copies its tokens' rows.  Each workgroup reads all n
+// ids, so from a few thousand slots on moe_count_kernel counts them in chunks
+// first and the workgroups add up the chunks' counts; with many chunks of
+// many experts moe_place_kernel does that once per chunk and
+// moe_gather_kernel copies.  The copies run token-major: a token's row is read
+// once and written to its k rows (or its k rows are read and one written), 16
+// bytes a thread; they are bound by HBM.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -20,6 +25,7 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kCopyThreads = 256;
+constexpr int kDispatchThreads = 512;
 
 // ---- sort ----
 
@@ -37,7 +43,8 @@ __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(MoeDispatchArgs
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) a.hist[(size_t)blockIdx.x * a.E + e] = sm[e];
 }
 
-// Exclusive prefix sum of v over the workgroup's kSortThreads threads.
+// Exclusive prefix sum of v over the workgroup's THREADS threads.
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* part, uint32_t* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint32_t incl = v;
@@ -50,7 +57,7 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* part, uin
   __syncthreads();
   uint32_t before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kSortThreads / 64; ++w) {
+  for (int w = 0; w < THREADS / 64; ++w) {
     if (w < wave) before += part[w];
     all += part[w];
   }
@@ -95,7 +102,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeDispatchArgs
   for (int e0 = 0; e0 < a.E; e0 += kSortThreads) {
     const int e = e0 + tid;
     uint32_t total;
-    const uint32_t off = run + block_prefix(e < a.E ? next[e] : 0u, part, &total);
+    const uint32_t off = run + block_prefix<kSortThreads>(e < a.E ? next[e] : 0u, part, &total);
     if (e < a.E) {
       first[e] += off;
       next[e] = 0;
@@ -153,13 +160,20 @@ template <>
 struct Piece<1> {
   uint16_t w;
 };
-template <int VEC>
+// NT: data that is not read again soon, past the caches.
+template <int VEC, bool NT = false>
 __device__ __forceinline__ Piece<VEC> load_piece(const uint16_t* p) {
-  return *reinterpret_cast<const Piece<VEC>*>(p);
+  Piece<VEC> v;
+  const auto* q = reinterpret_cast<const decltype(v.w)*>(p);
+  if constexpr (NT) v.w = __builtin_nontemporal_load(q);
+  else v.w = *q;
+  return v;
 }
-template <int VEC>
+template <int VEC, bool NT = false>
 __device__ __forceinline__ void store_piece(uint16_t* p, Piece<VEC> v) {
-  *reinterpret_cast<Piece<VEC>*>(p) = v;
+  auto* q = reinterpret_cast<decltype(v.w)*>(p);
+  if constexpr (NT) __builtin_nontemporal_store(v.w, q);
+  else *q = v.w;
 }
 __device__ __forceinline__ void add_piece(float* acc, Piece<8> v, float w) {
 #pragma unroll
@@ -182,80 +196,216 @@ __device__ __forceinline__ Piece<VEC> round_piece(const float* f) {
   else return Piece<1>{f32_to_bf16(f[0])};
 }
 
+// Sort and copy in one launch, after moe_count_kernel where there are more
+// chunks than one: the workgroup's tokens are [G * blockIdx.x, + G), G * k <=
+// 64.  LDS: all[E] (slots of e), then first[E] (the row where the
+// workgroup's slots of e begin).
+template <int VEC>
+__global__ __launch_bounds__(kDispatchThreads) void moe_dispatch_kernel(MoeDispatchArgs a, int64_t T, int G, int bits,
+                                                                    int pieces) {
+  extern __shared__ uint32_t sm[];
+  __shared__ uint32_t part[kDispatchThreads / 64];
+  __shared__ int32_t row[64];
+  uint32_t* all = sm;
+  uint32_t* first = sm + a.E;
+  const int tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * G, t1 = min(t0 + G, T);
+  const int s0 = (int)(t0 * a.k), s1 = (int)(t1 * a.k);
+  for (int e = tid; e < 2 * a.E; e += kDispatchThreads) sm[e] = 0;
+  __syncthreads();
+  if (a.chunks == 1) {
+    for (int s = tid; s < a.n; s += kDispatchThreads) {
+      const uint32_t id = (uint32_t)a.ids[s];
+      if (id < (uint32_t)a.E) {
+        atomicAdd(&all[id], 1u);
+        if (s < s0) atomicAdd(&first[id], 1u);
+      }
+    }
+  } else {
+    const int chunk = s0 / a.chunk;
+    for (int c = tid; c < a.E * a.chunks; c += kDispatchThreads) {
+      const uint32_t h = a.hist[c];
+      const int e = c % a.E;
+      if (h) {
+        atomicAdd(&all[e], h);
+        if (c / a.E < chunk) atomicAdd(&first[e], h);
+      }
+    }
+    for (int s = chunk * a.chunk + tid; s < s0; s += kDispatchThreads) {
+      const uint32_t id = (uint32_t)a.ids[s];
+      if (id < (uint32_t)a.E) atomicAdd(&first[id], 1u);
+    }
+  }
+  __syncthreads();
+  uint32_t run = 0;
+  for (int e0 = 0; e0 < a.E; e0 += kDispatchThreads) {
+    const int e = e0 + tid;
+    uint32_t total;
+    const uint32_t off = run + block_prefix<kDispatchThreads>(e < a.E ? all[e] : 0u, part, &total);
+    if (e < a.E) {
+      first[e] += off;
+      if (blockIdx.x == 0) a.off[e] = (int32_t)off;
+    }
+    run += total;
+  }
+  if (blockIdx.x == 0 && tid == 0) a.off[a.E] = (int32_t)run;
+  __syncthreads();
+  if (tid < 64) {
+    const int s = s0 + tid;
+    const uint32_t id = s < s1 ? (uint32_t)a.ids[s] : 0xFFFFFFFFu;
+    const bool ok = id < (uint32_t)a.E;
+    const uint64_t m = same_id(ok ? id : 0u, bits) & __ballot(ok);
+    const int32_t r = ok ? (int32_t)(first[id] + (uint32_t)__popcll(m & ((1ull << tid) - 1ull))) : -1;
+    row[tid] = r;
+    if (s < s1) a.rows[s] = r;
+    if (ok && a.slots) a.slots[r] = s;
+  }
+  __syncthreads();
+  if (!a.X) return;
+  const int total = (int)(t1 - t0) * pieces;
+  for (int i = tid; i < total; i += kDispatchThreads) {
+    const int g = i / pieces;
+    const int64_t d = (int64_t)(i - g * pieces) * VEC;
+    const Piece<VEC> v = load_piece<VEC>(a.X + (t0 + g) * a.D + d);
+    for (int j = 0; j < a.k; ++j) {
+      const int32_t r = row[g * a.k + j];
+      if (r >= 0) store_piece<VEC, true>(a.Xs + (int64_t)r * a.D + d, v);
+    }
+  }
+}
+
+// i / n for n < 2^32 (in 32 bits wherever i allows it).
+__device__ __forceinline__ int64_t divide(int64_t i, int64_t n) {
+  return (uint64_t)i >> 32 ? i / n : (int64_t)((uint32_t)i / (uint32_t)n);
+}
+
 // Xs[rows[t][j]] = X[t]: one thread per (token, piece).
 template <int VEC>
 __global__ __launch_bounds__(kCopyThreads) void moe_gather_kernel(MoeDispatchArgs a, int64_t pieces, int64_t total) {
   for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kCopyThreads) {
-    const int64_t t = i / pieces, d = (i - t * pieces) * VEC;
+    const int64_t t = divide(i, pieces), d = (i - t * pieces) * VEC;
     const Piece<VEC> v = load_piece<VEC>(a.X + t * a.D + d);
     for (int j = 0; j < a.k; ++j) {
       const int32_t r = a.rows[t * a.k + j];
-      if (r >= 0) store_piece<VEC>(a.Xs + (int64_t)r * a.D + d, v);
+      if (r >= 0) store_piece<VEC, true>(a.Xs + (int64_t)r * a.D + d, v);
     }
   }
 }
 
-// Y[t] = base[t] + sum_j w[t][j] Ys[rows[t][j]]: one thread per (token, piece).
-template <int VEC>
-__global__ __launch_bounds__(kCopyThreads) void moe_combine_kernel(MoeCombineArgs a, int64_t pieces, int64_t total) {
-  for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kCopyThreads) {
-    const int64_t t = i / pieces, d = (i - t * pieces) * VEC;
+// Y[t] = base[t] + sum_j w[t][j] Ys[rows[t][j]], a piece a thread; KB rows are
+// requested before the first is used.  WAVE: a wave has `width` = 64
+// consecutive pieces of one token (row starts and weights become scalar
+// loads), the last of a token's `parts` waves maybe fewer; else thread i has
+// piece i of all (parts = 1, width = pieces).
+template <int VEC, int KB, bool NT, bool WAVE>
+__global__ __launch_bounds__(kCopyThreads) void moe_combine_kernel(MoeCombineArgs a, int parts, int width,
+                                                                   int64_t total) {
+  const int lane = threadIdx.x & 63;
+  const int per = WAVE ? kCopyThreads / 64 : kCopyThreads;  // items a workgroup: waves' shares, or pieces
+  const int mine = WAVE ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : (int)threadIdx.x;
+  for (int64_t i = (int64_t)blockIdx.x * per + mine; i < total; i += (int64_t)gridDim.x * per) {
+    const int64_t t = divide(i, WAVE ? parts : width);
+    const int64_t d = (WAVE ? (i - t * parts) * 64 + lane : i - t * width) * VEC;
+    if (WAVE && d >= a.D) continue;
     float acc[VEC];
 #pragma unroll
     for (int c = 0; c < VEC; ++c) acc[c] = 0.f;
-    if (a.base) add_piece(acc, load_piece<VEC>(a.base + t * a.D + d), 1.f);
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t r = a.rows[t * a.k + j];
-      if (r < 0 || r >= a.R) continue;
-      const float w = a.weights ? a.weights[t * a.k + j] : 1.f;
-      add_piece(acc, load_piece<VEC>(a.Ys + r * a.D + d), w);
+    Piece<VEC> b;
+    if (a.base) b = load_piece<VEC, NT>(a.base + t * a.D + d);
+    for (int j0 = 0; j0 < a.k; j0 += KB) {
+      Piece<VEC> v[KB];
+      float w[KB];
+      bool ok[KB];
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const int64_t r = j0 + j < a.k ? a.rows[t * a.k + j0 + j] : -1;
+        ok[j] = r >= 0 && r < a.R;
+        w[j] = ok[j] && a.weights ? a.weights[t * a.k + j0 + j] : 1.f;
+        if (ok[j]) v[j] = load_piece<VEC, NT>(a.Ys + r * a.D + d);
+      }
+      if (j0 == 0 && a.base) add_piece(acc, b, 1.f);
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+        if (ok[j]) add_piece(acc, v[j], w[j]);
     }
-    store_piece<VEC>(a.out + t * a.D + d, round_piece<VEC>(acc));
+    store_piece<VEC, true>(a.out + t * a.D + d, round_piece<VEC>(acc));
   }
 }
 
-// A workgroup per token: each slot's row is read for its dot product and
-// written (dYs) in turn.
-template <int VEC>
-__global__ __launch_bounds__(kCopyThreads) void moe_combine_backward_kernel(MoeCombineArgs a, int64_t pieces) {
-  __shared__ float part[kCopyThreads / 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t r = a.rows[t * a.k + j];
-      const bool ok = r >= 0 && r < a.R;
-      const float w = a.weights ? a.weights[t * a.k + j] : 1.f;
-      float dot = 0.f;
-      if (ok) {
-        for (int64_t p = threadIdx.x; p < pieces; p += kCopyThreads) {
-          float g[VEC], o[VEC];
+__device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
-          for (int c = 0; c < VEC; ++c) g[c] = o[c] = 0.f;
-          add_piece(g, load_piece<VEC>(a.dY + t * a.D + p * VEC), 1.f);
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// dYs and dweights of one token by THREADS threads (a wave, or the workgroup
+// for long rows): a piece of dY is loaded once for KB slots, whose
+// rows' pieces are requested together.
+template <int VEC, int THREADS, int KB, bool NT>
+__global__ __launch_bounds__(kCopyThreads) void moe_combine_backward_kernel(MoeCombineArgs a, int pieces) {
+  constexpr int kTokens = kCopyThreads / THREADS;
+  __shared__ float part[kCopyThreads / 64][KB];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tid = threadIdx.x % THREADS;
+  for (int64_t t = (int64_t)blockIdx.x * kTokens + (kTokens > 1 ? wave : 0); t < a.T; t += (int64_t)gridDim.x * kTokens) {
+    for (int j0 = 0; j0 < a.k; j0 += KB) {
+      int64_t r[KB];
+      float w[KB], dot[KB];
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        r[j] = j0 + j < a.k ? a.rows[t * a.k + j0 + j] : -1;
+        if (r[j] >= a.R) r[j] = -1;
+        w[j] = r[j] >= 0 && a.weights ? a.weights[t * a.k + j0 + j] : 1.f;
+        dot[j] = 0.f;
+      }
+      for (int p = tid; p < pieces; p += THREADS) {
+        float g[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) g[c] = 0.f;
+        const Piece<VEC> gp = load_piece<VEC>(a.dY + t * a.D + (int64_t)p * VEC);
+        Piece<VEC> y[KB];
+        if (a.dweights) {
+#pragma unroll
+          for (int j = 0; j < KB; ++j)
+            if (r[j] >= 0) y[j] = load_piece<VEC, NT>(a.Ys + r[j] * a.D + (int64_t)p * VEC);
+        }
+        add_piece(g, gp, 1.f);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (r[j] < 0) continue;
           if (a.dweights) {
-            float y[VEC];
+            float f[VEC];
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) y[c] = 0.f;
-            add_piece(y, load_piece<VEC>(a.Ys + r * a.D + p * VEC), 1.f);
+            for (int c = 0; c < VEC; ++c) f[c] = 0.f;
+            add_piece(f, y[j], 1.f);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) dot += g[c] * y[c];
+            for (int c = 0; c < VEC; ++c) dot[j] += g[c] * f[c];
           }
           if (a.out) {
+            float o[VEC];
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) o[c] = w * g[c];
-            store_piece<VEC>(a.out + r * a.D + p * VEC, round_piece<VEC>(o));
+            for (int c = 0; c < VEC; ++c) o[c] = w[j] * g[c];
+            store_piece<VEC, true>(a.out + r[j] * a.D + (int64_t)p * VEC, round_piece<VEC>(o));
           }
         }
       }
-      if (a.dweights) {
+      if (!a.dweights) continue;
 #pragma unroll
-        for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d, 64);
-        if (lane == 0) part[wave] = dot;
+      for (int j = 0; j < KB; ++j) dot[j] = wave_sum(dot[j]);
+      if constexpr (THREADS == 64) {
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+          if (lane == j && j0 + j < a.k) a.dweights[t * a.k + j0 + j] = dot[j];
+      } else {
+        if (lane == 0) {
+#pragma unroll
+          for (int j = 0; j < KB; ++j) part[wave][j] = dot[j];
+        }
         __syncthreads();
-        if (threadIdx.x == 0) {
+        if (tid < KB && j0 + tid < a.k) {
           float sum = 0.f;
-          for (int q = 0; q < kCopyThreads / 64; ++q) sum += part[q];
-          a.dweights[t * a.k + j] = ok ? sum : 0.f;
+          for (int q = 0; q < THREADS / 64; ++q) sum += part[q][tid];
+          a.dweights[t * a.k + j0 + tid] = sum;
         }
         __syncthreads();
       }
@@ -274,48 +424,119 @@ int32_t moe_sort_chunk(int64_t n) {
   return (int32_t)std::max<int64_t>(1024, (c + 1023) / 1024 * 1024);
 }
 
-hipError_t launch_moe_dispatch(const MoeDispatchArgs& a, hipStream_t s) {
+// Which form of the dispatch, and how many tokens a workgroup takes in the
+// first two (measured in us on random experts, sort and copy):
+//  - one launch up to 4096 slots: every workgroup reads all of them (680
+//    tokens, 6 of 64, 2048 columns: 8.2; counted first: 9.4);
+//  - counted first while the chunks' counts are few enough for every workgroup to
+//    add up (4099 tokens, 6 of 64, 2048 columns: 25.0; placed in a launch
+//    of their own: 31.3 with its launch);
+//  - else counted, placed and copied in a launch each.
+// A workgroup's share of the sort does not shrink with its tokens, so there
+// are about kDispatchGroups workgroups (two a CU), not more (1000 tokens, 2
+// of 8: 7.5; with a workgroup a token: 9.6).
+constexpr int64_t kOneLaunchSlots = 4096;
+constexpr int kFusedExperts = 1024;        // (their counters: 8 KB of LDS)
+constexpr int64_t kFusedTable = 4096;      // counts
+constexpr int64_t kFusedSlots = 1 << 20;   // (a chunk is then 2^14 slots, read by each of its workgroups)
+constexpr int64_t kDispatchGroups = 512;
+
+hipError_t launch_moe_dispatch(const MoeDispatchArgs& args, hipStream_t s) {
+  MoeDispatchArgs a = args;
   int bits = 0;
   while ((1 << bits) < a.E) ++bits;
+  const int64_t T = a.n / a.k;
+  const int vec = a.D % 8 == 0 ? 8 : 1;
+  const int64_t p = a.X ? a.D / vec : 0;
+  if (a.n <= kOneLaunchSlots && a.E <= kFusedExperts) a.chunks = 1;
+  else
+    hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)a.chunks), dim3(kSortThreads), (size_t)a.E * 4, s, a);
+  if (a.n <= kFusedSlots && a.E <= kFusedExperts && (int64_t)a.chunks * a.E <= kFusedTable) {
+    const int G = (int)std::min<int64_t>(64 / a.k, std::max<int64_t>(1, (T + kDispatchGroups - 1) / kDispatchGroups));
+    const dim3 grid((unsigned)std::max<int64_t>(1, (T + G - 1) / G));
+    const size_t lds = (size_t)a.E * 8;
+    if (vec == 8)
+      hipLaunchKernelGGL(moe_dispatch_kernel<8>, grid, dim3(kDispatchThreads), lds, s, a, T, G, bits, (int)p);
+    else
+      hipLaunchKernelGGL(moe_dispatch_kernel<1>, grid, dim3(kDispatchThreads), lds, s, a, T, G, bits, (int)p);
+    return hipGetLastError();
+  }
   // (each wave's counters: 4 waves keep E = 4096 within 80 KB of LDS)
   const int waves = a.E <= 1024 ? 16 : 4;
-  const int chunks = std::max(a.chunks, 1);  // (no slots: workgroup 0 still writes the offsets)
-  hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)chunks), dim3(kSortThreads), (size_t)a.E * 4, s, a);
-  hipLaunchKernelGGL(moe_place_kernel, dim3((unsigned)chunks), dim3(kSortThreads), (size_t)a.E * (waves + 1) * 4, s,
+  hipLaunchKernelGGL(moe_place_kernel, dim3((unsigned)a.chunks), dim3(kSortThreads), (size_t)a.E * (waves + 1) * 4, s,
                      a, waves, bits);
   if (a.X && a.n > 0) {
-    const int64_t T = a.n / a.k;
-    if (a.D % 8 == 0) {
-      const int64_t p = a.D / 8;
-      hipLaunchKernelGGL(moe_gather_kernel<8>, dim3(blocks_for(T * p, kCopyThreads)), dim3(kCopyThreads), 0, s, a, p,
-                         T * p);
-    } else {
-      hipLaunchKernelGGL(moe_gather_kernel<1>, dim3(blocks_for(T * a.D, kCopyThreads)), dim3(kCopyThreads), 0, s, a,
-                         a.D, T * a.D);
-    }
+    const dim3 grid(blocks_for(T * p, kCopyThreads));
+    if (vec == 8)
+      hipLaunchKernelGGL(moe_gather_kernel<8>, grid, dim3(kCopyThreads), 0, s, a, p, T * p);
+    else
+      hipLaunchKernelGGL(moe_gather_kernel<1>, grid, dim3(kCopyThreads), 0, s, a, p, T * p);
   }
   return hipGetLastError();
 }
 
+// f with the row batch, and with or without caching, as template arguments.
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+template <class F>
+void with_form(int k, bool nt, F f) {
+  const auto go = [&](auto kb) { nt ? f(kb, Int<1>{}) : f(kb, Int<0>{}); };
+  if (k <= 2) go(Int<2>{});
+  else if (k <= 4) go(Int<4>{});
+  else go(Int<8>{});
+}
+
+// A wave per token up to this many pieces of a row, a workgroup from there on
+// (8192 tokens, 2 of 4096 columns: 58.5 us, a wave each 77; 20000 tokens, 8
+// of 256 columns: 80.7 us, a wave each 40.1; equal at 1024 columns).
+constexpr int kWavePieces = 96;
+
+// From here on the gathered rows do not stay in the caches between the
+// kernel that wrote them and this one, and reading them past the caches is
+// faster (combine of 8192 tokens, 2 of 4096 columns, 134 MB: 34.9 against 37.4
+// us); below, they do and it is slower (500 tokens, 8 of 4096 columns, 33
+// MB: 10.4 against 8.3 us).
+constexpr int64_t kStreamRowBytes = int64_t(64) << 20;
+
 hipError_t launch_moe_combine(const MoeCombineArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  if (a.D % 8 == 0) {
-    const int64_t p = a.D / 8;
-    hipLaunchKernelGGL(moe_combine_kernel<8>, dim3(blocks_for(a.T * p, kCopyThreads)), dim3(kCopyThreads), 0, s, a, p,
-                       a.T * p);
-  } else {
-    hipLaunchKernelGGL(moe_combine_kernel<1>, dim3(blocks_for(a.T * a.D, kCopyThreads)), dim3(kCopyThreads), 0, s, a,
-                       a.D, a.T * a.D);
-  }
+  const bool vec = a.D % 8 == 0;
+  const int64_t p = vec ? a.D / 8 : a.D, parts = (p + 63) / 64;
+  const dim3 threads(kCopyThreads);
+  with_form(a.k, a.T * a.k * a.D * 2 >= kStreamRowBytes, [&](auto kb, auto nt) {
+    constexpr int KB = decltype(kb)::value;
+    constexpr bool NT = decltype(nt)::value;
+    if (!vec) {
+      hipLaunchKernelGGL((moe_combine_kernel<1, KB, NT, false>), dim3(blocks_for(a.T * p, kCopyThreads)), threads, 0, s,
+                         a, 1, (int)p, a.T * p);
+    } else if (4 * p >= 3 * 64 * parts) {  // (waves at least three quarters full)
+      hipLaunchKernelGGL((moe_combine_kernel<8, KB, NT, true>), dim3(blocks_for(a.T * parts, kCopyThreads / 64)),
+                         threads, 0, s, a, (int)parts, 64, a.T * parts);
+    } else {
+      hipLaunchKernelGGL((moe_combine_kernel<8, KB, NT, false>), dim3(blocks_for(a.T * p, kCopyThreads)), threads, 0, s,
+                         a, 1, (int)p, a.T * p);
+    }
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_backward(const MoeCombineArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  if (a.D % 8 == 0)
-    hipLaunchKernelGGL(moe_combine_backward_kernel<8>, dim3(blocks_for(a.T, 1)), dim3(kCopyThreads), 0, s, a, a.D / 8);
-  else
-    hipLaunchKernelGGL(moe_combine_backward_kernel<1>, dim3(blocks_for(a.T, 1)), dim3(kCopyThreads), 0, s, a, a.D);
+  const bool vec = a.D % 8 == 0;
+  const int p = (int)(vec ? a.D / 8 : a.D);
+  const dim3 threads(kCopyThreads);
+  with_form(a.k, a.T * a.k * a.D * 2 >= kStreamRowBytes, [&](auto kb, auto nt) {
+    constexpr int KB = decltype(kb)::value;
+    constexpr bool NT = decltype(nt)::value;
+    if (!vec)
+      hipLaunchKernelGGL((moe_combine_backward_kernel<1, 256, KB, NT>), dim3(blocks_for(a.T, 1)), threads, 0, s, a, p);
+    else if (p > kWavePieces)
+      hipLaunchKernelGGL((moe_combine_backward_kernel<8, 256, KB, NT>), dim3(blocks_for(a.T, 1)), threads, 0, s, a, p);
+    else
+      hipLaunchKernelGGL((moe_combine_backward_kernel<8, 64, KB, NT>), dim3(blocks_for(a.T, 4)), threads, 0, s, a, p);
+  });
   return hipGetLastError();
 }
 
