@@ -77,6 +77,24 @@ __device__ __forceinline__ uint64_t same_id(uint32_t id, int bits) {
   return m;
 }
 
+// Adds the chunks' counts: all[e] over every chunk, first[e] over those
+// before `chunk`.  Threads share an expert's chunks as far as they go round.
+template <int THREADS>
+__device__ __forceinline__ void add_chunks(const MoeDispatchArgs& a, int chunk, uint32_t* all, uint32_t* first) {
+  const int groups = max(1, THREADS / a.E), g = (int)threadIdx.x / a.E;
+  for (int e = (int)threadIdx.x - g * a.E; e < a.E && g < groups; e += THREADS) {
+    uint32_t sum = 0, before = 0;
+#pragma unroll 4
+    for (int c = g; c < a.chunks; c += groups) {
+      const uint32_t h = a.hist[(size_t)c * a.E + e];
+      sum += h;
+      before += c < chunk ? h : 0u;
+    }
+    if (sum) atomicAdd(&all[e], sum);
+    if (before) atomicAdd(&first[e], before);
+  }
+}
+
 // rows and slots of one chunk of slots; workgroup 0 writes the offsets.
 // LDS: first[E] (the row where the chunk's slots of e begin), then
 // next[waves][E]: each wave's running row of e.
@@ -89,14 +107,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeDispatchArgs
   for (int e = tid; e < a.E * (waves + 1); e += kSortThreads) sm[e] = 0;
   __syncthreads();
   // next[0][e]: all slots of e; first[e]: those of the chunks before
-  for (int c = tid; c < a.E * a.chunks; c += kSortThreads) {
-    const uint32_t h = a.hist[c];
-    const int e = c % a.E;
-    if (h) {
-      atomicAdd(&next[e], h);
-      if (c / a.E < (int)blockIdx.x) atomicAdd(&first[e], h);
-    }
-  }
+  add_chunks<kSortThreads>(a, blockIdx.x, next, first);
   __syncthreads();
   uint32_t run = 0;
   for (int e0 = 0; e0 < a.E; e0 += kSortThreads) {
@@ -223,14 +234,7 @@ __global__ __launch_bounds__(kDispatchThreads) void moe_dispatch_kernel(MoeDispa
     }
   } else {
     const int chunk = s0 / a.chunk;
-    for (int c = tid; c < a.E * a.chunks; c += kDispatchThreads) {
-      const uint32_t h = a.hist[c];
-      const int e = c % a.E;
-      if (h) {
-        atomicAdd(&all[e], h);
-        if (c / a.E < chunk) atomicAdd(&first[e], h);
-      }
-    }
+    add_chunks<kDispatchThreads>(a, chunk, all, first);
     for (int s = chunk * a.chunk + tid; s < s0; s += kDispatchThreads) {
       const uint32_t id = (uint32_t)a.ids[s];
       if (id < (uint32_t)a.E) atomicAdd(&first[id], 1u);
