@@ -25,11 +25,12 @@ static_assert(kAdamwThreads * kPer == kAdamwChunk, "one chunk per workgroup");
 constexpr int kRunLanes = 256 / kPer;
 constexpr float kTiny = 0x1p-100f;
 
-// 8 elements from i on, those at or past n read as 0 and are not written.
-// Pointers are 16-byte aligned and i is a multiple of 8, so whole groups move
-// as 16-byte vectors.
+// 8 elements from i on; unless WHOLE those at or past n read as 0 and are not
+// written.  Pointers are 16-byte aligned and i is a multiple of 8, so whole
+// groups move as 16-byte vectors.
+template <bool WHOLE>
 __device__ __forceinline__ void load8(const float* p, int64_t i, int64_t n, float* x) {
-  if (i + kPer <= n) {
+  if (WHOLE || i + kPer <= n) {
     const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p + i), b = *reinterpret_cast<const f32x4_t*>(p + i + 4);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -41,8 +42,9 @@ __device__ __forceinline__ void load8(const float* p, int64_t i, int64_t n, floa
     for (int c = 0; c < kPer; ++c) x[c] = i + c < n ? p[i + c] : 0.f;
   }
 }
+template <bool WHOLE>
 __device__ __forceinline__ void load8(const uint16_t* p, int64_t i, int64_t n, float* x) {
-  if (i + kPer <= n) {
+  if (WHOLE || i + kPer <= n) {
     const u32x4_t a = load16(p + i);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -54,8 +56,9 @@ __device__ __forceinline__ void load8(const uint16_t* p, int64_t i, int64_t n, f
     for (int c = 0; c < kPer; ++c) x[c] = i + c < n ? bf16_to_f32(p[i + c]) : 0.f;
   }
 }
+template <bool WHOLE>
 __device__ __forceinline__ void store8(float* p, int64_t i, int64_t n, const float* x) {
-  if (i + kPer <= n) {
+  if (WHOLE || i + kPer <= n) {
     *reinterpret_cast<f32x4_t*>(p + i) = f32x4_t{x[0], x[1], x[2], x[3]};
     *reinterpret_cast<f32x4_t*>(p + i + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
   } else {
@@ -64,8 +67,9 @@ __device__ __forceinline__ void store8(float* p, int64_t i, int64_t n, const flo
       if (i + c < n) p[i + c] = x[c];
   }
 }
+template <bool WHOLE>
 __device__ __forceinline__ void store8(uint16_t* p, int64_t i, int64_t n, const float* x) {
-  if (i + kPer <= n) {
+  if (WHOLE || i + kPer <= n) {
     u32x4_t w;
 #pragma unroll
     for (int c = 0; c < 4; ++c) w[c] = (uint32_t)f32_to_bf16(x[2 * c]) | ((uint32_t)f32_to_bf16(x[2 * c + 1]) << 16);
@@ -78,16 +82,18 @@ __device__ __forceinline__ void store8(uint16_t* p, int64_t i, int64_t n, const 
 }
 
 // 8 codes as two words (the codes past n as 0).
+template <bool WHOLE>
 __device__ __forceinline__ u32x2_t load_codes(const uint8_t* p, int64_t i, int64_t n) {
-  if (i + kPer <= n) return *reinterpret_cast<const u32x2_t*>(p + i);
+  if (WHOLE || i + kPer <= n) return *reinterpret_cast<const u32x2_t*>(p + i);
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int c = 0; c < kPer; ++c)
     if (i + c < n) w[c / 4] |= (uint32_t)p[i + c] << (8 * (c % 4));
   return u32x2_t{w[0], w[1]};
 }
+template <bool WHOLE>
 __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, u32x2_t w) {
-  if (i + kPer <= n) {
+  if (WHOLE || i + kPer <= n) {
     *reinterpret_cast<u32x2_t*>(p + i) = w;
   } else {
 #pragma unroll
@@ -119,23 +125,43 @@ __device__ __forceinline__ u32x2_t encode8(const float* x) {
 
 // The largest |x| of a run (32 lanes; NaN left aside), the run's scale and
 // its inverse (0 and 0 for a run of zeros).
+template <int N>
+__device__ __forceinline__ float row_max(float v) {  // with the lane N before in its row of 16, cyclically
+  const int i = __float_as_int(v);
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(i, i, 0x120 + N, 0xF, 0xF, false)));
+}
 __device__ __forceinline__ void run_scale(const float* x, float* scale, float* inv) {
   float top = 0.f;
 #pragma unroll
   for (int c = 0; c < kPer; ++c) top = fmaxf(top, fabsf(x[c]));
-#pragma unroll
-  for (int d = kRunLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kRunLanes));
+  top = row_max<1>(row_max<2>(row_max<4>(row_max<8>(top))));
+  top = fmaxf(top, __shfl_xor(top, 16, kRunLanes));
   const bool live = top >= kTiny;
   *scale = live ? top / 448.f : 0.f;
   *inv = live ? 448.f / top : 0.f;
 }
 
-template <class P, class G, bool S8, bool MASTER>
-__global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwArgs a) {
+// Square roots to 1 ulp (the instruction alone takes no subnormal: values
+// below 2^-96, zeros among them, go scaled).
+__device__ __forceinline__ void roots(const float* v, float* s) {
+  float low = v[0];
+#pragma unroll
+  for (int c = 1; c < kPer; ++c) low = fminf(low, v[c]);
+  if (low < 0x1p-96f) {
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) {
+      const bool tiny = v[c] < 0x1p-96f;
+      s[c] = __builtin_amdgcn_sqrtf(tiny ? v[c] * 0x1p32f : v[c]) * (tiny ? 0x1p-16f : 1.f);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) s[c] = __builtin_amdgcn_sqrtf(v[c]);
+  }
+}
+
+template <class P, class G, bool S8, bool MASTER, bool WHOLE>
+__device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwTensor& t, int64_t i) {
 #pragma clang fp contract(off)
-  const AdamwChunk ch = a.chunks[blockIdx.x];
-  const AdamwTensor t = a.tensors[ch.tensor];
-  const int64_t i = (int64_t)ch.chunk * kAdamwChunk + threadIdx.x * kPer;
   float decay = a.decay, rate = a.rate, gs = a.grad_scale, isb2 = a.inv_sqrt_bias2;
   if (a.dyn) {
     const float lr = a.dyn[0];
@@ -145,32 +171,34 @@ __global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwArgs a) {
     isb2 = a.dyn[3];
   }
   float g[kPer], m[kPer], v[kPer], p[kPer], s[kPer];
-  load8(static_cast<const G*>(t.g), i, t.n, g);
+  load8<WHOLE>(static_cast<const G*>(t.g), i, t.n, g);
   const int64_t run = i / 256;
   if constexpr (S8) {
-    const bool in = i < t.n;
-    const u32x2_t mc = load_codes(static_cast<const uint8_t*>(t.m), i, t.n);
-    const u32x2_t vc = load_codes(static_cast<const uint8_t*>(t.v), i, t.n);
+    const bool in = WHOLE || i < t.n;
+    const u32x2_t mc = load_codes<WHOLE>(static_cast<const uint8_t*>(t.m), i, t.n);
+    const u32x2_t vc = load_codes<WHOLE>(static_cast<const uint8_t*>(t.v), i, t.n);
     decode8(mc, in ? t.ms[run] : 0.f, m);
     decode8(vc, in ? t.vs[run] : 0.f, s);
 #pragma unroll
     for (int c = 0; c < kPer; ++c) v[c] = s[c] * s[c];
   } else {
-    load8(static_cast<const float*>(t.m), i, t.n, m);
-    load8(static_cast<const float*>(t.v), i, t.n, v);
+    load8<WHOLE>(static_cast<const float*>(t.m), i, t.n, m);
+    load8<WHOLE>(static_cast<const float*>(t.v), i, t.n, v);
   }
-  if constexpr (MASTER) load8(t.master, i, t.n, p);
-  else load8(static_cast<const P*>(t.p), i, t.n, p);
+  if constexpr (MASTER) load8<WHOLE>(t.master, i, t.n, p);
+  else load8<WHOLE>(static_cast<const P*>(t.p), i, t.n, p);
 #pragma unroll
   for (int c = 0; c < kPer; ++c) {
     g[c] *= gs;
     m[c] = m[c] * a.beta1 + g[c] * a.rest1;
     v[c] = v[c] * a.beta2 + (g[c] * g[c]) * a.rest2;
-    s[c] = sqrtf(v[c]);
-    p[c] = p[c] * decay - (m[c] / (s[c] * isb2 + a.eps)) * rate;
   }
-  if constexpr (MASTER) store8(t.master, i, t.n, p);
-  store8(static_cast<P*>(t.p), i, t.n, p);
+  roots(v, s);
+#pragma unroll
+  for (int c = 0; c < kPer; ++c)  // (the reciprocal to 1 ulp: the quotient's error stays far below m's)
+    p[c] = p[c] * decay - (m[c] * __builtin_amdgcn_rcpf(s[c] * isb2 + a.eps)) * rate;
+  if constexpr (MASTER) store8<WHOLE>(t.master, i, t.n, p);
+  store8<WHOLE>(static_cast<P*>(t.p), i, t.n, p);
   if constexpr (S8) {
     float scale_m, inv_m, scale_s, inv_s;
     run_scale(m, &scale_m, &inv_m);
@@ -181,18 +209,29 @@ __global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwArgs a) {
       s[c] *= inv_s;
       s[c] = s[c] > 0.f ? fmaxf(s[c], 0x1p-9f) : s[c];  // (the smallest code)
     }
-    if (i < t.n) {
-      store_codes(static_cast<uint8_t*>(t.m), i, t.n, encode8(m));
-      store_codes(static_cast<uint8_t*>(t.v), i, t.n, encode8(s));
+    if (WHOLE || i < t.n) {
+      store_codes<WHOLE>(static_cast<uint8_t*>(t.m), i, t.n, encode8(m));
+      store_codes<WHOLE>(static_cast<uint8_t*>(t.v), i, t.n, encode8(s));
       if ((threadIdx.x & (kRunLanes - 1)) == 0) {
         t.ms[run] = scale_m;
         t.vs[run] = scale_s;
       }
     }
   } else {
-    store8(static_cast<float*>(t.m), i, t.n, m);
-    store8(static_cast<float*>(t.v), i, t.n, v);
+    store8<WHOLE>(static_cast<float*>(t.m), i, t.n, m);
+    store8<WHOLE>(static_cast<float*>(t.v), i, t.n, v);
   }
+}
+
+// (bounds only in a tensor's last chunk: a branch around each load would make
+// the loads wait for one another)
+template <class P, class G, bool S8, bool MASTER>
+__global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwArgs a) {
+  const AdamwChunk ch = a.chunks[blockIdx.x];
+  const AdamwTensor t = a.tensors[ch.tensor];
+  const int64_t base = (int64_t)ch.chunk * kAdamwChunk, i = base + threadIdx.x * kPer;
+  if (base + kAdamwChunk <= t.n) adamw_chunk<P, G, S8, MASTER, true>(a, t, i);
+  else adamw_chunk<P, G, S8, MASTER, false>(a, t, i);
 }
 
 template <class P, class G, bool S8, bool MASTER>
