@@ -32,8 +32,9 @@ __device__ __forceinline__ void stream_store(V* p, V v) {
   __builtin_nontemporal_store(v, p);
 }
 
-// 8 elements from i on; unless WHOLE those at or past n read as 0 and are not
-// written.  Pointers are 16-byte aligned and i is a multiple of 8, so whole
+// 8 elements from i on; unless WHOLE those at or past n read as 0 (from the
+// last one's address: no branch keeps the loads apart) and are not written.
+// Pointers are 16-byte aligned and i is a multiple of 8, so whole
 // groups move as 16-byte vectors.
 template <bool WHOLE>
 __device__ __forceinline__ void load8(const float* p, int64_t i, int64_t n, float* x) {
@@ -46,7 +47,9 @@ __device__ __forceinline__ void load8(const float* p, int64_t i, int64_t n, floa
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) x[c] = i + c < n ? p[i + c] : 0.f;
+    for (int c = 0; c < kPer; ++c) x[c] = p[min(i + c, n - 1)];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) x[c] = i + c < n ? x[c] : 0.f;
   }
 }
 template <bool WHOLE>
@@ -60,7 +63,9 @@ __device__ __forceinline__ void load8(const uint16_t* p, int64_t i, int64_t n, f
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) x[c] = i + c < n ? bf16_to_f32(p[i + c]) : 0.f;
+    for (int c = 0; c < kPer; ++c) x[c] = bf16_to_f32(p[min(i + c, n - 1)]);
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) x[c] = i + c < n ? x[c] : 0.f;
   }
 }
 template <bool WHOLE>
@@ -92,10 +97,11 @@ __device__ __forceinline__ void store8(uint16_t* p, int64_t i, int64_t n, const 
 template <bool WHOLE>
 __device__ __forceinline__ u32x2_t load_codes(const uint8_t* p, int64_t i, int64_t n) {
   if (WHOLE || i + kPer <= n) return *reinterpret_cast<const u32x2_t*>(p + i);
-  uint32_t w[2] = {0u, 0u};
+  uint32_t b[kPer], w[2] = {0u, 0u};
 #pragma unroll
-  for (int c = 0; c < kPer; ++c)
-    if (i + c < n) w[c / 4] |= (uint32_t)p[i + c] << (8 * (c % 4));
+  for (int c = 0; c < kPer; ++c) b[c] = p[min(i + c, n - 1)];
+#pragma unroll
+  for (int c = 0; c < kPer; ++c) w[c / 4] |= i + c < n ? b[c] << (8 * (c % 4)) : 0u;
   return u32x2_t{w[0], w[1]};
 }
 template <bool WHOLE>
@@ -166,9 +172,52 @@ __device__ __forceinline__ void roots(const float* v, float* s) {
   }
 }
 
-template <class P, class G, bool S8, bool MASTER, bool WHOLE>
+// What a thread holds of its 8 elements.
+template <class P, class G, bool S8, bool MASTER>
+struct Eight {
+  float g[kPer], m[kPer], v[kPer], p[kPer];
+  float s[kPer];  // root of v (8-bit states)
+  u32x2_t mc, vc;
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) g[c] = m[c] = v[c] = p[c] = 0.f;
+    mc = vc = u32x2_t{0u, 0u};
+  }
+
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const AdamwTensor& t, int64_t i) {
+    load8<WHOLE>(static_cast<const G*>(t.g), i, t.n, g);
+    if constexpr (S8) {
+      mc = load_codes<WHOLE>(static_cast<const uint8_t*>(t.m), i, t.n);
+      vc = load_codes<WHOLE>(static_cast<const uint8_t*>(t.v), i, t.n);
+    } else {
+      load8<WHOLE>(static_cast<const float*>(t.m), i, t.n, m);
+      load8<WHOLE>(static_cast<const float*>(t.v), i, t.n, v);
+    }
+    if constexpr (MASTER) load8<WHOLE>(t.master, i, t.n, p);
+    else load8<WHOLE>(static_cast<const P*>(t.p), i, t.n, p);
+  }
+
+  template <bool WHOLE>
+  __device__ __forceinline__ void store(const AdamwTensor& t, int64_t i) const {
+    if constexpr (MASTER) store8<WHOLE>(t.master, i, t.n, p);
+    store8<WHOLE>(static_cast<P*>(t.p), i, t.n, p);
+    if constexpr (S8) {
+      store_codes<WHOLE>(static_cast<uint8_t*>(t.m), i, t.n, mc);
+      store_codes<WHOLE>(static_cast<uint8_t*>(t.v), i, t.n, vc);
+    } else {
+      store8<WHOLE>(static_cast<float*>(t.m), i, t.n, m);
+      store8<WHOLE>(static_cast<float*>(t.v), i, t.n, v);
+    }
+  }
+};
+
+// FULL: the chunk has all its elements.
+template <class P, class G, bool S8, bool MASTER, bool FULL>
 __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwTensor& t, int64_t i) {
 #pragma clang fp contract(off)
+  const int64_t run = i / 256;
   float decay = a.decay, rate = a.rate, gs = a.grad_scale, isb2 = a.inv_sqrt_bias2;
   if (a.dyn) {
     const float lr = a.dyn[0];
@@ -177,61 +226,54 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwTenso
     rate = lr * a.dyn[2];
     isb2 = a.dyn[3];
   }
-  float g[kPer], m[kPer], v[kPer], p[kPer], s[kPer];
-  load8<WHOLE>(static_cast<const G*>(t.g), i, t.n, g);
-  const int64_t run = i / 256;
-  if constexpr (S8) {
-    const bool in = WHOLE || i < t.n;
-    const u32x2_t mc = load_codes<WHOLE>(static_cast<const uint8_t*>(t.m), i, t.n);
-    const u32x2_t vc = load_codes<WHOLE>(static_cast<const uint8_t*>(t.v), i, t.n);
-    decode8(mc, in ? t.ms[run] : 0.f, m);
-    decode8(vc, in ? t.vs[run] : 0.f, s);
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) v[c] = s[c] * s[c];
-  } else {
-    load8<WHOLE>(static_cast<const float*>(t.m), i, t.n, m);
-    load8<WHOLE>(static_cast<const float*>(t.v), i, t.n, v);
+  Eight<P, G, S8, MASTER> x;
+  // (one branch around all the loads: around each, they wait for one another)
+  const bool whole = FULL || i + kPer <= t.n, some = FULL || i < t.n;
+  float scale_m = 0.f, scale_s = 0.f;
+  if (S8 && some) {
+    scale_m = t.ms[run];
+    scale_s = t.vs[run];
   }
-  if constexpr (MASTER) load8<WHOLE>(t.master, i, t.n, p);
-  else load8<WHOLE>(static_cast<const P*>(t.p), i, t.n, p);
+  if (whole) x.template load<true>(t, i);
+  else if (some) x.template load<false>(t, i);
+  else x.zero();
+  if constexpr (S8) {
+    decode8(x.mc, scale_m, x.m);
+    decode8(x.vc, scale_s, x.s);
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) x.v[c] = x.s[c] * x.s[c];
+  }
 #pragma unroll
   for (int c = 0; c < kPer; ++c) {
-    g[c] *= gs;
-    m[c] = m[c] * a.beta1 + g[c] * a.rest1;
-    v[c] = v[c] * a.beta2 + (g[c] * g[c]) * a.rest2;
+    x.g[c] *= gs;
+    x.m[c] = x.m[c] * a.beta1 + x.g[c] * a.rest1;
+    x.v[c] = x.v[c] * a.beta2 + (x.g[c] * x.g[c]) * a.rest2;
   }
-  roots(v, s);
+  roots(x.v, x.s);
 #pragma unroll
   for (int c = 0; c < kPer; ++c)  // (the reciprocal to 1 ulp: the quotient's error stays far below m's)
-    p[c] = p[c] * decay - (m[c] * __builtin_amdgcn_rcpf(s[c] * isb2 + a.eps)) * rate;
-  if constexpr (MASTER) store8<WHOLE>(t.master, i, t.n, p);
-  store8<WHOLE>(static_cast<P*>(t.p), i, t.n, p);
+    x.p[c] = x.p[c] * decay - (x.m[c] * __builtin_amdgcn_rcpf(x.s[c] * isb2 + a.eps)) * rate;
   if constexpr (S8) {
-    float scale_m, inv_m, scale_s, inv_s;
-    run_scale(m, &scale_m, &inv_m);
-    run_scale(s, &scale_s, &inv_s);
+    float inv_m, inv_s;
+    run_scale(x.m, &scale_m, &inv_m);
+    run_scale(x.s, &scale_s, &inv_s);
 #pragma unroll
     for (int c = 0; c < kPer; ++c) {
-      m[c] *= inv_m;
-      s[c] *= inv_s;
-      s[c] = s[c] > 0.f ? fmaxf(s[c], 0x1p-9f) : s[c];  // (the smallest code)
+      x.m[c] *= inv_m;
+      x.s[c] *= inv_s;
+      x.s[c] = x.s[c] > 0.f ? fmaxf(x.s[c], 0x1p-9f) : x.s[c];  // (the smallest code)
     }
-    if (WHOLE || i < t.n) {
-      store_codes<WHOLE>(static_cast<uint8_t*>(t.m), i, t.n, encode8(m));
-      store_codes<WHOLE>(static_cast<uint8_t*>(t.v), i, t.n, encode8(s));
-      if ((threadIdx.x & (kRunLanes - 1)) == 0) {
-        t.ms[run] = scale_m;
-        t.vs[run] = scale_s;
-      }
+    x.mc = encode8(x.m);
+    x.vc = encode8(x.s);
+    if (some && (threadIdx.x & (kRunLanes - 1)) == 0) {
+      t.ms[run] = scale_m;
+      t.vs[run] = scale_s;
     }
-  } else {
-    store8<WHOLE>(static_cast<float*>(t.m), i, t.n, m);
-    store8<WHOLE>(static_cast<float*>(t.v), i, t.n, v);
   }
+  if (whole) x.template store<true>(t, i);
+  else if (some) x.template store<false>(t, i);
 }
 
-// (bounds only in a tensor's last chunk: a branch around each load would make
-// the loads wait for one another)
 template <class P, class G, bool S8, bool MASTER>
 __global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwArgs a) {
   const AdamwChunk ch = a.chunks[blockIdx.x];
