@@ -440,7 +440,8 @@ int salr_moe_expert(const salr_moe_layer_t* G, int32_t e, salr_layer_t* out);
  * X    device bf16 [T][K], rows grouped by expert; Y device bf16 [T][N]
  *      (may not alias X).
  * expert_offsets  DEVICE int32 [E + 1], read by the kernels (routing needs
- *      no host round trip): off[0] = 0, nondecreasing, off[E] = T.  The
+ *      no host round trip; salr_moe_dispatch writes them): off[0] = 0,
+ *      nondecreasing, off[E] <= T (rows from off[E] on are not written).  The
  *      kernels clamp each boundary into [0, T] and never leave X or Y, but
  *      rows outside every valid group are then not written.
  * m_cap  the expected most rows of one expert (0: T); it only sizes the

@@ -693,6 +693,20 @@ class SalrMoE:
         _check(_lib().salr_moe_expert(C.byref(d), e, C.byref(out)), "salr_moe_expert")
         return out
 
+    def expert_adapters(self, e: int):
+        """Expert e's adapters as stored, (a_cat bf16 [r_cat][K], b_cat bf16
+        [N][r_cat]): views into the stacked buffers, so that an optimizer's
+        step on them is what the next forward reads."""
+        import torch
+
+        if not 0 <= e < self.E:
+            raise ValueError(f"expert must be in [0, {self.E})")
+        sz = moe_query_sizes(self.E, self.N, self.K, self.n_keep, self.r_cat, 0)
+        view = lambda buf, stride, rows, cols: buf[e * stride:e * stride + rows * cols].view(torch.bfloat16).view(
+            rows, cols)
+        return (view(self.a_cat, sz["a_cat_stride"], self.r_cat, self.K),
+                view(self.b_cat, sz["b_cat_stride"], self.N, self.r_cat))
+
     def set_expert(self, e: int, masks, values, offsets, a_cat, b_cat):
         """Upload expert e's encoding from numpy arrays in the stored layout
         (uint64 masks, uint16 values [N][n_keep], uint32 offsets, uint16 a_cat
@@ -763,12 +777,24 @@ MOE_MAX_TOPK = 32
 ADAMW_BLOCK = 256
 
 
+_TORCH = None
+
+
+def _torch():
+    """The torch module (these calls take a few us: an import statement in
+    each helper would be felt)."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+
+        _TORCH = torch
+    return _TORCH
+
+
 def _elsewhere(dev, stream) -> bool:
     """Whether a call on `dev` has to change the current device or stream
     (or cannot run at all): the calls then run themselves inside _Place."""
-    import torch
-
-    return stream is not None or dev.index != torch.cuda.current_device() if dev.type == "cuda" else True
+    return stream is not None or dev.type != "cuda" or dev.index != _torch().cuda.current_device()
 
 
 class _Place:
@@ -796,31 +822,27 @@ class _Place:
 def _raw_stream(dev):
     """The current stream of `dev` as an address.  (torch.cuda.current_stream
     builds a stream object each time, 1.9 us of a 9 us call.)"""
-    import torch
-
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _torch()._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _ptr(t, name, dtype, shape, dev):
     """The address of tensor t after checking it (an empty one: None)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev.index:
+        return t.data_ptr() or None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev} (is on {t.device})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() or None
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _float_type(t, name):
-    import torch
-
-    if t.dtype == torch.bfloat16:
-        return TYPE_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is _torch().float32:
         return TYPE_F32
+    if t.dtype is _torch().bfloat16:
+        return TYPE_BF16
     raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
 
 
@@ -829,8 +851,7 @@ def moe_route(logits, k: int, renorm: bool = True, ids=None, weights=None, strea
     softmax weights (float [T][k]; renorm: over the chosen experts) from
     router logits, bf16 or float [T][E] (salr_moe_route).  -inf logits are
     never chosen: id -1, weight 0 where too few others are left."""
-    import torch
-
+    torch = _torch()
     if logits.dim() != 2:
         raise ValueError("logits must be [T][E]")
     T, E = logits.shape
@@ -852,8 +873,7 @@ def moe_route(logits, k: int, renorm: bool = True, ids=None, weights=None, strea
 def moe_route_backward(logits, ids, dweights, renorm: bool = True, dlogits=None, stream=None):
     """dL/dlogits (the logits' type, [T][E]) from dL/dweights for the choice
     moe_route made (salr_moe_route_backward)."""
-    import torch
-
+    torch = _torch()
     if logits.dim() != 2 or ids.dim() != 2:
         raise ValueError("logits must be [T][E] and ids [T][k]")
     T, E = logits.shape
@@ -887,8 +907,7 @@ def moe_dispatch(ids, E: int, X=None, Xs=None, offsets=None, rows=None, slots=No
     (salr_moe_dispatch).  Returns (Xs bf16 [T * k][D] or None, offsets int32
     [E + 1], rows int32 [T][k], slots int32 [T * k]); ids outside [0, E) get
     row -1, and Xs and slots are not written from row offsets[E] on."""
-    import torch
-
+    torch = _torch()
     if ids.dim() != 2:
         raise ValueError("ids must be [T][k]")
     T, k = ids.shape
@@ -926,8 +945,7 @@ def moe_dispatch(ids, E: int, X=None, Xs=None, offsets=None, rows=None, slots=No
 
 
 def _combine(Ys, rows, weights, base, Y, stream):
-    import torch
-
+    torch = _torch()
     if Ys.dim() != 2 or rows.dim() != 2:
         raise ValueError("the rows' values must be [R][D] and rows [T][k]")
     (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
@@ -963,8 +981,7 @@ def moe_combine_backward(dY, Ys, rows, weights=None, dYs=None, dweights=None, st
     weights[t][j] dY[t]; dweights float [T][k], the products <dY[t],
     Ys[rows[t][j]]>).  A dYs made here is zero in the rows that no slot
     names; a given one keeps them (salr_moe_combine_backward)."""
-    import torch
-
+    torch = _torch()
     if Ys.dim() != 2 or rows.dim() != 2:
         raise ValueError("Ys must be [R][D] and rows [T][k]")
     (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
@@ -990,8 +1007,7 @@ def adamw_states(params, bits: int = 32, master: bool = False) -> dict:
     (float, or with bits = 8 e4m3 codes with the lists m_scale and v_scale)
     and, with master, float copies of bf16 parameters; keywords of
     adamw_plan."""
-    import torch
-
+    torch = _torch()
     if bits not in (8, 32):
         raise ValueError("bits must be 8 or 32")
     zeros = lambda n, dtype: [torch.zeros(n(p), dtype=dtype, device=p.device) for p in params]
@@ -1022,8 +1038,7 @@ def adamw_plan(params, grads, m, v, m_scale=None, v_scale=None, master=None, str
     adamw_states), element i of every list belonging together; all tensors
     contiguous and 16-byte aligned (scales: 4-byte), written ones disjoint.
     Synchronous."""
-    import torch
-
+    torch = _torch()
     lists = {"params": params, "grads": grads, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale,
              "master": master}
     lists = {name: list(ts) for name, ts in lists.items() if ts is not None}
@@ -1081,8 +1096,7 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     in place and in one launch (salr_adamw_step).  dyn: a device float
     tensor [4] with adamw_dyn's values, read when the step runs instead of
     step, lr and grad_scale (for captured graphs)."""
-    import torch
-
+    torch = _torch()
     args, dev = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale), plan.device
     if _elsewhere(dev, stream):
         with _Place(dev, stream):
