@@ -791,10 +791,16 @@ def _torch():
     return _TORCH
 
 
-def _elsewhere(dev, stream) -> bool:
-    """Whether a call on `dev` has to change the current device or stream
-    (or cannot run at all): the calls then run themselves inside _Place."""
-    return stream is not None or dev.type != "cuda" or dev.index != _torch().cuda.current_device()
+def _stream_here(dev, stream):
+    """The current stream of `dev` as an address where a call can run as
+    things are; None where the current device or stream has to change first
+    (or the call cannot run): the calls then run themselves inside _Place.
+    (torch.cuda.current_stream builds a stream object each time, 1.9 us of a
+    9 us call.)"""
+    c = _torch()._C
+    if stream is None and dev.type == "cuda" and dev.index == c._cuda_getDevice():
+        return c._cuda_getCurrentRawStream(dev.index)
+    return None
 
 
 class _Place:
@@ -817,12 +823,6 @@ class _Place:
         for c in reversed(self._contexts):
             c.__exit__(*exc)
         return False
-
-
-def _raw_stream(dev):
-    """The current stream of `dev` as an address.  (torch.cuda.current_stream
-    builds a stream object each time, 1.9 us of a 9 us call.)"""
-    return _torch()._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _ptr(t, name, dtype, shape, dev):
@@ -856,7 +856,8 @@ def moe_route(logits, k: int, renorm: bool = True, ids=None, weights=None, strea
         raise ValueError("logits must be [T][E]")
     T, E = logits.shape
     dev, shape = logits.device, (T, k)
-    if _elsewhere(dev, stream):
+    at = _stream_here(dev, stream)
+    if at is None:
         with _Place(dev, stream):
             return moe_route(logits, k, renorm, ids, weights)
     if ids is None:
@@ -865,7 +866,7 @@ def moe_route(logits, k: int, renorm: bool = True, ids=None, weights=None, strea
         weights = torch.empty(shape, dtype=torch.float32, device=dev)
     _check(_lib().salr_moe_route(_ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"),
                                  T, E, k, bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
-                                 _ptr(weights, "weights", torch.float32, shape, dev), _raw_stream(dev)),
+                                 _ptr(weights, "weights", torch.float32, shape, dev), at),
            "salr_moe_route")
     return ids, weights
 
@@ -878,7 +879,8 @@ def moe_route_backward(logits, ids, dweights, renorm: bool = True, dlogits=None,
         raise ValueError("logits must be [T][E] and ids [T][k]")
     T, E = logits.shape
     dev, shape = logits.device, (T, ids.shape[1])
-    if _elsewhere(dev, stream):
+    at = _stream_here(dev, stream)
+    if at is None:
         with _Place(dev, stream):
             return moe_route_backward(logits, ids, dweights, renorm, dlogits)
     if dlogits is None:
@@ -887,7 +889,7 @@ def moe_route_backward(logits, ids, dweights, renorm: bool = True, dlogits=None,
         _ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"), T, E, shape[1],
         bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
         _ptr(dweights, "dweights", torch.float32, shape, dev),
-        _ptr(dlogits, "dlogits", logits.dtype, (T, E), dev), _raw_stream(dev)), "salr_moe_route_backward")
+        _ptr(dlogits, "dlogits", logits.dtype, (T, E), dev), at), "salr_moe_route_backward")
     return dlogits
 
 
@@ -912,7 +914,8 @@ def moe_dispatch(ids, E: int, X=None, Xs=None, offsets=None, rows=None, slots=No
         raise ValueError("ids must be [T][k]")
     T, k = ids.shape
     n, D, dev = T * k, 0, ids.device
-    if _elsewhere(dev, stream):
+    at = _stream_here(dev, stream)
+    if at is None:
         with _Place(dev, stream):
             return moe_dispatch(ids, E, X, Xs, offsets, rows, slots, ws)
     if offsets is None:
@@ -940,7 +943,7 @@ def moe_dispatch(ids, E: int, X=None, Xs=None, offsets=None, rows=None, slots=No
                                     _ptr(offsets, "offsets", torch.int32, (E + 1,), dev),
                                     _ptr(rows, "rows", torch.int32, (T, k), dev),
                                     _ptr(slots, "slots", torch.int32, (n,), dev), xs, ws.data_ptr(),
-                                    ws.numel() * ws.element_size(), _raw_stream(dev)), "salr_moe_dispatch")
+                                    ws.numel() * ws.element_size(), at), "salr_moe_dispatch")
     return Xs, offsets, rows, slots
 
 
@@ -950,7 +953,8 @@ def _combine(Ys, rows, weights, base, Y, stream):
         raise ValueError("the rows' values must be [R][D] and rows [T][k]")
     (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
     bf16 = torch.bfloat16
-    if _elsewhere(dev, stream):
+    at = _stream_here(dev, stream)
+    if at is None:
         with _Place(dev, stream):
             return _combine(Ys, rows, weights, base, Y, None)
     if Y is None:
@@ -959,7 +963,7 @@ def _combine(Ys, rows, weights, base, Y, stream):
         _ptr(Ys, "the rows' values", bf16, (R, D), dev), R, _ptr(rows, "rows", torch.int32, (T, k), dev),
         None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev),
         None if base is None else _ptr(base, "base", bf16, (T, D), dev), T, k, D,
-        _ptr(Y, "the output", bf16, (T, D), dev), _raw_stream(dev)), "salr_moe_combine")
+        _ptr(Y, "the output", bf16, (T, D), dev), at), "salr_moe_combine")
     return Y
 
 
@@ -986,7 +990,8 @@ def moe_combine_backward(dY, Ys, rows, weights=None, dYs=None, dweights=None, st
         raise ValueError("Ys must be [R][D] and rows [T][k]")
     (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
     bf16 = torch.bfloat16
-    if _elsewhere(dev, stream):
+    at = _stream_here(dev, stream)
+    if at is None:
         with _Place(dev, stream):
             return moe_combine_backward(dY, Ys, rows, weights, dYs, dweights)
     if dYs is None:
@@ -997,7 +1002,7 @@ def moe_combine_backward(dY, Ys, rows, weights=None, dYs=None, dweights=None, st
         _ptr(dY, "dY", bf16, (T, D), dev), _ptr(Ys, "Ys", bf16, (R, D), dev), R,
         _ptr(rows, "rows", torch.int32, (T, k), dev),
         None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev), T, k, D,
-        _ptr(dYs, "dYs", bf16, (R, D), dev), _ptr(dweights, "dweights", torch.float32, (T, k), dev), _raw_stream(dev)),
+        _ptr(dYs, "dYs", bf16, (R, D), dev), _ptr(dweights, "dweights", torch.float32, (T, k), dev), at),
         "salr_moe_combine_backward")
     return dYs, dweights
 
@@ -1076,12 +1081,13 @@ def adamw_plan(params, grads, m, v, m_scale=None, v_scale=None, master=None, str
     sizes = (C.c_int64 * count)(*[r.n for r in recs])
     _check(_lib().salr_adamw_plan_bytes(sizes, count, C.byref(nbytes)), "salr_adamw_plan_bytes")
     p_type, g_type = _float_type(params[0], "params"), _float_type(lists["grads"][0], "grads")
-    if _elsewhere(dev, stream):
+    at = _stream_here(dev, stream)
+    if at is None:
         with _Place(dev, stream):
             return adamw_plan(**lists)
     table = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
     _check(_lib().salr_adamw_plan(recs, count, p_type, g_type, STATE_8BIT if bits8 else STATE_F32,
-                                  table.data_ptr(), nbytes.value, C.byref(desc), _raw_stream(dev)), "salr_adamw_plan")
+                                  table.data_ptr(), nbytes.value, C.byref(desc), at), "salr_adamw_plan")
     return AdamWPlan(desc, table, [t for ts in lists.values() for t in ts], dev)
 
 
@@ -1098,11 +1104,12 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     step, lr and grad_scale (for captured graphs)."""
     torch = _torch()
     args, dev = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale), plan.device
-    if _elsewhere(dev, stream):
+    at = _stream_here(dev, stream)
+    if at is None:
         with _Place(dev, stream):
             return adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, dyn)
     d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (4,), dev)
-    _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, _raw_stream(dev)), "salr_adamw_step")
+    _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, at), "salr_adamw_step")
 
 
 def probe_stream_read(src, sink, workgroups: int, stream=None):
