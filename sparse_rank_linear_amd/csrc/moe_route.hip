@@ -12,6 +12,12 @@
 // once.  The k largest are taken one after the other: a maximum over the
 // group, then the lowest expert that holds it; within 16 lanes both run on
 // DPP row rotations, without the LDS round trips of a shuffle.
+//
+// Bound by the launch up to a few thousand rows, then by the issue of
+// instructions (16384 rows of 64 floats, top 6: 4.2 us, backward 4.1, where
+// reading and writing them takes 0.8 and 1.5; 16384 of 256, top 8: 8.7 and
+// 10.6).  A wave per row took 18.6 us for the first, float maxima (which
+// quiet NaNs) and the library's exp 4.9.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -34,7 +40,7 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = f32_to_
 // v combined over the row's lanes, in every one of them.
 template <int N>
 __device__ __forceinline__ int row_ror(int v) {  // lane i of 16 from lane (i - N) mod 16
-  return __builtin_amdgcn_update_dpp(v, v, 0x120 + N, 0xF, 0xF, false);
+  return __builtin_amdgcn_update_dpp(0, v, 0x120 + N, 0xF, 0xF, true);
 }
 template <int LANES, class F>
 __device__ __forceinline__ int group_all(int v, F f) {
@@ -49,10 +55,12 @@ __device__ __forceinline__ int group_all(int v, F f) {
   return v;
 }
 template <int LANES>
-__device__ __forceinline__ float group_max(float v) {  // (NaN left aside)
-  return __int_as_float(group_all<LANES>(__float_as_int(v), [](int a, int b) {
-    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
-  }));
+__device__ __forceinline__ int group_max(int v) {
+  return group_all<LANES>(v, [](int a, int b) { return max(a, b); });
+}
+template <int LANES>
+__device__ __forceinline__ int group_min(int v) {
+  return group_all<LANES>(v, [](int a, int b) { return min(a, b); });
 }
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
@@ -60,9 +68,25 @@ __device__ __forceinline__ float group_sum(float v) {
     return __float_as_int(__int_as_float(a) + __int_as_float(b));
   }));
 }
-template <int LANES>
-__device__ __forceinline__ int group_min(int v) {
-  return group_all<LANES>(v, [](int a, int b) { return min(a, b); });
+
+// Logits as integers in the same order (-0 as 0, NaN as -inf): their maxima
+// take one instruction each, where those of floats also quiet NaNs.
+constexpr int kLeast = (int)0x807FFFFF;  // order_of(-inf)
+__device__ __forceinline__ int order_of(float x) {
+  const int b = __float_as_int(x + 0.f);
+  return x == x ? b ^ ((b >> 31) & 0x7FFFFFFF) : kLeast;
+}
+__device__ __forceinline__ float value_of(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7FFFFFFF)); }
+
+// exp(x) for x <= 0 to 2 ulp, 0 below -150 (NaN stays): 2^y for y = x log2(e),
+// times 1 + ln(2) (x log2(e) - y) for what y's rounding dropped.
+__device__ __forceinline__ float exp_down(float x) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  x = x < -150.f ? -150.f : x;
+  const float y = x * kLog2e;
+  const float rest = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return __builtin_fmaf(e, rest * kLn2, e);
 }
 
 template <class Tl, int LANES, int PER>
@@ -72,55 +96,56 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const Tl* logi
   const int lane = threadIdx.x % LANES;
   const int64_t groups = (int64_t)gridDim.x * (kRouteThreads / LANES);
   for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES; t < T; t += groups) {
+    const Tl* row = logits + t * E;
     float l[PER];
+    int o[PER];
+#pragma unroll
+    for (int q = 0; q < PER; ++q) l[q] = q * LANES + lane < E ? load_logit(row + q * LANES + lane) : kNegInf;
+    int best = kLeast;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      const int e = q * LANES + lane;
-      l[q] = e < E ? load_logit(logits + t * E + e) : kNegInf;
+      o[q] = order_of(l[q]);
+      best = max(best, o[q]);
     }
-    float top = kNegInf;
-#pragma unroll
-    for (int q = 0; q < PER; ++q) top = fmaxf(top, l[q]);
-    top = group_max<LANES>(top);
+    best = group_max<LANES>(best);
+    const float top = value_of(best);
     float total = 0.f;
     if (!renorm) {
 #pragma unroll
-      for (int q = 0; q < PER; ++q) total += q * LANES + lane < E ? expf(l[q] - top) : 0.f;
+      for (int q = 0; q < PER; ++q) total += q * LANES + lane < E ? exp_down(l[q] - top) : 0.f;
       total = group_sum<LANES>(total);
     }
     // lane j % LANES keeps the j-th choice
-    float val[SLOTS];
-    int id[SLOTS];
+    int val[SLOTS], id[SLOTS];
 #pragma unroll
     for (int c = 0; c < SLOTS; ++c) {
-      val[c] = kNegInf;
+      val[c] = kLeast;
       id[c] = -1;
     }
-    float best = top;
     for (int j = 0; j < k; ++j) {
       int at = 1 << 30;
 #pragma unroll
-      for (int q = PER - 1; q >= 0; --q) at = l[q] == best ? q * LANES + lane : at;
+      for (int q = PER - 1; q >= 0; --q) at = o[q] == best ? q * LANES + lane : at;
       at = group_min<LANES>(at);
-      const bool keep = lane == j % LANES && best > kNegInf;
+      const bool keep = lane == j % LANES && best > kLeast;
 #pragma unroll
       for (int c = 0; c < SLOTS; ++c)
         if (keep && j / LANES == c) {
           val[c] = best;
           id[c] = at;
         }
-      float next = kNegInf;
+      best = kLeast;
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
-        l[q] = q * LANES + lane == at ? kNegInf : l[q];
-        next = fmaxf(next, l[q]);
+        o[q] = q * LANES + lane == at ? kLeast : o[q];
+        best = max(best, o[q]);
       }
-      best = group_max<LANES>(next);
+      best = group_max<LANES>(best);
     }
     float w[SLOTS], sum = 0.f;
 #pragma unroll
     for (int c = 0; c < SLOTS; ++c) {
-      w[c] = id[c] >= 0 ? expf(val[c] - top) : 0.f;
+      w[c] = id[c] >= 0 ? exp_down(value_of(val[c]) - top) : 0.f;
       sum += w[c];
     }
     if (renorm) total = group_sum<LANES>(sum);
@@ -138,37 +163,73 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_backward_kernel(const
                                                                            int32_t k, int32_t renorm,
                                                                            const int32_t* ids, const float* dweights,
                                                                            Tl* dlogits) {
+  constexpr int SLOTS = SALR_MOE_MAX_TOPK > LANES ? SALR_MOE_MAX_TOPK / LANES : 1;
+  constexpr int BATCH = 4;  // choices handed round together
   const int lane = threadIdx.x % LANES;
   const int64_t groups = (int64_t)gridDim.x * (kRouteThreads / LANES);
   for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES; t < T; t += groups) {
+    const Tl* row = logits + t * E;
+    int id[SLOTS];
+    float dw[SLOTS];
+#pragma unroll
+    for (int c = 0; c < SLOTS; ++c) {
+      const bool in = c * LANES + lane < k;
+      id[c] = in ? ids[t * k + c * LANES + lane] : -1;
+      dw[c] = in ? dweights[t * k + c * LANES + lane] : 0.f;
+    }
     float l[PER], up[PER];  // logit, gradient that reaches its probability
-    bool chosen[PER];
+    bool in[PER];           // part of the softmax
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int e = q * LANES + lane;
-      l[q] = e < E ? load_logit(logits + t * E + e) : kNegInf;
+      l[q] = e < E ? load_logit(row + e) : kNegInf;
       up[q] = 0.f;
-      chosen[q] = false;
+      in[q] = !renorm && e < E;
     }
-    for (int j = 0; j < k; ++j) {  // (one address a group)
-      const int e = ids[t * k + j];
-      const float d = dweights[t * k + j];
+    if constexpr (LANES == 64) {
+      // (one row a wave: each choice is the wave's, and only one q's registers take it)
+      for (int j = 0; j < k; ++j) {
+        const int e = __builtin_amdgcn_readlane(id[0], j);
+        const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dw[0]), j));
+        if ((uint32_t)e >= (uint32_t)E) continue;
 #pragma unroll
-      for (int q = 0; q < PER; ++q)
-        if (e == q * LANES + lane && e < E) {
-          up[q] += d;
-          chosen[q] = true;
+        for (int q = 0; q < PER; ++q)
+          if (e / LANES == q) {
+            const bool hit = lane == e % LANES;
+            up[q] += hit ? d : 0.f;
+            in[q] = in[q] || hit;
+          }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < SLOTS; ++c)
+        for (int j0 = c * LANES; j0 < min(k, (c + 1) * LANES); j0 += BATCH) {
+          int ej[BATCH];
+          float dj[BATCH];
+#pragma unroll
+          for (int b = 0; b < BATCH; ++b) {  // (past k: id -1, which no lane has)
+            ej[b] = __shfl(id[c], (j0 + b) % LANES, LANES);
+            dj[b] = __shfl(dw[c], (j0 + b) % LANES, LANES);
+          }
+#pragma unroll
+          for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+              const bool hit = ej[b] == q * LANES + lane && ej[b] < E;
+              up[q] += hit ? dj[b] : 0.f;
+              in[q] = in[q] || hit;
+            }
         }
     }
-    float top = kNegInf;
+    int best = kLeast;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) top = fmaxf(top, !renorm || chosen[q] ? l[q] : kNegInf);
-    top = group_max<LANES>(top);
+    for (int q = 0; q < PER; ++q) best = max(best, in[q] ? order_of(l[q]) : kLeast);
+    best = group_max<LANES>(best);
+    const float top = value_of(best);
     float total = 0.f, c = 0.f;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      const bool in = q * LANES + lane < E && (!renorm || chosen[q]);
-      l[q] = in && top > kNegInf ? expf(l[q] - top) : 0.f;
+      l[q] = in[q] && best > kLeast ? exp_down(l[q] - top) : 0.f;
       total += l[q];
       c += l[q] * up[q];
     }
