@@ -469,8 +469,9 @@ int salr_moe_forward(const salr_moe_layer_t* G, const uint16_t* X, int64_t T,
  * expert, or -1.  Types: SALR_TYPE_BF16 or SALR_TYPE_F32 where a call names
  * one; ids, rows and offsets are int32, router weights and their gradients
  * float, token rows bf16.  Sums are held in fp32 and rounded once to bf16.
- * T == 0 is allowed everywhere.  Results do not depend on timing: no call
- * here sums with floating-point atomics.
+ * T == 0 is allowed everywhere.  What a call writes may not overlap anything
+ * else that it is given (INVALID_ARG), except where said.  Results do not
+ * depend on timing: no call here sums with floating-point atomics.
  */
 #define SALR_TYPE_BF16 0
 #define SALR_TYPE_F32 1
@@ -529,7 +530,7 @@ int salr_moe_dispatch_ws_bytes(int64_t T_max, int32_t k, int32_t E, size_t* out)
  *                   off[E] on are not written.  X and Xs both NULL: sort only.
  * ids  device int32 [T][k], any values (see above), also the same expert
  *      twice for one token.
- * X    device bf16 [T][D], 1 <= D <= 2^20 (Xs may not alias it).
+ * X    device bf16 [T][D], 1 <= D <= 2^20.
  * ws   device, salr_moe_dispatch_ws_bytes long for some T_max >= T with this
  *      k and E; contents on entry do not matter.  Calls that share it (or
  *      captured graphs of such calls) must be ordered.
@@ -550,8 +551,7 @@ int salr_moe_dispatch(const int32_t* ids, int64_t T, int32_t k, int32_t E,
  * weights  device float [T][k], or NULL: ones.
  * base     device bf16 [T][D] (a shared expert's output, the residual
  *          stream; may be Y itself), or NULL: zeros.
- * Y        device bf16 [T][D] (may not alias Ys).  A token without any row gets
- *          base, or zeros.
+ * Y        device bf16 [T][D].  A token without any row gets base, or zeros.
  * Asynchronous on `stream`.  Errors: INVALID_ARG, HIP.
  */
 int salr_moe_combine(const uint16_t* Ys, int64_t R, const int32_t* rows,
@@ -568,7 +568,7 @@ int salr_moe_combine(const uint16_t* Ys, int64_t R, const int32_t* rows,
  *           [0, R) gets dweights 0.
  * weights   device float [T][k], or NULL: ones.
  * dYs       device bf16 [R][D] or NULL to skip; rows that no slot names are
- *           left as they were.  May be Ys's own buffer, not dY's.
+ *           left as they were.  May be Ys's own buffer.
  * dweights  device float [T][k] or NULL to skip (Ys is then not read and may
  *           be NULL).
  * Asynchronous on `stream`.  Errors: INVALID_ARG, HIP.

@@ -29,6 +29,8 @@ inline int status(hipError_t e) { return e == hipSuccess ? SALR_OK : SALR_ERR_HI
 
 bool type_ok(int32_t t) { return t == SALR_TYPE_BF16 || t == SALR_TYPE_F32; }
 
+size_t type_bytes(int32_t t) { return t == SALR_TYPE_F32 ? 4 : 2; }
+
 bool slots_ok(int64_t T, int32_t k) {
   return T >= 0 && k >= 1 && k <= SALR_MOE_MAX_TOPK && T <= kMaxSlots / k;
 }
@@ -51,6 +53,27 @@ bool all_aligned(const void* const (&p)[n]) {
   return true;
 }
 
+// A buffer of a call, and whether two share no byte.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool apart(const Span& x, const Span& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return !x.p || !y.p || a + x.bytes <= b || b + y.bytes <= a;
+}
+// What a call writes shares no byte with anything else of it.
+template <size_t nw, size_t nr>
+bool writes_apart(const Span (&written)[nw], const Span (&read)[nr]) {
+  for (size_t i = 0; i < nw; ++i) {
+    for (size_t j = i + 1; j < nw; ++j)
+      if (!apart(written[i], written[j])) return false;
+    for (const Span& r : read)
+      if (!apart(written[i], r)) return false;
+  }
+  return true;
+}
+
 size_t dispatch_ws(int64_t n, int32_t E) {
   return align_up((size_t)std::min<int64_t>(salr::kMoeSortChunks, std::max<int64_t>(1, cdiv(n, 1024))) * E * 4, 256);
 }
@@ -64,6 +87,9 @@ int salr_moe_route(const void* logits, int32_t logits_type, int64_t T, int32_t E
   if (!route_ok(logits_type, T, E, k)) return SALR_ERR_INVALID_ARG;
   if (T == 0) return SALR_OK;
   if (!all_given({logits, ids, weights})) return SALR_ERR_INVALID_ARG;
+  const size_t n = (size_t)T * k;
+  if (!writes_apart({{ids, n * 4}, {weights, n * 4}}, {{logits, (size_t)T * E * type_bytes(logits_type)}}))
+    return SALR_ERR_INVALID_ARG;
   return status(salr::launch_moe_route(logits, logits_type == SALR_TYPE_F32, T, E, k, renorm != 0, ids, weights,
                                        static_cast<hipStream_t>(stream)));
 }
@@ -73,6 +99,9 @@ int salr_moe_route_backward(const void* logits, int32_t logits_type, int64_t T, 
   if (!route_ok(logits_type, T, E, k)) return SALR_ERR_INVALID_ARG;
   if (T == 0) return SALR_OK;
   if (!all_given({logits, ids, dweights, dlogits})) return SALR_ERR_INVALID_ARG;
+  const size_t n = (size_t)T * k, bytes = (size_t)T * E * type_bytes(logits_type);
+  if (!writes_apart({{dlogits, bytes}}, {{ids, n * 4}, {dweights, n * 4}, {dlogits == logits ? nullptr : logits, bytes}}))
+    return SALR_ERR_INVALID_ARG;
   return status(salr::launch_moe_route_backward(logits, logits_type == SALR_TYPE_F32, T, E, k, renorm != 0, ids,
                                                 dweights, dlogits, static_cast<hipStream_t>(stream)));
 }
@@ -88,9 +117,14 @@ int salr_moe_dispatch(const int32_t* ids, int64_t T, int32_t k, int32_t E, const
                       void* stream) {
   if (!slots_ok(T, k) || E < 1 || E > kMaxExperts) return SALR_ERR_INVALID_ARG;
   if (!expert_offsets || (T > 0 && (!ids || !rows || !X != !Xs))) return SALR_ERR_INVALID_ARG;
-  if (T > 0 && X && (D < 1 || D > kMaxColumns || X == Xs)) return SALR_ERR_INVALID_ARG;
+  if (T > 0 && X && (D < 1 || D > kMaxColumns)) return SALR_ERR_INVALID_ARG;
   if (!all_aligned({ids, X, expert_offsets, rows, slots, Xs})) return SALR_ERR_INVALID_ARG;
-  if (!ws || !aligned16(ws) || ws_bytes < dispatch_ws(T * k, E)) return SALR_ERR_WORKSPACE;
+  const size_t n = (size_t)T * k, row = X ? (size_t)D * 2 : 0;
+  const Span w{ws, dispatch_ws(n, E)};
+  if (!writes_apart({{expert_offsets, ((size_t)E + 1) * 4}, {rows, n * 4}, {slots, n * 4}, {Xs, n * row}, w},
+                    {{ids, n * 4}, {X, T * row}}))
+    return SALR_ERR_INVALID_ARG;
+  if (!ws || !aligned16(ws) || ws_bytes < w.bytes) return SALR_ERR_WORKSPACE;
   salr::MoeDispatchArgs a{};
   a.ids = ids;
   a.X = T > 0 ? X : nullptr;
@@ -112,8 +146,12 @@ int salr_moe_combine(const uint16_t* Ys, int64_t R, const int32_t* rows, const f
                      int64_t T, int32_t k, int64_t D, uint16_t* Y, void* stream) {
   if (!slots_ok(T, k) || R < 0 || R > kMaxSlots || D < 1 || D > kMaxColumns) return SALR_ERR_INVALID_ARG;
   if (T == 0) return SALR_OK;
-  if (!rows || !Y || (R > 0 && !Ys) || Y == Ys) return SALR_ERR_INVALID_ARG;
+  if (!rows || !Y || (R > 0 && !Ys)) return SALR_ERR_INVALID_ARG;
   if (!all_aligned({Ys, rows, weights, base, Y})) return SALR_ERR_INVALID_ARG;
+  const size_t n = (size_t)T * k, row = (size_t)D * 2;
+  if (!writes_apart({{Y, T * row}},
+                    {{Ys, R * row}, {rows, n * 4}, {weights, n * 4}, {base == Y ? nullptr : base, T * row}}))
+    return SALR_ERR_INVALID_ARG;
   salr::MoeCombineArgs a{};
   a.Ys = Ys;
   a.rows = rows;
@@ -132,8 +170,14 @@ int salr_moe_combine_backward(const uint16_t* dY, const uint16_t* Ys, int64_t R,
                               void* stream) {
   if (!slots_ok(T, k) || R < 0 || R > kMaxSlots || D < 1 || D > kMaxColumns) return SALR_ERR_INVALID_ARG;
   if (T == 0 || (!dYs && !dweights)) return SALR_OK;
-  if (!dY || !rows || (R > 0 && dweights && !Ys) || dYs == dY) return SALR_ERR_INVALID_ARG;
+  if (!dY || !rows || (R > 0 && dweights && !Ys)) return SALR_ERR_INVALID_ARG;
   if (!all_aligned({dY, Ys, rows, weights, dYs, dweights})) return SALR_ERR_INVALID_ARG;
+  const size_t n = (size_t)T * k, row = (size_t)D * 2;
+  const Span ys{Ys, R * row};
+  if (!writes_apart({{dYs, R * row}, {dweights, n * 4}},
+                    {{dY, T * row}, {rows, n * 4}, {weights, n * 4}, {dYs == Ys ? nullptr : Ys, R * row}}) ||
+      !apart({dweights, n * 4}, ys))
+    return SALR_ERR_INVALID_ARG;
   salr::MoeCombineArgs a{};
   a.dY = dY;
   a.Ys = Ys;

@@ -22,8 +22,13 @@ def test_route_refusals():
                 dict(weights=P + 2), dict(type=2), dict(type=-1), dict(T=-1), dict(E=0), dict(E=4097), dict(k=0),
                 dict(k=9), dict(E=64, k=33), dict(T=1 << 31), dict(T=(1 << 31) // 2, k=2)):
         assert _route(**bad) == -1, bad
+    # what is written overlaps nothing (logits 4 x 8 floats, ids and weights 4 x 2 words)
+    for bad in (dict(ids=P + 112), dict(weights=P), dict(weights=P + 4096 + 16), dict(ids=P - 16)):
+        assert _route(**bad) == -1, bad
     lib = srl.lib()
     args = [P, 1, 4, 8, 2, 1, P + 4096, P + 8192, P + 16384, None]
+    for over in (P + 4096, P + 8192 + 16, P + 16, P - 112):
+        assert lib.salr_moe_route_backward(*args[:8], over, None) == -1
     for i in (0, 6, 7, 8):
         for v in (None, P + 4):
             assert lib.salr_moe_route_backward(*args[:i], v, *args[i + 1:]) == -1
@@ -39,9 +44,11 @@ def _dispatch(ids=P, T=4, k=2, E=8, X=P + 4096, D=64, off=P + 8192, rows=P + 122
 def test_dispatch_refusals_and_sizes():
     for bad in (dict(ids=None), dict(rows=None), dict(off=None), dict(X=None), dict(Xs=None), dict(Xs=P + 4096),
                 dict(X=P + 4104), dict(slots=P + 4), dict(off=P + 4), dict(D=0), dict(D=(1 << 20) + 1), dict(T=-1),
-                dict(k=0), dict(k=33), dict(E=0), dict(E=4097), dict(T=1 << 31), dict(T=0, off=None)):
+                dict(k=0), dict(k=33), dict(E=0), dict(E=4097), dict(T=1 << 31), dict(T=0, off=None),
+                dict(rows=P + 16), dict(slots=P + 12288), dict(off=P), dict(Xs=P + 4096 + 496), dict(Xs=P - 16),
+                dict(ws=P + 12288), dict(slots=P)):
         assert _dispatch(**bad) == -1, bad
-    for bad in (dict(ws=None), dict(ws=P + 8), dict(ws_bytes=16), dict(T=0, ws_bytes=0)):
+    for bad in (dict(ws=None), dict(ws=P + 65544), dict(ws_bytes=16), dict(T=0, ws_bytes=0)):
         assert _dispatch(**bad) == -3, bad
     out = C.c_size_t()
     size = srl.lib().salr_moe_dispatch_ws_bytes
@@ -60,7 +67,8 @@ def test_combine_refusals():
     call = lambda **kw: lib.salr_moe_combine(*{**good, **kw}.values(), None)
     assert call(T=0) == 0
     for bad in (dict(Ys=None), dict(rows=None), dict(Y=None), dict(Y=P), dict(Ys=P + 2), dict(rows=P + 4),
-                dict(weights=P + 4), dict(base=P + 8), dict(Y=P + 16386), dict(R=-1), dict(T=-1), dict(k=0),
+                dict(weights=P + 4), dict(base=P + 8), dict(Y=P + 16386), dict(Y=P + 1008), dict(Y=P + 4096 - 16),
+                dict(Y=P + 8192), dict(base=P + 16384 + 16), dict(R=-1), dict(T=-1), dict(k=0),
                 dict(k=33), dict(D=0), dict(D=(1 << 20) + 1), dict(R=1 << 31)):
         assert call(**bad) == -1, bad
     good = dict(dY=P, Ys=P + 65536, R=8, rows=P + 4096, weights=P + 8192, T=4, k=2, D=64, dYs=P + 16384,
@@ -68,7 +76,8 @@ def test_combine_refusals():
     back = lambda **kw: lib.salr_moe_combine_backward(*{**good, **kw}.values(), None)
     assert back(T=0) == 0 and back(dYs=None, dweights=None) == 0
     for bad in (dict(dY=None), dict(Ys=None), dict(rows=None), dict(dYs=P), dict(dY=P + 2), dict(dYs=P + 2),
-                dict(dweights=P + 4), dict(weights=P + 4), dict(R=-1), dict(T=-1), dict(k=0), dict(k=33), dict(D=0)):
+                dict(dweights=P + 4), dict(weights=P + 4), dict(dYs=P + 496), dict(dYs=P + 65536 + 128),
+                dict(dweights=P + 65536 + 1008), dict(dweights=P + 8192), dict(dweights=P + 16384), dict(R=-1), dict(T=-1), dict(k=0), dict(k=33), dict(D=0)):
         assert back(**bad) == -1, bad
 
 
