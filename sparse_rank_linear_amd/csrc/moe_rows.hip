@@ -429,20 +429,24 @@ int32_t moe_sort_chunk(int64_t n) {
 }
 
 // Which form of the dispatch, and how many tokens a workgroup takes in the
-// first two (measured in us on random experts, sort and copy):
-//  - one launch up to 4096 slots: every workgroup reads all of them (680
-//    tokens, 6 of 64, 2048 columns: 8.2; counted first: 9.4);
-//  - counted first while the chunks' counts are few enough for every workgroup to
-//    add up (4099 tokens, 6 of 64, 2048 columns: 25.0; placed in a launch
-//    of their own: 31.3 with its launch);
+// first two (measured in us on random experts, sort and copy unless said):
+//  - one launch up to 8192 slots: every workgroup reads all of them (1024
+//    tokens, 6 of 64, 2048 columns: 9.1; counted first 9.9; at 12288 slots
+//    15.5 against 14.8);
+//  - counted first while the chunks' counts are few enough for every
+//    workgroup to add up (16384 tokens, 2 of 256, 512 columns: 13.0; placed in
+//    a launch of their own 15.7; 8 of 128, 1024 columns: 56.5 and 61.2),
+//    without rows to copy only for as many workgroups as the CUs hold (those
+//    131072 slots sorted alone: 15.0, and 9.4 placed);
 //  - else counted, placed and copied in a launch each.
 // A workgroup's share of the sort does not shrink with its tokens, so there
 // are about kDispatchGroups workgroups (two a CU), not more (1000 tokens, 2
-// of 8: 7.5; with a workgroup a token: 9.6).
-constexpr int64_t kOneLaunchSlots = 4096;
+// of 8, 4096 columns: 7.5; with a workgroup a token 9.6).
+constexpr int64_t kOneLaunchSlots = 8192;
 constexpr int kFusedExperts = 1024;        // (their counters: 8 KB of LDS)
-constexpr int64_t kFusedTable = 4096;      // counts
+constexpr int64_t kFusedTable = 16384;     // counts
 constexpr int64_t kFusedSlots = 1 << 20;   // (a chunk is then 2^14 slots, read by each of its workgroups)
+constexpr int64_t kFusedSortGroups = 1024;
 constexpr int64_t kDispatchGroups = 512;
 
 hipError_t launch_moe_dispatch(const MoeDispatchArgs& args, hipStream_t s) {
@@ -455,9 +459,11 @@ hipError_t launch_moe_dispatch(const MoeDispatchArgs& args, hipStream_t s) {
   if (a.n <= kOneLaunchSlots && a.E <= kFusedExperts) a.chunks = 1;
   else
     hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)a.chunks), dim3(kSortThreads), (size_t)a.E * 4, s, a);
-  if (a.n <= kFusedSlots && a.E <= kFusedExperts && (int64_t)a.chunks * a.E <= kFusedTable) {
-    const int G = (int)std::min<int64_t>(64 / a.k, std::max<int64_t>(1, (T + kDispatchGroups - 1) / kDispatchGroups));
-    const dim3 grid((unsigned)std::max<int64_t>(1, (T + G - 1) / G));
+  const int G = (int)std::min<int64_t>(64 / a.k, std::max<int64_t>(1, (T + kDispatchGroups - 1) / kDispatchGroups));
+  const int64_t fused_groups = std::max<int64_t>(1, (T + G - 1) / G);
+  if (a.n <= kFusedSlots && a.E <= kFusedExperts && (int64_t)a.chunks * a.E <= kFusedTable &&
+      (a.X || fused_groups <= kFusedSortGroups)) {
+    const dim3 grid((unsigned)fused_groups);
     const size_t lds = (size_t)a.E * 8;
     if (vec == 8)
       hipLaunchKernelGGL(moe_dispatch_kernel<8>, grid, dim3(kDispatchThreads), lds, s, a, T, G, bits, (int)p);
