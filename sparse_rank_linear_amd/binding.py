@@ -1061,24 +1061,33 @@ def adamw_plan(params, grads, m, v, m_scale=None, v_scale=None, master=None, str
     dtypes = {"params": (params[0].dtype,), "grads": (lists["grads"][0].dtype,), "m": state_dtypes,
               "v": state_dtypes, "m_scale": (torch.float32,), "v_scale": (torch.float32,),
               "master": (torch.float32,)}
-    field = {"params": "p", "grads": "g"}
-    recs = (salr_adamw_tensor_t * count)()
-    for name, ts in lists.items():
-        for i, t in enumerate(ts):
-            n = params[i].numel()
-            want = -(-n // ADAMW_BLOCK) if name.endswith("_scale") else n
-            if t.dtype not in dtypes[name]:
-                raise TypeError(f"{name}[{i}] must be {dtypes[name][0]} (got {t.dtype})")
-            if t.numel() != want:
-                raise ValueError(f"{name}[{i}] must have {want} elements (got {t.numel()})")
-            if t.device != dev:
-                raise ValueError(f"{name}[{i}] must be on {dev} (is on {t.device})")
-            if not t.is_contiguous():
-                raise ValueError(f"{name}[{i}] must be contiguous")
-            setattr(recs[i], field.get(name, name), t.data_ptr() or None)
-            recs[i].n = n
+    size = [p.numel() for p in params]
+    runs = [-(-n // ADAMW_BLOCK) for n in size]
+    where = -1 if dev.index is None else dev.index
+    columns, T = [], torch.Tensor
+    for name in ("params", "grads", "m", "v", "m_scale", "v_scale", "master"):
+        ts = lists.get(name)
+        if ts is None:
+            columns.append([0] * count)
+            continue
+        want = runs if name.endswith("_scale") else size
+        if not (list(map(T.numel, ts)) == want and set(map(T.get_device, ts)) == {where}
+                and all(map(T.is_contiguous, ts)) and {t.dtype for t in ts} <= set(dtypes[name])):
+            for i, (t, n) in enumerate(zip(ts, want)):  # (which one)
+                if t.dtype not in dtypes[name]:
+                    raise TypeError(f"{name}[{i}] must be {dtypes[name][0]} (got {t.dtype})")
+                if t.numel() != n:
+                    raise ValueError(f"{name}[{i}] must have {n} elements (got {t.numel()})")
+                if t.get_device() != where:
+                    raise ValueError(f"{name}[{i}] must be on {dev} (is on {t.device})")
+                if not t.is_contiguous():
+                    raise ValueError(f"{name}[{i}] must be contiguous")
+        columns.append(list(map(T.data_ptr, ts)))
+    # (a record is its seven addresses and its size, eight bytes each)
+    words = [w for record in zip(*columns, size) for w in record]
+    recs = C.cast((C.c_uint64 * len(words))(*words), C.POINTER(salr_adamw_tensor_t))
     desc, nbytes = salr_adamw_plan_t(), C.c_size_t()
-    sizes = (C.c_int64 * count)(*[r.n for r in recs])
+    sizes = (C.c_int64 * count)(*size)
     _check(_lib().salr_adamw_plan_bytes(sizes, count, C.byref(nbytes)), "salr_adamw_plan_bytes")
     p_type, g_type = _float_type(params[0], "params"), _float_type(lists["grads"][0], "grads")
     at = _stream_here(dev, stream)
