@@ -288,16 +288,17 @@ __global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwArgs a) {
 // a share of its LDS (201 M bf16 parameters, float gradients and states, 28 KB
 // a workgroup: 8 a CU 937 us, 4 933, 3 901, 2 818, 1 1012; 53 M with 8-bit
 // states, 16 KB: 8 128, 6 122, 4 117, 3 130, 2 164).
-constexpr int kLdsBytes = 160 * 1024;
+// Two, four or six then hold 48 to 80 KB.
+constexpr int kLdsUnits = 128, kLdsUnit = 1280;  // a CU's LDS, as it is given out
 constexpr int kFlightBytes = 80 * 1024;
 
 template <class P, class G, bool S8, bool MASTER>
 void launch(const AdamwArgs& a, hipStream_t s) {
   constexpr int kLoads = kAdamwChunk * (int)(sizeof(G) + (S8 ? 2 : 8) + (MASTER ? 4 : sizeof(P)));
-  constexpr int kGroups = kFlightBytes / kLoads < 8 ? kFlightBytes / kLoads : 8;
-  static_assert(kGroups >= 2, "workgroups a CU");
+  constexpr int kGroups = kFlightBytes / kLoads & ~1;
+  static_assert(kGroups >= 2 && kGroups <= 8, "workgroups a CU");
   hipLaunchKernelGGL((adamw_kernel<P, G, S8, MASTER>), dim3((unsigned)a.n_chunks), dim3(kAdamwThreads),
-                     kLdsBytes / kGroups / 1024 * 1024, s, a);
+                     kLdsUnits / kGroups * kLdsUnit, s, a);
 }
 
 template <class P, bool MASTER>
