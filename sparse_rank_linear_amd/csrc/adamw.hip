@@ -6,8 +6,8 @@
 // largest / 448 (v spans twice the exponents of its root, which the format's
 // 2^-9 .. 448 would not hold).
 //
-// One workgroup per 2048 elements of a tensor, found in the plan's chunk
-// list; 8 consecutive elements a thread, so a float array moves 32 bytes and
+// One workgroup per chunk of a tensor (2048 or 4096 elements), found in the
+// plan's chunk list; 8 consecutive elements a thread, so a float array moves 32 bytes and
 // the codes 8 bytes a thread, and an 8-bit run is 32 lanes of one wave.
 // Bound by HBM: 24 bytes an element with float states, 12 with 8-bit ones
 // (bf16 parameters, float gradients, no master).
@@ -19,9 +19,7 @@
 namespace salr {
 namespace {
 
-constexpr int kAdamwThreads = 256;
 constexpr int kPer = 8;  // elements a thread
-static_assert(kAdamwThreads * kPer == kAdamwChunk, "one chunk per workgroup");
 constexpr int kRunLanes = 256 / kPer;
 constexpr float kTiny = 0x1p-100f;
 
@@ -215,7 +213,7 @@ struct Eight {
 
 // FULL: the chunk has all its elements.
 template <class P, class G, bool S8, bool MASTER, bool FULL>
-__device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwTensor& t, int64_t i) {
+__device__ __forceinline__ void adamw_elements(const AdamwArgs& a, const AdamwTensor& t, int64_t i) {
 #pragma clang fp contract(off)
   const int64_t run = i / 256;
   float decay = a.decay, rate = a.rate, gs = a.grad_scale, isb2 = a.inv_sqrt_bias2;
@@ -275,29 +273,31 @@ __device__ __forceinline__ void adamw_chunk(const AdamwArgs& a, const AdamwTenso
 }
 
 template <class P, class G, bool S8, bool MASTER>
-__global__ __launch_bounds__(kAdamwThreads) void adamw_kernel(AdamwArgs a) {
+__global__ __launch_bounds__(adamw_chunk(S8, MASTER) / kPer) void adamw_kernel(AdamwArgs a) {
+  constexpr int kChunk = adamw_chunk(S8, MASTER);
   const AdamwChunk ch = a.chunks[blockIdx.x];
   const AdamwTensor t = a.tensors[ch.tensor];
-  const int64_t base = (int64_t)ch.chunk * kAdamwChunk, i = base + threadIdx.x * kPer;
-  if (base + kAdamwChunk <= t.n) adamw_chunk<P, G, S8, MASTER, true>(a, t, i);
-  else adamw_chunk<P, G, S8, MASTER, false>(a, t, i);
+  const int64_t base = (int64_t)ch.chunk * kChunk, i = base + threadIdx.x * kPer;
+  if (base + kChunk <= t.n) adamw_elements<P, G, S8, MASTER, true>(a, t, i);
+  else adamw_elements<P, G, S8, MASTER, false>(a, t, i);
 }
 
 // Loads in flight a CU: more of them than about 80 KB open more DRAM pages
-// than it serves well, so the workgroups a CU holds are bounded, by asking for
-// a share of its LDS (201 M bf16 parameters, float gradients and states, 28 KB
-// a workgroup: 8 a CU 937 us, 4 933, 3 901, 2 818, 1 1012; 53 M with 8-bit
-// states, 16 KB: 8 128, 6 122, 4 117, 3 130, 2 164).
-// Two, four or six then hold 48 to 80 KB.
+// than it serves well, so the waves a CU holds are bounded, by asking for a
+// share of its LDS (201 M bf16 parameters, float gradients and states, 28 KB
+// of loads in 4 waves: 32 waves a CU 937 us, 16 933, 12 901, 8 818, 4 1012;
+// 53 M with 8-bit states, 16 KB: 32 waves 128, 24 122, 16 117, 12 130, 8
+// 164).  Eight, sixteen or twenty-four waves then load 48 to 80 KB.
 constexpr int kLdsUnits = 128, kLdsUnit = 1280;  // a CU's LDS, as it is given out
 constexpr int kFlightBytes = 80 * 1024;
 
 template <class P, class G, bool S8, bool MASTER>
 void launch(const AdamwArgs& a, hipStream_t s) {
-  constexpr int kLoads = kAdamwChunk * (int)(sizeof(G) + (S8 ? 2 : 8) + (MASTER ? 4 : sizeof(P)));
-  constexpr int kGroups = kFlightBytes / kLoads & ~1;
-  static_assert(kGroups >= 2 && kGroups <= 8, "workgroups a CU");
-  hipLaunchKernelGGL((adamw_kernel<P, G, S8, MASTER>), dim3((unsigned)a.n_chunks), dim3(kAdamwThreads),
+  constexpr int kThreads = adamw_chunk(S8, MASTER) / kPer;
+  constexpr int kFourWaves = 256 * kPer * (int)(sizeof(G) + (S8 ? 2 : 8) + (MASTER ? 4 : sizeof(P)));  // bytes
+  constexpr int kGroups = (kFlightBytes / kFourWaves & ~1) * 256 / kThreads;
+  static_assert(kGroups >= 1 && kGroups * kThreads <= 2048, "workgroups a CU");
+  hipLaunchKernelGGL((adamw_kernel<P, G, S8, MASTER>), dim3((unsigned)a.n_chunks), dim3(kThreads),
                      kLdsUnits / kGroups * kLdsUnit, s, a);
 }
 

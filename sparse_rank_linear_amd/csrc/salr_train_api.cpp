@@ -198,7 +198,9 @@ int salr_moe_combine_backward(const uint16_t* dY, const uint16_t* Ys, int64_t R,
 // AdamW: the plan's table is the tensor records, then the chunk list.
 namespace {
 
-static_assert(salr::kAdamwChunk % SALR_ADAMW_BLOCK == 0, "a chunk holds whole 8-bit runs");
+static_assert(salr::kAdamwSmallChunk % SALR_ADAMW_BLOCK == 0 && salr::adamw_chunk(true, true) % SALR_ADAMW_BLOCK == 0 &&
+                  salr::adamw_chunk(false, false) >= salr::kAdamwSmallChunk,
+              "a chunk holds whole 8-bit runs, and the small one sizes the table");
 
 size_t table_records_bytes(int32_t count) { return align_up((size_t)count * sizeof(salr::AdamwTensor), 256); }
 size_t table_bytes_for(int32_t count, int64_t chunks) {
@@ -253,18 +255,18 @@ int adamw_fill(const salr_adamw_tensor_t* t, int32_t count, int32_t p_type, int3
     }
     if (master) add(ranges, nw, q.master, n * 4);
     add(read, nr, q.g, n * gb);
-    for (int64_t c = 0; c < cdiv(q.n, salr::kAdamwChunk); ++c) *chunk++ = salr::AdamwChunk{i, (int32_t)c};
+    for (int64_t c = 0; c < cdiv(q.n, salr::adamw_chunk(state8, master)); ++c) *chunk++ = salr::AdamwChunk{i, (int32_t)c};
   }
   return overlaps(ranges, nw, read, nr) ? SALR_ERR_INVALID_ARG : SALR_OK;
 }
 
 // The chunks of `count` tensors, or -1.
 template <class F>
-int64_t adamw_chunks(int32_t count, F n) {
+int64_t adamw_chunks(int32_t count, int64_t chunk, F n) {
   int64_t chunks = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (n(i) < 0 || n(i) >= kMaxTensorElements) return -1;
-    chunks += cdiv(n(i), salr::kAdamwChunk);
+    chunks += cdiv(n(i), chunk);
     if (chunks > kMaxChunks) return -1;
   }
   return chunks;
@@ -276,7 +278,7 @@ extern "C" {
 
 int salr_adamw_plan_bytes(const int64_t* n, int32_t count, size_t* out) {
   if (!out || count < 0 || count > kMaxTensors || (count > 0 && !n)) return SALR_ERR_INVALID_ARG;
-  const int64_t chunks = adamw_chunks(count, [&](int32_t i) { return n[i]; });
+  const int64_t chunks = adamw_chunks(count, salr::kAdamwSmallChunk, [&](int32_t i) { return n[i]; });
   if (chunks < 0) return SALR_ERR_INVALID_ARG;
   *out = table_bytes_for(count, chunks);
   return SALR_OK;
@@ -287,10 +289,12 @@ int salr_adamw_plan(const salr_adamw_tensor_t* tensors, int32_t count, int32_t p
   if (!out || count < 0 || count > kMaxTensors || (count > 0 && !tensors)) return SALR_ERR_INVALID_ARG;
   if (!type_ok(p_type) || !type_ok(g_type)) return SALR_ERR_INVALID_ARG;
   if (state_type != SALR_STATE_F32 && state_type != SALR_STATE_8BIT) return SALR_ERR_INVALID_ARG;
-  const int64_t chunks = adamw_chunks(count, [&](int32_t i) { return tensors[i].n; });
-  if (chunks < 0) return SALR_ERR_INVALID_ARG;
+  const bool state8 = state_type == SALR_STATE_8BIT;
   bool master = false;
   for (int32_t i = 0; i < count && !master; ++i) master = tensors[i].n > 0 && tensors[i].master != nullptr;
+  const auto size = [&](int32_t i) { return tensors[i].n; };
+  if (adamw_chunks(count, salr::kAdamwSmallChunk, size) < 0) return SALR_ERR_INVALID_ARG;  // (as the table's size says)
+  const int64_t chunks = adamw_chunks(count, salr::adamw_chunk(state8, master), size);
   if (master && p_type != SALR_TYPE_BF16) return SALR_ERR_INVALID_ARG;
   const size_t bytes = table_bytes_for(count, chunks);
   unsigned char* host = new (std::nothrow) unsigned char[bytes];
@@ -298,7 +302,7 @@ int salr_adamw_plan(const salr_adamw_tensor_t* tensors, int32_t count, int32_t p
   int rc = host && ranges ? SALR_OK : SALR_ERR_UNSUPPORTED;
   if (rc == SALR_OK) {
     std::memset(host, 0, bytes);
-    rc = adamw_fill(tensors, count, p_type, g_type, state_type == SALR_STATE_8BIT, master, host, ranges);
+    rc = adamw_fill(tensors, count, p_type, g_type, state8, master, host, ranges);
   }
   delete[] ranges;
   // (every argument check above comes before the buffer's)

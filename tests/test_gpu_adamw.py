@@ -121,7 +121,7 @@ def _before(params, grads, st, bits):
     return [(_f64(p), _f64(g), *_states64(st, i, bits)) for i, (p, g) in enumerate(zip(src, grads))]
 
 
-SIZES = [1, 7, 8, 255, 256, 257, 2047, 2048, 2049, 0, 5000, 12345]
+SIZES = [1, 7, 8, 255, 256, 257, 2047, 2048, 2049, 0, 4095, 4096, 4097, 5000, 12345]
 
 
 @pytest.mark.parametrize("bits", [32, 8])
