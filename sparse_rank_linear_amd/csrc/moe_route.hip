@@ -16,7 +16,7 @@
 // Bound by the launch up to a few thousand rows, then by the issue of
 // instructions (16384 rows of 64 floats, top 6: 4.2 us, backward 4.1, where
 // reading and writing them takes 0.8 and 1.5; 16384 of 256, top 8: 8.7 and
-// 10.6).  A wave per row took 18.6 us for the first, float maxima (which
+// 9.7).  A wave per row took 18.6 us for the first, float maxima (which
 // quiet NaNs) and the library's exp 4.9.
 #include <hip/hip_runtime.h>
 
@@ -165,6 +165,11 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_backward_kernel(const
                                                                            Tl* dlogits) {
   constexpr int SLOTS = SALR_MOE_MAX_TOPK > LANES ? SALR_MOE_MAX_TOPK / LANES : 1;
   constexpr int BATCH = 4;  // choices handed round together
+  // From 8 logits a lane on, comparing each with every choice costs more than
+  // a row of LDS (rows of 16 lanes 16 banks apart).
+  constexpr bool SHARED = PER >= 8;
+  constexpr int kStride = LANES * PER + (LANES == 16 ? 16 : 0);
+  __shared__ float taken[SHARED ? kRouteThreads / LANES * kStride : 1];
   const int lane = threadIdx.x % LANES;
   const int64_t groups = (int64_t)gridDim.x * (kRouteThreads / LANES);
   for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES; t < T; t += groups) {
@@ -186,19 +191,27 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_backward_kernel(const
       up[q] = 0.f;
       in[q] = !renorm && e < E;
     }
-    if constexpr (LANES == 64) {
-      // (one row a wave: each choice is the wave's, and only one q's registers take it)
-      for (int j = 0; j < k; ++j) {
-        const int e = __builtin_amdgcn_readlane(id[0], j);
-        const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dw[0]), j));
-        if ((uint32_t)e >= (uint32_t)E) continue;
+    if constexpr (SHARED) {
+      // Each choice adds to its expert's place in LDS, one after the other
+      // (the same expert twice adds up in order); -0, which no sum of a +0
+      // and other values is, marks the places that no choice took.
+      volatile float* place = &taken[threadIdx.x / LANES * kStride];
 #pragma unroll
-        for (int q = 0; q < PER; ++q)
-          if (e / LANES == q) {
-            const bool hit = lane == e % LANES;
-            up[q] += hit ? d : 0.f;
-            in[q] = in[q] || hit;
+      for (int q = 0; q < PER; ++q) place[q * LANES + lane] = -0.f;
+      for (int j = 0; j < k; ++j) {
+#pragma unroll
+        for (int c = 0; c < SLOTS; ++c)
+          if (c * LANES + lane == j && (uint32_t)id[c] < (uint32_t)E) {
+            const float sum = place[id[c]];
+            place[id[c]] = (sum + 0.f) + dw[c];
           }
+        __builtin_amdgcn_wave_barrier();
+      }
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const float sum = place[q * LANES + lane];
+        in[q] = in[q] || __float_as_int(sum) != __float_as_int(-0.f);
+        up[q] = sum;
       }
     } else {
 #pragma unroll
