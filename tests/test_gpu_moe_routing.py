@@ -130,6 +130,28 @@ def test_route_backward(T, E, k, half):
         assert torch.equal(buf, got)
 
 
+@pytest.mark.parametrize("E,k", [(3, 3), (8, 8), (40, 32), (64, 6), (100, 32), (256, 9), (700, 32), (3000, 8)])
+def test_route_backward_any_ids(E, k):
+    """Choices of the caller's own: the same expert several times (its
+    gradients add up), and ids outside the experts, which take no part."""
+    import torch
+
+    srl = _srl()
+    rng = np.random.default_rng(E)
+    T = 21
+    x = rng.standard_normal((T, E)).astype(np.float32).astype(np.float64)
+    ids = rng.integers(0, max(2, E // 4), (T, k)).astype(np.int32)
+    far = rng.random((T, k)) < 0.2
+    ids[far] = rng.choice(np.array([-1, -7, E, E + 5, 2 ** 31 - 1, -2 ** 31]), far.sum()).astype(np.int32)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    dw[0] = 0.0                                         # (a chosen expert with no gradient is chosen all the same)
+    for renorm in (False, True):
+        want = orr.route_backward(x, ids, dw, renorm)
+        got = srl.moe_route_backward(_up(x), torch.from_numpy(ids).cuda(), _up(dw), renorm=renorm)
+        scale = np.abs(dw).sum(1, keepdims=True) * 2
+        assert (np.abs(got.double().cpu().numpy() - want) <= 512 * U * scale + 1e-38).all()
+
+
 def test_route_not_finite():
     """A NaN logit is never chosen and makes full-softmax weights NaN; with
     renorm the others stand; +inf is chosen first, its row's weights NaN."""
@@ -208,6 +230,15 @@ def test_dispatch_sort(T, k, E, kind):
         got = to_host_bits(Xs)
         assert np.array_equal(got[: off[-1]], xb[slots // k])
         assert (got[off[-1]:] == 0x40E0).all()           # rows behind the last stay (7.0)
+    # the sort alone, and without slots
+    _, soff, srows, sslots = srl.moe_dispatch(torch.from_numpy(ids).cuda(), E)
+    assert torch.equal(soff, goff) and torch.equal(srows, grows)
+    assert np.array_equal(sslots.cpu().numpy()[: off[-1]], slots)
+    d, o2, r2 = torch.from_numpy(ids).cuda(), torch.empty_like(goff), torch.empty_like(grows)
+    assert srl.lib().salr_moe_dispatch(d.data_ptr() or None, T, k, E, None, 0, o2.data_ptr(), r2.data_ptr() or None,
+                                       None, None, ws.data_ptr(), ws.numel(),
+                                       torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(o2, goff) and torch.equal(r2, grows)
 
 
 @pytest.mark.parametrize("D", [1, 3, 8, 40, 1000, 2048, 2056, 4099, 8192])
@@ -261,6 +292,46 @@ def test_dispatch_and_combine_columns(D):
         gy1, gw1 = srl.moe_combine_backward(to_dev(db), over, grows, dYs=over)
         assert torch.equal(gw1, gw)
         assert np.array_equal(to_host_bits(gy1)[live], db[slots // k])
+
+
+@pytest.mark.parametrize("T,k,D", [(70000, 4, 128), (140000, 2, 127), (9000, 1, 4096), (5000, 8, 1024), (3000, 12, 1000),
+                                   (70000, 2, 256)])
+def test_rows_of_many_megabytes(T, k, D):
+    """Gathered rows of 64 MB and more (read past the caches), against the
+    same sums in float64 on the device."""
+    import torch
+
+    srl = _srl()
+    say(f"many megabytes T={T} k={k} D={D}")
+    E = 7
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ids = torch.from_numpy(_ids(T, k, E, T)).cuda()
+    half = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    X, base, Ys = half(T, D), half(T, D), half(T * k, D)
+    assert Ys.numel() * 2 >= 64 << 20
+    w = torch.rand(T, k, generator=g, device="cuda")
+    Xs, off, rows, slots = srl.moe_dispatch(ids, E, X)
+    n = int(off[-1])
+    assert torch.equal(Xs[:n], X[slots[:n].long() // k])
+    Ys[n:] = NAN
+    w[rows < 0] = NAN
+    at = rows.clamp(min=0).long()
+    Y, dY = srl.moe_combine(Ys, rows, w, base=base), X
+    dYs, dw = srl.moe_combine_backward(dY, Ys, rows, w)
+    want, mag = base.double(), base.double().abs()
+    for j in range(k):
+        ok = (rows[:, j] >= 0)[:, None]
+        y = torch.where(ok, Ys[at[:, j]].double(), 0.0)
+        part = torch.where(ok, w[:, j, None].double(), 0.0) * y
+        want, mag = want + part, mag + part.abs()
+        dot = (dY.double() * y).sum(1)
+        tol = (D + 8) * U * (dY.double() * y).abs().sum(1)
+        assert ((dw[:, j].double() - dot).abs() <= tol).all()
+        d = torch.where(ok, w[:, j, None].double() * dY.double(), 0.0)
+        err = torch.where(ok, (dYs[at[:, j]].double() - d).abs(), 0.0)
+        assert (err <= (H + 2 * U) * d.abs() + 1e-38).all()
+    assert ((Y.double() - want).abs() <= (k + 3) * U * mag + H * want.abs() + 1e-38).all()
+    assert torch.count_nonzero(dYs[n:]) == 0
 
 
 def test_rows_outside_are_skipped():
