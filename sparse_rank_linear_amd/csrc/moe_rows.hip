@@ -161,11 +161,20 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeDispatchArgs
 
 // ---- rows ----
 
+// VEC bf16 values of a row, as wide as the row's length allows.
 template <int VEC>
-struct Piece;  // VEC bf16 values
+struct Piece;
 template <>
 struct Piece<8> {
   u32x4_t w;
+};
+template <>
+struct Piece<4> {
+  u32x2_t w;
+};
+template <>
+struct Piece<2> {
+  uint32_t w;
 };
 template <>
 struct Piece<1> {
@@ -186,25 +195,33 @@ __device__ __forceinline__ void store_piece(uint16_t* p, Piece<VEC> v) {
   if constexpr (NT) __builtin_nontemporal_store(v.w, q);
   else *q = v.w;
 }
-__device__ __forceinline__ void expand_piece(float* x, Piece<8> v) {
+template <int VEC>
+__device__ __forceinline__ void expand_piece(float* x, Piece<VEC> v) {
+  if constexpr (VEC == 1) {
+    x[0] = bf16_to_f32(v.w);
+  } else {
+    uint32_t w[VEC / 2];
+    __builtin_memcpy(w, &v, sizeof(v));
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    x[2 * c] = bf16_to_f32((uint16_t)v.w[c]);
-    x[2 * c + 1] = bf16_to_f32((uint16_t)(v.w[c] >> 16));
+    for (int c = 0; c < VEC / 2; ++c) {
+      x[2 * c] = bf16_to_f32((uint16_t)w[c]);
+      x[2 * c + 1] = bf16_to_f32((uint16_t)(w[c] >> 16));
+    }
   }
-}
-__device__ __forceinline__ void expand_piece(float* x, Piece<1> v) { x[0] = bf16_to_f32(v.w); }
-__device__ __forceinline__ Piece<8> round_piece8(const float* f) {
-  Piece<8> v;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    v.w[c] = (uint32_t)f32_to_bf16(f[2 * c]) | ((uint32_t)f32_to_bf16(f[2 * c + 1]) << 16);
-  return v;
 }
 template <int VEC>
 __device__ __forceinline__ Piece<VEC> round_piece(const float* f) {
-  if constexpr (VEC == 8) return round_piece8(f);
-  else return Piece<1>{f32_to_bf16(f[0])};
+  Piece<VEC> v;
+  if constexpr (VEC == 1) {
+    v.w = f32_to_bf16(f[0]);
+  } else {
+    uint32_t w[VEC / 2];
+#pragma unroll
+    for (int c = 0; c < VEC / 2; ++c)
+      w[c] = (uint32_t)f32_to_bf16(f[2 * c]) | ((uint32_t)f32_to_bf16(f[2 * c + 1]) << 16);
+    __builtin_memcpy(&v, w, sizeof(v));
+  }
+  return v;
 }
 
 // Sort and copy in one launch, after moe_count_kernel where there are more
@@ -421,6 +438,21 @@ __global__ __launch_bounds__(kCopyThreads) void moe_combine_backward_kernel(MoeC
   }
 }
 
+// The widest pieces that rows of D values start on (the pointers are 16-byte
+// aligned), and f with that as a template argument.
+inline int piece_width(int64_t D) { return D % 8 == 0 ? 8 : D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1; }
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+template <class F>
+void with_width(int vec, F f) {
+  if (vec == 8) f(Int<8>{});
+  else if (vec == 4) f(Int<4>{});
+  else if (vec == 2) f(Int<2>{});
+  else f(Int<1>{});
+}
+
 // Workgroups for n items, `per` each (more than kMaxBlocks: they loop).
 constexpr int64_t kMaxBlocks = int64_t(1) << 22;
 inline unsigned blocks_for(int64_t n, int64_t per) { return (unsigned)std::min(kMaxBlocks, (n + per - 1) / per); }
@@ -458,7 +490,7 @@ hipError_t launch_moe_dispatch(const MoeDispatchArgs& args, hipStream_t s) {
   int bits = 0;
   while ((1 << bits) < a.E) ++bits;
   const int64_t T = a.n / a.k;
-  const int vec = a.D % 8 == 0 ? 8 : 1;
+  const int vec = piece_width(a.D);
   const int64_t p = a.X ? a.D / vec : 0;
   if (a.n <= kOneLaunchSlots && a.E <= kFusedExperts) a.chunks = 1;
   else
@@ -469,10 +501,10 @@ hipError_t launch_moe_dispatch(const MoeDispatchArgs& args, hipStream_t s) {
       (a.X || fused_groups <= kFusedSortGroups)) {
     const dim3 grid((unsigned)fused_groups);
     const size_t lds = (size_t)a.E * 8;
-    if (vec == 8)
-      hipLaunchKernelGGL(moe_dispatch_kernel<8>, grid, dim3(kDispatchThreads), lds, s, a, T, G, bits, (int)p);
-    else
-      hipLaunchKernelGGL(moe_dispatch_kernel<1>, grid, dim3(kDispatchThreads), lds, s, a, T, G, bits, (int)p);
+    with_width(vec, [&](auto v) {
+      hipLaunchKernelGGL(moe_dispatch_kernel<decltype(v)::value>, grid, dim3(kDispatchThreads), lds, s, a, T, G, bits,
+                         (int)p);
+    });
     return hipGetLastError();
   }
   // (each wave's counters: 4 waves keep E = 4096 within 80 KB of LDS)
@@ -481,19 +513,14 @@ hipError_t launch_moe_dispatch(const MoeDispatchArgs& args, hipStream_t s) {
                      a, waves, bits);
   if (a.X && a.n > 0) {
     const dim3 grid(blocks_for(T * p, kCopyThreads));
-    if (vec == 8)
-      hipLaunchKernelGGL(moe_gather_kernel<8>, grid, dim3(kCopyThreads), 0, s, a, p, T * p);
-    else
-      hipLaunchKernelGGL(moe_gather_kernel<1>, grid, dim3(kCopyThreads), 0, s, a, p, T * p);
+    with_width(vec, [&](auto v) {
+      hipLaunchKernelGGL(moe_gather_kernel<decltype(v)::value>, grid, dim3(kCopyThreads), 0, s, a, p, T * p);
+    });
   }
   return hipGetLastError();
 }
 
 // f with the row batch, and with or without caching, as template arguments.
-template <int N>
-struct Int {
-  static constexpr int value = N;
-};
 template <class F>
 void with_form(int k, bool nt, F f) {
   const auto go = [&](auto kb) { nt ? f(kb, Int<1>{}) : f(kb, Int<0>{}); };
@@ -516,21 +543,20 @@ constexpr int64_t kStreamRowBytes = int64_t(64) << 20;
 
 hipError_t launch_moe_combine(const MoeCombineArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  const bool vec = a.D % 8 == 0;
-  const int64_t p = vec ? a.D / 8 : a.D, parts = (p + 63) / 64;
+  const int vec = piece_width(a.D);
+  const int64_t p = a.D / vec, parts = (p + 63) / 64;
   const dim3 threads(kCopyThreads);
   with_form(a.k, a.T * a.k * a.D * 2 >= kStreamRowBytes, [&](auto kb, auto nt) {
     constexpr int KB = decltype(kb)::value;
     constexpr bool NT = decltype(nt)::value;
-    if (!vec) {
-      hipLaunchKernelGGL((moe_combine_kernel<1, KB, NT, false>), dim3(blocks_for(a.T * p, kCopyThreads)), threads, 0, s,
-                         a, 1, (int)p, a.T * p);
-    } else if (4 * p >= 3 * 64 * parts) {  // (waves at least three quarters full)
+    if (vec == 8 && 4 * p >= 3 * 64 * parts) {  // (waves at least three quarters full)
       hipLaunchKernelGGL((moe_combine_kernel<8, KB, NT, true>), dim3(blocks_for(a.T * parts, kCopyThreads / 64)),
                          threads, 0, s, a, (int)parts, 64, a.T * parts);
     } else {
-      hipLaunchKernelGGL((moe_combine_kernel<8, KB, NT, false>), dim3(blocks_for(a.T * p, kCopyThreads)), threads, 0, s,
-                         a, 1, (int)p, a.T * p);
+      with_width(vec, [&](auto v) {
+        hipLaunchKernelGGL((moe_combine_kernel<decltype(v)::value, KB, NT, false>),
+                           dim3(blocks_for(a.T * p, kCopyThreads)), threads, 0, s, a, 1, (int)p, a.T * p);
+      });
     }
   });
   return hipGetLastError();
@@ -538,18 +564,21 @@ hipError_t launch_moe_combine(const MoeCombineArgs& a, hipStream_t s) {
 
 hipError_t launch_moe_combine_backward(const MoeCombineArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  const bool vec = a.D % 8 == 0;
-  const int p = (int)(vec ? a.D / 8 : a.D);
+  const int vec = piece_width(a.D);
+  const int p = (int)(a.D / vec);
   const dim3 threads(kCopyThreads);
   with_form(a.k, a.T * a.k * a.D * 2 >= kStreamRowBytes, [&](auto kb, auto nt) {
     constexpr int KB = decltype(kb)::value;
     constexpr bool NT = decltype(nt)::value;
-    if (!vec)
-      hipLaunchKernelGGL((moe_combine_backward_kernel<1, 256, KB, NT>), dim3(blocks_for(a.T, 1)), threads, 0, s, a, p);
-    else if (p > kWavePieces)
-      hipLaunchKernelGGL((moe_combine_backward_kernel<8, 256, KB, NT>), dim3(blocks_for(a.T, 1)), threads, 0, s, a, p);
-    else
-      hipLaunchKernelGGL((moe_combine_backward_kernel<8, 64, KB, NT>), dim3(blocks_for(a.T, 4)), threads, 0, s, a, p);
+    with_width(vec, [&](auto v) {
+      constexpr int VEC = decltype(v)::value;
+      if (p > kWavePieces)
+        hipLaunchKernelGGL((moe_combine_backward_kernel<VEC, 256, KB, NT>), dim3(blocks_for(a.T, 1)), threads, 0, s, a,
+                           p);
+      else
+        hipLaunchKernelGGL((moe_combine_backward_kernel<VEC, 64, KB, NT>), dim3(blocks_for(a.T, 4)), threads, 0, s, a,
+                           p);
+    });
   });
   return hipGetLastError();
 }

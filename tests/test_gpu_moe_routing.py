@@ -241,7 +241,7 @@ def test_dispatch_sort(T, k, E, kind):
     assert torch.equal(o2, goff) and torch.equal(r2, grows)
 
 
-@pytest.mark.parametrize("D", [1, 3, 8, 40, 1000, 2048, 2056, 4099, 8192])
+@pytest.mark.parametrize("D", [1, 2, 3, 4, 8, 36, 40, 1000, 1002, 2044, 2048, 2056, 4099, 8192])
 def test_dispatch_and_combine_columns(D):
     """Every width, also odd ones, in few and many tokens."""
     import torch
