@@ -78,9 +78,11 @@ __device__ __forceinline__ uint64_t same_id(uint32_t id, int bits) {
 }
 
 // Adds the chunks' counts: all[e] over every chunk, first[e] over those
-// before `chunk`.  Threads share an expert's chunks as far as they go round.
+// before `chunk` (both at e << shift).  Threads share an expert's chunks as far
+// as they go round.
 template <int THREADS>
-__device__ __forceinline__ void add_chunks(const MoeDispatchArgs& a, int chunk, uint32_t* all, uint32_t* first) {
+__device__ __forceinline__ void add_chunks(const MoeDispatchArgs& a, int chunk, int shift, uint32_t* all,
+                                           uint32_t* first) {
   const int groups = max(1, THREADS / a.E), g = (int)threadIdx.x / a.E;
   for (int e = (int)threadIdx.x - g * a.E; e < a.E && g < groups; e += THREADS) {
     uint32_t sum = 0, before = 0;
@@ -90,8 +92,8 @@ __device__ __forceinline__ void add_chunks(const MoeDispatchArgs& a, int chunk, 
       sum += h;
       before += c < chunk ? h : 0u;
     }
-    if (sum) atomicAdd(&all[e], sum);
-    if (before) atomicAdd(&first[e], before);
+    if (sum) atomicAdd(&all[e << shift], sum);
+    if (before) atomicAdd(&first[e << shift], before);
   }
 }
 
@@ -107,7 +109,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeDispatchArgs
   for (int e = tid; e < a.E * (waves + 1); e += kSortThreads) sm[e] = 0;
   __syncthreads();
   // next[0][e]: all slots of e; first[e]: those of the chunks before
-  add_chunks<kSortThreads>(a, blockIdx.x, next, first);
+  add_chunks<kSortThreads>(a, blockIdx.x, 0, next, first);
   __syncthreads();
   uint32_t run = 0;
   for (int e0 = 0; e0 < a.E; e0 += kSortThreads) {
@@ -226,17 +228,18 @@ __device__ __forceinline__ Piece<VEC> round_piece(const float* f) {
 
 // Sort and copy in one launch, after moe_count_kernel where there are more
 // chunks than one: the workgroup's tokens are [G * blockIdx.x, + G), G * k <=
-// 64.  LDS: all[E] (slots of e), then first[E] (the row where the
-// workgroup's slots of e begin).
+// 64.  LDS: all (slots of each expert), then first (in the end the row where the
+// workgroup's slots of e begin), 1 << shift counters an expert each, which a
+// wave's lanes share out: few experts would make them queue at one.
 template <int VEC>
 __global__ __launch_bounds__(kDispatchThreads) void moe_dispatch_kernel(MoeDispatchArgs a, int64_t T, int G, int bits,
-                                                                    int pieces) {
+                                                                        int shift, int pieces) {
   extern __shared__ uint32_t sm[];
   __shared__ uint32_t part[kDispatchThreads / 64];
   __shared__ int32_t row[64];
   uint32_t* all = sm;
-  uint32_t* first = sm + a.E;
-  const int tid = threadIdx.x;
+  uint32_t* first = sm + (a.E << shift);
+  const int tid = threadIdx.x, mine_of = tid & ((1 << shift) - 1);
   const int64_t t0 = (int64_t)blockIdx.x * G, t1 = min(t0 + G, T);
   const int s0 = (int)(t0 * a.k), s1 = (int)(t1 * a.k);
   // (what does not wait for the sort is requested before it, and the barriers
@@ -245,22 +248,29 @@ __global__ __launch_bounds__(kDispatchThreads) void moe_dispatch_kernel(MoeDispa
   const int total = a.X ? (int)(t1 - t0) * pieces : 0;
   Piece<VEC> ahead;
   if (tid < total) ahead = load_piece<VEC>(a.X + t0 * a.D + (int64_t)tid * VEC);
-  for (int e = tid; e < 2 * a.E; e += kDispatchThreads) sm[e] = 0;
+  for (int e = tid; e < 2 * (a.E << shift); e += kDispatchThreads) sm[e] = 0;
   lds_barrier();
   if (a.chunks == 1) {
-    for (int s = tid; s < a.n; s += kDispatchThreads) {
-      const uint32_t id = (uint32_t)a.ids[s];
-      if (id < (uint32_t)a.E) {
-        atomicAdd(&all[id], 1u);
-        if (s < s0) atomicAdd(&first[id], 1u);
+    // (four ids requested at a time; one atomic each: those from the
+    // workgroup's slots on go to `all`, which takes the others after)
+    for (int base = tid; base < a.n; base += 4 * kDispatchThreads) {
+      uint32_t id[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int s = base + q * kDispatchThreads;
+        id[q] = s < a.n ? (uint32_t)a.ids[s] : 0xFFFFFFFFu;
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (id[q] < (uint32_t)a.E)
+          atomicAdd(&(base + q * kDispatchThreads < s0 ? first : all)[(id[q] << shift) + mine_of], 1u);
     }
   } else {
     const int chunk = s0 / a.chunk;
-    add_chunks<kDispatchThreads>(a, chunk, all, first);
+    add_chunks<kDispatchThreads>(a, chunk, shift, all, first);
     for (int s = chunk * a.chunk + tid; s < s0; s += kDispatchThreads) {
       const uint32_t id = (uint32_t)a.ids[s];
-      if (id < (uint32_t)a.E) atomicAdd(&first[id], 1u);
+      if (id < (uint32_t)a.E) atomicAdd(&first[(id << shift) + mine_of], 1u);
     }
   }
   lds_barrier();
@@ -268,9 +278,14 @@ __global__ __launch_bounds__(kDispatchThreads) void moe_dispatch_kernel(MoeDispa
   for (int e0 = 0; e0 < a.E; e0 += kDispatchThreads) {
     const int e = e0 + tid;
     uint32_t total;
-    const uint32_t off = run + block_prefix<kDispatchThreads>(e < a.E ? all[e] : 0u, part, &total);
+    uint32_t before = 0, rest = 0;
+    for (int c = e << shift; e < a.E && c < (e + 1) << shift; ++c) {
+      before += first[c];
+      rest += all[c];
+    }
+    const uint32_t off = run + block_prefix<kDispatchThreads>(a.chunks == 1 ? before + rest : rest, part, &total);
     if (e < a.E) {
-      first[e] += off;
+      first[e << shift] = before + off;
       if (blockIdx.x == 0) a.off[e] = (int32_t)off;
     }
     run += total;
@@ -281,7 +296,7 @@ __global__ __launch_bounds__(kDispatchThreads) void moe_dispatch_kernel(MoeDispa
     const int s = s0 + tid;
     const bool ok = mine < (uint32_t)a.E;
     const uint64_t m = same_id(ok ? mine : 0u, bits) & __ballot(ok);
-    const int32_t r = ok ? (int32_t)(first[mine] + (uint32_t)__popcll(m & ((1ull << tid) - 1ull))) : -1;
+    const int32_t r = ok ? (int32_t)(first[mine << shift] + (uint32_t)__popcll(m & ((1ull << tid) - 1ull))) : -1;
     row[tid] = r;
     if (s < s1) a.rows[s] = r;
     if (ok && a.slots) a.slots[r] = s;
@@ -466,9 +481,10 @@ int32_t moe_sort_chunk(int64_t n) {
 
 // Which form of the dispatch, and how many tokens a workgroup takes in the
 // first two (measured in us on random experts, sort and copy unless said):
-//  - one launch up to 8192 slots: every workgroup reads all of them (1024
-//    tokens, 6 of 64, 2048 columns: 9.1; counted first 9.9; at 12288 slots
-//    15.5 against 14.8);
+//  - one launch up to 12288 slots: every workgroup reads all of them (of 64
+//    experts, 1024 columns: 4092 slots 5.4, counted first 7.6; 12288 8.7 and
+//    9.9; 16380 11.2 and 11.8, but of 8 experts, 4096 columns 36.5 and 35.3;
+//    of 2000 experts, 1024 columns: 12000 slots 10.5, counted and placed 19.3);
 //  - counted first while the chunks' counts are few enough for every
 //    workgroup to add up (16384 tokens, 2 of 256, 512 columns: 13.0; placed in
 //    a launch of their own 15.7; 8 of 128, 1024 columns: 56.5 and 61.2),
@@ -477,9 +493,8 @@ int32_t moe_sort_chunk(int64_t n) {
 //  - else counted, placed and copied in a launch each.
 // A workgroup's share of the sort does not shrink with its tokens, so there
 // are about kDispatchGroups workgroups (two a CU), not more (1000 tokens, 2
-// of 8, 4096 columns: 7.5; with a workgroup a token 9.6).
-constexpr int64_t kOneLaunchSlots = 8192;
-constexpr int kFusedExperts = 1024;        // (their counters: 8 KB of LDS)
+// of 8, 4096 columns: 7.5, with a workgroup a token 9.6; 6.0 since).
+constexpr int64_t kOneLaunchSlots = 12288;
 constexpr int64_t kFusedTable = 16384;     // counts
 constexpr int64_t kFusedSlots = 1 << 20;   // (a chunk is then 2^14 slots, read by each of its workgroups)
 constexpr int64_t kFusedSortGroups = 1024;
@@ -492,18 +507,20 @@ hipError_t launch_moe_dispatch(const MoeDispatchArgs& args, hipStream_t s) {
   const int64_t T = a.n / a.k;
   const int vec = piece_width(a.D);
   const int64_t p = a.X ? a.D / vec : 0;
-  if (a.n <= kOneLaunchSlots && a.E <= kFusedExperts) a.chunks = 1;
+  if (a.n <= kOneLaunchSlots) a.chunks = 1;
   else
     hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)a.chunks), dim3(kSortThreads), (size_t)a.E * 4, s, a);
   const int G = (int)std::min<int64_t>(64 / a.k, std::max<int64_t>(1, (T + kDispatchGroups - 1) / kDispatchGroups));
   const int64_t fused_groups = std::max<int64_t>(1, (T + G - 1) / G);
-  if (a.n <= kFusedSlots && a.E <= kFusedExperts && (int64_t)a.chunks * a.E <= kFusedTable &&
+  if (a.n <= kFusedSlots && (int64_t)a.chunks * a.E <= kFusedTable &&
       (a.X || fused_groups <= kFusedSortGroups)) {
     const dim3 grid((unsigned)fused_groups);
-    const size_t lds = (size_t)a.E * 8;
+    // (up to 64 counters, one a bank, for few experts; chunks leave few ids to count)
+    const int shift = a.chunks == 1 ? std::min(3, std::max(0, 6 - bits)) : 0;
+    const size_t lds = ((size_t)a.E << shift) * 8;
     with_width(vec, [&](auto v) {
       hipLaunchKernelGGL(moe_dispatch_kernel<decltype(v)::value>, grid, dim3(kDispatchThreads), lds, s, a, T, G, bits,
-                         (int)p);
+                         shift, (int)p);
     });
     return hipGetLastError();
   }

@@ -197,7 +197,7 @@ def _want_dispatch(ids, E):
 
 # T, k, E: no token, one, around the sizes where the work is cut, many experts
 DISPATCH = [(0, 2, 8), (1, 1, 1), (1, 2, 8), (1, 32, 64), (16, 2, 8), (16, 6, 64), (63, 1, 3), (64, 1, 64), (65, 1, 2),
-            (341, 3, 5), (512, 2, 8), (683, 3, 60), (1024, 1, 4096), (1025, 1, 1024), (2047, 2, 1025), (2049, 2, 8),
+            (341, 3, 5), (512, 2, 8), (683, 3, 60), (2047, 8, 3), (2731, 6, 2), (8192, 2, 1), (5462, 3, 33), (1024, 1, 4096), (1025, 1, 1024), (2047, 2, 1025), (2049, 2, 8),
             (4099, 6, 64), (11000, 6, 64), (16384, 8, 256), (70001, 1, 2), (33000, 3, 4096),
             (8192, 8, 64), (8192, 8, 65), (40000, 2, 1000)]
 
