@@ -4,9 +4,10 @@ SALR (Sparsity-Aware Low-Rank Representation) serves a linear layer as
 Y = X W_s^T + (X A_cat) B_cat: W_s is the frozen weight after a static
 per-row magnitude prune, stored as a bitmap plus packed bf16 values, and
 A_cat / B_cat stack the truncated-SVD residual adapter with the LoRA
-adapters.  Encode, forward and the adapter backward run in hand-written gfx950 HIP kernels behind
-the C ABI of include/salr.h (libsalr.so); this package only marshals
-arguments (binding.py) and draws synthetic inputs (synth.py).
+adapters.  Encode, forward, the adapter backward, grouped experts with their
+router, dispatch and combine, and the AdamW step run in hand-written gfx950
+HIP kernels behind the C ABI of include/salr.h (libsalr.so); this package only
+marshals arguments (binding.py) and draws synthetic inputs (synth.py).
 """
 
 from .binding import (  # noqa: F401

@@ -777,29 +777,31 @@ MOE_MAX_TOPK = 32
 ADAMW_BLOCK = 256
 
 
-_TORCH = None
+# (These calls take a few us, so what they look up is held here: an import
+# statement or a stream object in each would be felt.)
+_TORCH = _TORCH_C = None
+_FLOAT_TYPES = {}
 
 
 def _torch():
-    """The torch module (these calls take a few us: an import statement in
-    each helper would be felt)."""
-    global _TORCH
+    """The torch module."""
+    global _TORCH, _TORCH_C
     if _TORCH is None:
         import torch
 
-        _TORCH = torch
+        _FLOAT_TYPES.update({torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32})
+        _TORCH, _TORCH_C = torch, torch._C
     return _TORCH
 
 
-def _stream_here(dev, stream):
-    """The current stream of `dev` as an address where a call can run as
-    things are; None where the current device or stream has to change first
-    (or the call cannot run): the calls then run themselves inside _Place.
-    (torch.cuda.current_stream builds a stream object each time, 1.9 us of a
-    9 us call.)"""
-    c = _torch()._C
-    if stream is None and dev.type == "cuda" and dev.index == c._cuda_getDevice():
-        return c._cuda_getCurrentRawStream(dev.index)
+def _stream_here(index, stream):
+    """The current stream of device `index` as an address where a call can run
+    as things are; None where the current device or stream has to change
+    first (or, without a device, it cannot run): the calls then run themselves
+    inside _Place.  (torch.cuda.current_stream builds a stream object each
+    time, 1.9 us of a 9 us call.)"""
+    if stream is None and index is not None and index == _TORCH_C._cuda_getDevice():
+        return _TORCH_C._cuda_getCurrentRawStream(index)
     return None
 
 
@@ -825,25 +827,24 @@ class _Place:
         return False
 
 
-def _ptr(t, name, dtype, shape, dev):
-    """The address of tensor t after checking it (an empty one: None)."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev.index:
-        return t.data_ptr() or None
+def _ptr(t, name, dtype, shape, index):
+    """The address of tensor t on device `index` after checking it."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev} (is on {t.device})")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index} (is on {t.device})")
     raise ValueError(f"{name} must be contiguous")
 
 
 def _float_type(t, name):
-    if t.dtype is _torch().float32:
-        return TYPE_F32
-    if t.dtype is _torch().bfloat16:
-        return TYPE_BF16
-    raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+    code = _FLOAT_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+    return code
 
 
 def moe_route(logits, k: int, renorm: bool = True, ids=None, weights=None, stream=None):
@@ -856,7 +857,8 @@ def moe_route(logits, k: int, renorm: bool = True, ids=None, weights=None, strea
         raise ValueError("logits must be [T][E]")
     T, E = logits.shape
     dev, shape = logits.device, (T, k)
-    at = _stream_here(dev, stream)
+    index = dev.index
+    at = _stream_here(index, stream)
     if at is None:
         with _Place(dev, stream):
             return moe_route(logits, k, renorm, ids, weights)
@@ -864,9 +866,9 @@ def moe_route(logits, k: int, renorm: bool = True, ids=None, weights=None, strea
         ids = torch.empty(shape, dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty(shape, dtype=torch.float32, device=dev)
-    _check(_lib().salr_moe_route(_ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"),
-                                 T, E, k, bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
-                                 _ptr(weights, "weights", torch.float32, shape, dev), at),
+    _check(_lib().salr_moe_route(_ptr(logits, "logits", logits.dtype, (T, E), index), _float_type(logits, "logits"),
+                                 T, E, k, bool(renorm), _ptr(ids, "ids", torch.int32, shape, index),
+                                 _ptr(weights, "weights", torch.float32, shape, index), at),
            "salr_moe_route")
     return ids, weights
 
@@ -879,17 +881,18 @@ def moe_route_backward(logits, ids, dweights, renorm: bool = True, dlogits=None,
         raise ValueError("logits must be [T][E] and ids [T][k]")
     T, E = logits.shape
     dev, shape = logits.device, (T, ids.shape[1])
-    at = _stream_here(dev, stream)
+    index = dev.index
+    at = _stream_here(index, stream)
     if at is None:
         with _Place(dev, stream):
             return moe_route_backward(logits, ids, dweights, renorm, dlogits)
     if dlogits is None:
         dlogits = torch.empty_like(logits)
     _check(_lib().salr_moe_route_backward(
-        _ptr(logits, "logits", logits.dtype, (T, E), dev), _float_type(logits, "logits"), T, E, shape[1],
-        bool(renorm), _ptr(ids, "ids", torch.int32, shape, dev),
-        _ptr(dweights, "dweights", torch.float32, shape, dev),
-        _ptr(dlogits, "dlogits", logits.dtype, (T, E), dev), at), "salr_moe_route_backward")
+        _ptr(logits, "logits", logits.dtype, (T, E), index), _float_type(logits, "logits"), T, E, shape[1],
+        bool(renorm), _ptr(ids, "ids", torch.int32, shape, index),
+        _ptr(dweights, "dweights", torch.float32, shape, index),
+        _ptr(dlogits, "dlogits", logits.dtype, (T, E), index), at), "salr_moe_route_backward")
     return dlogits
 
 
@@ -914,7 +917,8 @@ def moe_dispatch(ids, E: int, X=None, Xs=None, offsets=None, rows=None, slots=No
         raise ValueError("ids must be [T][k]")
     T, k = ids.shape
     n, D, dev = T * k, 0, ids.device
-    at = _stream_here(dev, stream)
+    index = dev.index
+    at = _stream_here(index, stream)
     if at is None:
         with _Place(dev, stream):
             return moe_dispatch(ids, E, X, Xs, offsets, rows, slots, ws)
@@ -931,18 +935,18 @@ def moe_dispatch(ids, E: int, X=None, Xs=None, offsets=None, rows=None, slots=No
         D = X.shape[1]
         if Xs is None:
             Xs = torch.empty((n, D), dtype=torch.bfloat16, device=dev)
-        x = _ptr(X, "X", torch.bfloat16, (T, D), dev)
-        xs = _ptr(Xs, "Xs", torch.bfloat16, (n, D), dev)
+        x = _ptr(X, "X", torch.bfloat16, (T, D), index)
+        xs = _ptr(Xs, "Xs", torch.bfloat16, (n, D), index)
     elif Xs is not None:
         raise ValueError("Xs needs X")
     if ws is None:
         ws = torch.empty(moe_dispatch_ws_bytes(T, k, E), dtype=torch.uint8, device=dev)
     elif ws.device != dev:
         raise ValueError(f"ws must be on {dev} (is on {ws.device})")
-    _check(_lib().salr_moe_dispatch(_ptr(ids, "ids", torch.int32, (T, k), dev), T, k, E, x, D,
-                                    _ptr(offsets, "offsets", torch.int32, (E + 1,), dev),
-                                    _ptr(rows, "rows", torch.int32, (T, k), dev),
-                                    _ptr(slots, "slots", torch.int32, (n,), dev), xs, ws.data_ptr(),
+    _check(_lib().salr_moe_dispatch(_ptr(ids, "ids", torch.int32, (T, k), index), T, k, E, x, D,
+                                    _ptr(offsets, "offsets", torch.int32, (E + 1,), index),
+                                    _ptr(rows, "rows", torch.int32, (T, k), index),
+                                    _ptr(slots, "slots", torch.int32, (n,), index), xs, ws.data_ptr(),
                                     ws.numel() * ws.element_size(), at), "salr_moe_dispatch")
     return Xs, offsets, rows, slots
 
@@ -953,17 +957,18 @@ def _combine(Ys, rows, weights, base, Y, stream):
         raise ValueError("the rows' values must be [R][D] and rows [T][k]")
     (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
     bf16 = torch.bfloat16
-    at = _stream_here(dev, stream)
+    index = dev.index
+    at = _stream_here(index, stream)
     if at is None:
         with _Place(dev, stream):
             return _combine(Ys, rows, weights, base, Y, None)
     if Y is None:
         Y = torch.empty((T, D), dtype=bf16, device=dev)
     _check(_lib().salr_moe_combine(
-        _ptr(Ys, "the rows' values", bf16, (R, D), dev), R, _ptr(rows, "rows", torch.int32, (T, k), dev),
-        None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev),
-        None if base is None else _ptr(base, "base", bf16, (T, D), dev), T, k, D,
-        _ptr(Y, "the output", bf16, (T, D), dev), at), "salr_moe_combine")
+        _ptr(Ys, "the rows' values", bf16, (R, D), index), R, _ptr(rows, "rows", torch.int32, (T, k), index),
+        None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), index),
+        None if base is None else _ptr(base, "base", bf16, (T, D), index), T, k, D,
+        _ptr(Y, "the output", bf16, (T, D), index), at), "salr_moe_combine")
     return Y
 
 
@@ -990,7 +995,8 @@ def moe_combine_backward(dY, Ys, rows, weights=None, dYs=None, dweights=None, st
         raise ValueError("Ys must be [R][D] and rows [T][k]")
     (R, D), (T, k), dev = Ys.shape, rows.shape, Ys.device
     bf16 = torch.bfloat16
-    at = _stream_here(dev, stream)
+    index = dev.index
+    at = _stream_here(index, stream)
     if at is None:
         with _Place(dev, stream):
             return moe_combine_backward(dY, Ys, rows, weights, dYs, dweights)
@@ -999,10 +1005,10 @@ def moe_combine_backward(dY, Ys, rows, weights=None, dYs=None, dweights=None, st
     if dweights is None:
         dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
     _check(_lib().salr_moe_combine_backward(
-        _ptr(dY, "dY", bf16, (T, D), dev), _ptr(Ys, "Ys", bf16, (R, D), dev), R,
-        _ptr(rows, "rows", torch.int32, (T, k), dev),
-        None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), dev), T, k, D,
-        _ptr(dYs, "dYs", bf16, (R, D), dev), _ptr(dweights, "dweights", torch.float32, (T, k), dev), at),
+        _ptr(dY, "dY", bf16, (T, D), index), _ptr(Ys, "Ys", bf16, (R, D), index), R,
+        _ptr(rows, "rows", torch.int32, (T, k), index),
+        None if weights is None else _ptr(weights, "weights", torch.float32, (T, k), index), T, k, D,
+        _ptr(dYs, "dYs", bf16, (R, D), index), _ptr(dweights, "dweights", torch.float32, (T, k), index), at),
         "salr_moe_combine_backward")
     return dYs, dweights
 
@@ -1090,7 +1096,8 @@ def adamw_plan(params, grads, m, v, m_scale=None, v_scale=None, master=None, str
     sizes = (C.c_int64 * count)(*size)
     _check(_lib().salr_adamw_plan_bytes(sizes, count, C.byref(nbytes)), "salr_adamw_plan_bytes")
     p_type, g_type = _float_type(params[0], "params"), _float_type(lists["grads"][0], "grads")
-    at = _stream_here(dev, stream)
+    index = dev.index
+    at = _stream_here(index, stream)
     if at is None:
         with _Place(dev, stream):
             return adamw_plan(**lists)
@@ -1113,11 +1120,12 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     step, lr and grad_scale (for captured graphs)."""
     torch = _torch()
     args, dev = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale), plan.device
-    at = _stream_here(dev, stream)
+    index = dev.index
+    at = _stream_here(index, stream)
     if at is None:
         with _Place(dev, stream):
             return adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, dyn)
-    d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (4,), dev)
+    d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (4,), index)
     _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, at), "salr_adamw_step")
 
 
