@@ -51,6 +51,8 @@ def route_backward(logits, ids, dweights, renorm: bool):
             if 0 <= e < E:
                 up[e] += float(d)
                 chosen[e] = True
+        if not chosen.any():                       # zeros, whatever the logits are
+            continue
         inside = chosen if renorm else np.ones(E, dtype=bool)
         top = np.max(x[t][inside], initial=-np.inf)
         if top == -np.inf:

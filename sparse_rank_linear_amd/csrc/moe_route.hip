@@ -69,6 +69,12 @@ __device__ __forceinline__ float group_sum(float v) {
   }));
 }
 
+template <int LANES>
+__device__ __forceinline__ bool group_any(bool v) {
+  const uint64_t m = __ballot(v);
+  return LANES == 64 ? m != 0 : ((m >> (threadIdx.x & 63 & ~(LANES - 1))) & ((1ull << (LANES & 63)) - 1)) != 0;
+}
+
 // Logits as integers in the same order (-0 as 0, NaN as -inf): their maxima
 // take one instruction each, where those of floats also quiet NaNs.
 constexpr int kLeast = (int)0x807FFFFF;  // order_of(-inf)
@@ -239,10 +245,15 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_backward_kernel(const
     for (int q = 0; q < PER; ++q) best = max(best, in[q] ? order_of(l[q]) : kLeast);
     best = group_max<LANES>(best);
     const float top = value_of(best);
+    // (a row without any choice gets zeros whatever its logits are, NaN too)
+    bool any = false;
+#pragma unroll
+    for (int c = 0; c < SLOTS; ++c) any = any || (uint32_t)id[c] < (uint32_t)E;
+    const bool live = group_any<LANES>(any) && best > kLeast;
     float total = 0.f, c = 0.f;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      l[q] = in[q] && best > kLeast ? exp_down(l[q] - top) : 0.f;
+      l[q] = in[q] && live ? exp_down(l[q] - top) : 0.f;
       total += l[q];
       c += l[q] * up[q];
     }

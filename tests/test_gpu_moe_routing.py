@@ -486,3 +486,33 @@ def test_binding_refusals():
         srl.moe_combine(h, i, torch.zeros(4, 2))
     with pytest.raises(srl.SalrError, match="INVALID_ARG"):
         srl.moe_combine(h[:4], i, Y=h[:4])
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 6), (100, 4), (256, 32), (700, 8), (4096, 5)])
+@pytest.mark.parametrize("half", [False, True], ids=["f32", "bf16"])
+def test_route_backward_rows_without_ids(E, k, half):
+    """A row none of whose ids is an expert gets zeros, also where its logits
+    are NaN or infinite (a dropped token's are whatever was left there); the
+    rows beside it are what they are without it."""
+    import torch
+
+    srl = _srl()
+    rng = np.random.default_rng(E)
+    T = 13
+    x = _bf16(rng.standard_normal((T, E)))[0]
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    dead = [1, 2, 4, 7, 8, 12]
+    ids[dead] = rng.choice(np.array([-1, -2 ** 31, E, 2 ** 31 - 1]), (len(dead), k)).astype(np.int32)
+    clean = [srl.moe_route_backward(_up(x, half), torch.from_numpy(ids).cuda(), _up(dw), renorm=r)
+             for r in (False, True)]
+    x[1, 0] = x[2, E - 1] = x[4, E // 2] = NAN
+    x[7, 1], x[8, E - 1] = INF, INF
+    x[8, 0], x[12] = NAN, NAN
+    dw[dead] = NAN
+    for renorm in (False, True):
+        assert (orr.route_backward(x, ids, np.where(ids < 0, 0, dw), renorm)[dead] == 0).all()
+        got = srl.moe_route_backward(_up(x, half), torch.from_numpy(ids).cuda(), _up(dw), renorm=renorm)
+        assert torch.count_nonzero(got[dead]) == 0
+        alive = [t for t in range(T) if t not in dead]
+        assert torch.isfinite(got).all() and torch.equal(got[alive], clean[renorm][alive])

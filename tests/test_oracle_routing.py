@@ -145,3 +145,13 @@ def test_e4m3_codes():
     down = np.array([table[:127][table[:127] <= q][-1] for q in down]) * scale
     assert (np.abs(down - np.abs(x)) > np.maximum(np.abs(x) * 2.0 ** -4, scale * 2.0 ** -10) * (1 + 1e-12)).any()
     assert oa.encode(np.full(3, 1e-31))[1][0] == 0.0
+
+
+def test_route_backward_of_rows_without_ids():
+    """Zeros, whatever the logits are."""
+    x = np.array([[NAN, 1.0, 2.0], [np.inf, 0.0, -1.0], [0.5, 1.0, 2.0]])
+    ids = np.array([[-1, 3], [7, -5], [2, -1]])
+    for renorm in (False, True):
+        d = orr.route_backward(x, ids, np.ones((3, 2)), renorm)
+        assert (d[:2] == 0).all() and np.isfinite(d).all()
+    assert (orr.route_backward(x, ids, np.ones((3, 2)), False)[2] != 0).all()
