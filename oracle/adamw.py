@@ -12,6 +12,10 @@ Regularization", 2019, Algorithm 2), in float64:
 nearest to x / scale, scale = largest |x| / 448.  e4m3 (OCP 8-bit floating
 point, 1 sign, 4 exponent, 3 mantissa bits, bias 7) holds 2^-9 i below 2^-6
 and (1 + i / 8) 2^e above, up to 448; 0x7F is NaN.
+
+encode_random takes the code above x / scale instead of the one below where a
+uniform number u is below (x - lo) / (hi - lo), or of the squares for roots, so
+that the expected value (square) is x (x^2).
 """
 
 from __future__ import annotations
@@ -68,3 +72,21 @@ def encode(x, root: bool = False):
                 c = max(c, 1)
             codes[a + i] = c | (128 if val < 0 else 0)
     return codes, np.array(scales)
+
+
+def encode_random(x, u, root: bool = False):
+    """(codes, scales) of x [n] with uniform numbers u [n] in [0, 1)."""
+    x, u = np.asarray(x, dtype=np.float64), np.asarray(u, dtype=np.float64)
+    table = code_values()[:127]
+    starts = np.arange(0, x.size, BLOCK)
+    top = np.maximum.reduceat(np.abs(x), starts)
+    scales = np.where(top >= 2.0 ** -100, top / 448, 0.0)
+    per = np.repeat(scales, BLOCK)[: x.size]
+    mag = np.where(per > 0, np.abs(x) / np.where(per > 0, per, 1.0), 0.0)
+    if root:
+        mag = np.where(mag > 0, np.maximum(mag, table[1]), mag)
+    below = np.clip(np.searchsorted(table, mag, side="right") - 1, 0, 125)
+    power = 2 if root else 1
+    lo, hi = table[below] ** power, table[below + 1] ** power
+    codes = below + (u < (mag ** power - lo) / (hi - lo))
+    return np.where(x < 0, codes | 128, codes).astype(np.uint8), scales

@@ -148,7 +148,7 @@ class salr_adamw_plan_t(C.Structure):
 
 class salr_adamw_step_args_t(C.Structure):
     _fields_ = [("step", C.c_int64)] + [(n, C.c_double) for n in (
-        "lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")]
+        "lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + [("rounding", C.c_int32), ("seed", C.c_uint32)]
 
 
 _LIB = None
@@ -1017,7 +1017,7 @@ def adamw_states(params, bits: int = 32, master: bool = False) -> dict:
     """Fresh AdamW states of the tensors in `params`: the lists m and v
     (float, or with bits = 8 e4m3 codes with the lists m_scale and v_scale)
     and, with master, float copies of bf16 parameters; keywords of
-    adamw_plan."""
+    adamw_plan.  8-bit states are trained with adamw_step's seed."""
     torch = _torch()
     if bits not in (8, 32):
         raise ValueError("bits must be 8 or 32")
@@ -1107,25 +1107,39 @@ def adamw_plan(params, grads, m, v, m_scale=None, v_scale=None, master=None, str
     return AdamWPlan(desc, table, [t for ts in lists.values() for t in ts], dev)
 
 
-def adamw_dyn(step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, grad_scale: float = 1.0) -> list:
-    """The four floats of adamw_step's `dyn` tensor for one step."""
-    return [lr, grad_scale, 1.0 / (1.0 - beta1 ** step), (1.0 - beta2 ** step) ** -0.5]
+def adamw_dyn(step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, grad_scale: float = 1.0,
+              seeded: bool = False) -> list:
+    """The floats of adamw_step's `dyn` tensor for one step: four, or five
+    where the step has a seed."""
+    return [lr, grad_scale, 1.0 / (1.0 - beta1 ** step), (1.0 - beta2 ** step) ** -0.5] + [float(step)] * seeded
 
 
 def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-               weight_decay: float = 0.01, grad_scale: float = 1.0, dyn=None, stream=None):
+               weight_decay: float = 0.01, grad_scale: float = 1.0, dyn=None, stream=None, seed: int | None = None):
     """One AdamW step (number `step`, from 1) over every tensor of the plan,
-    in place and in one launch (salr_adamw_step).  dyn: a device float
-    tensor [4] with adamw_dyn's values, read when the step runs instead of
+    in place and in one launch (salr_adamw_step).
+
+    seed (0 .. 2^32 - 1, one for a whole training): 8-bit states are rounded
+    by chance, so that m and v follow their formulas in the mean (the chance
+    is fixed by the seed and the step's number).  Without it each takes the
+    nearest code, which is right for one step only: over many, v stays where
+    it is, as a step changes it by less than half a code.  Float states are
+    the same either way.
+
+    dyn: a device float tensor with adamw_dyn's values ([4]; with a seed [5],
+    from adamw_dyn(..., seeded=True)), read when the step runs instead of
     step, lr and grad_scale (for captured graphs)."""
     torch = _torch()
-    args, dev = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale), plan.device
+    if seed is not None and not 0 <= seed < 1 << 32:
+        raise ValueError("seed must be in [0, 2^32)")
+    args, dev = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed is not None,
+                                       seed or 0), plan.device
     index = dev.index
     at = _stream_here(index, stream)
     if at is None:
         with _Place(dev, stream):
-            return adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, dyn)
-    d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (4,), index)
+            return adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, dyn, seed=seed)
+    d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (4 if seed is None else 5,), index)
     _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, at), "salr_adamw_step")
 
 

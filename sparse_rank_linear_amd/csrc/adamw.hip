@@ -4,7 +4,8 @@
 // p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
 // 8-bit states hold m and s = sqrt(v) of 256 elements as e4m3 codes times
 // largest / 448 (v spans twice the exponents of its root, which the format's
-// 2^-9 .. 448 would not hold).
+// 2^-9 .. 448 would not hold), the nearest code or one of the two around the
+// value by chance.
 //
 // One workgroup per chunk of a tensor (2048 or 4096 elements), found in the
 // plan's chunk list; 8 consecutive elements a thread, so a float array moves
@@ -12,7 +13,8 @@
 // wave.  Bound by HBM: 24 bytes an element with float states, 12 with 8-bit
 // ones (bf16 parameters, float gradients, no master), 6 more with a master.
 // 201 M with float states and masters: 1000 to 1086 us, 5.6 to 6.0 TB/s; 53 M
-// with 8-bit states: 110 us, 5.8 TB/s.
+// with 8-bit states: 110 us, 5.8 TB/s; rounded by chance 128, then bound by
+// the issue of instructions (201 M: 403 and 473 us, with masters 630 and 637).
 #include <hip/hip_runtime.h>
 
 #include "salr_device.hpp"
@@ -154,6 +156,48 @@ __device__ __forceinline__ void run_scale(const float* x, float* scale, float* i
   *inv = live ? 448.f / top : 0.f;
 }
 
+// ---- random rounding of the codes ----
+//
+// A value x between two codes lo <= x < hi takes hi with a chance that makes
+// what is expected of the stored value x itself: (x - lo) / (hi - lo) for m,
+// and for s = sqrt(v) the chance of the squares, (x^2 - lo^2) / (hi^2 - lo^2),
+// so that v is.  Only then do m and v follow their recurrences: a step changes
+// s by (1 - b2) / 2 at most downwards, far below half a code, and rounding to
+// the nearest would undo it every time.
+
+// x's bits mixed, one to one (two multiplications by odd constants, the first
+// bits of the roots of 2 and 3, between shifts).
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x6A09E667u;
+  x ^= x >> 15;
+  x *= 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+constexpr uint32_t kGolden = 0x9E3779B9u;
+
+// Elements at or past 2^-6 (in scales) lie in steps of 1/8 of their power of
+// two, so that the code below is a float's bits cut off after three; smaller
+// ones in steps of 2^-9, as the floats in [2^-6, 2^-5) do.
+constexpr uint32_t kCodeBits = 0xFFF00000u;
+__device__ __forceinline__ float code_shift(float x) { return x < 0x1p-6f ? 0x1p-6f : 0.f; }
+
+__device__ __forceinline__ float random_m(float x, uint32_t r) {
+  const float mag = fminf(fabsf(x), 448.f);  // (the scale's rounding can leave 448 and an ulp)
+  const float shift = code_shift(mag);
+  const uint32_t b = (__float_as_uint(mag + shift) + (r & ~kCodeBits)) & kCodeBits;
+  return x == x ? copysignf(__uint_as_float(b) - shift, x) : x;
+}
+
+__device__ __forceinline__ float random_s(float x, uint32_t r) {
+  const float mag = fminf(x, 448.f);
+  const float shift = code_shift(mag);
+  const uint32_t b = __float_as_uint(mag + shift) & kCodeBits;
+  const float lo = __uint_as_float(b) - shift, hi = __uint_as_float(b + ~kCodeBits + 1) - shift;
+  const bool up = (float)r * 0x1p-32f * ((hi - lo) * (hi + lo)) < (mag - lo) * (mag + lo);
+  return x == x ? (up ? hi : lo) : x;
+}
+
 // Square roots to 1 ulp (the instruction alone takes no subnormal: values
 // below 2^-96, zeros among them, go scaled).
 __device__ __forceinline__ void roots(const float* v, float* s) {
@@ -213,9 +257,10 @@ struct Eight {
   }
 };
 
-// FULL: the chunk has all its elements.
-template <class P, class G, bool S8, bool MASTER, bool FULL>
-__device__ __forceinline__ void adamw_elements(const AdamwArgs& a, const AdamwTensor& t, int64_t i) {
+// FULL: the chunk has all its elements.  RANDOM: 8-bit codes by chance, from
+// the bits of `key` (the chunk's) and the element's place.
+template <class P, class G, bool S8, bool MASTER, bool RANDOM, bool FULL>
+__device__ __forceinline__ void adamw_elements(const AdamwArgs& a, const AdamwTensor& t, int64_t i, uint32_t key) {
 #pragma clang fp contract(off)
   const int64_t run = i / 256;
   float decay = a.decay, rate = a.rate, gs = a.grad_scale, isb2 = a.inv_sqrt_bias2;
@@ -262,6 +307,11 @@ __device__ __forceinline__ void adamw_elements(const AdamwArgs& a, const AdamwTe
       x.m[c] *= inv_m;
       x.s[c] *= inv_s;
       x.s[c] = x.s[c] > 0.f ? fmaxf(x.s[c], 0x1p-9f) : x.s[c];  // (the smallest code)
+      if constexpr (RANDOM) {
+        const uint32_t r = mix(key + (uint32_t)(i + c) * kGolden);
+        x.m[c] = random_m(x.m[c], r);  // (by its low 20 bits, s by all from the top)
+        x.s[c] = random_s(x.s[c], r);
+      }
     }
     x.mc = encode8(x.m);
     x.vc = encode8(x.s);
@@ -274,14 +324,21 @@ __device__ __forceinline__ void adamw_elements(const AdamwArgs& a, const AdamwTe
   else if (some) x.template store<false>(t, i);
 }
 
-template <class P, class G, bool S8, bool MASTER>
+template <class P, class G, bool S8, bool MASTER, bool RANDOM>
 __global__ __launch_bounds__(adamw_chunk(S8, MASTER) / kPer) void adamw_kernel(AdamwArgs a) {
   constexpr int kChunk = adamw_chunk(S8, MASTER);
   const AdamwChunk ch = a.chunks[blockIdx.x];
   const AdamwTensor t = a.tensors[ch.tensor];
   const int64_t base = (int64_t)ch.chunk * kChunk, i = base + threadIdx.x * kPer;
-  if (base + kChunk <= t.n) adamw_elements<P, G, S8, MASTER, true>(a, t, i);
-  else adamw_elements<P, G, S8, MASTER, false>(a, t, i);
+  uint32_t key = 0;
+  if constexpr (RANDOM) {
+    key = mix(a.seed + kGolden);
+    key = mix(key ^ __float_as_uint(a.dyn ? a.dyn[4] : a.step));
+    key = mix(key ^ (uint32_t)ch.tensor);
+    key = mix(key ^ (uint32_t)(base >> 32));
+  }
+  if (base + kChunk <= t.n) adamw_elements<P, G, S8, MASTER, RANDOM, true>(a, t, i, key);
+  else adamw_elements<P, G, S8, MASTER, RANDOM, false>(a, t, i, key);
 }
 
 // Loads in flight a CU: more of them than about 80 KB open more DRAM pages
@@ -293,31 +350,36 @@ __global__ __launch_bounds__(adamw_chunk(S8, MASTER) / kPer) void adamw_kernel(A
 constexpr int kLdsUnits = 128, kLdsUnit = 1280;  // a CU's LDS, as it is given out
 constexpr int kFlightBytes = 80 * 1024;
 
-template <class P, class G, bool S8, bool MASTER>
+template <class P, class G, bool S8, bool MASTER, bool RANDOM>
 void launch(const AdamwArgs& a, hipStream_t s) {
   constexpr int kThreads = adamw_chunk(S8, MASTER) / kPer;
   constexpr int kFourWaves = 256 * kPer * (int)(sizeof(G) + (S8 ? 2 : 8) + (MASTER ? 4 : sizeof(P)));  // bytes
   constexpr int kGroups = (kFlightBytes / kFourWaves & ~1) * 256 / kThreads;
   static_assert(kGroups >= 1 && kGroups * kThreads <= 2048, "workgroups a CU");
-  hipLaunchKernelGGL((adamw_kernel<P, G, S8, MASTER>), dim3((unsigned)a.n_chunks), dim3(kThreads),
+  hipLaunchKernelGGL((adamw_kernel<P, G, S8, MASTER, RANDOM>), dim3((unsigned)a.n_chunks), dim3(kThreads),
                      kLdsUnits / kGroups * kLdsUnit, s, a);
 }
 
+template <class P, class G, bool MASTER>
+void launch_g(const AdamwArgs& a, bool state8, bool random, hipStream_t s) {
+  if (!state8) launch<P, G, false, MASTER, false>(a, s);
+  else if (random) launch<P, G, true, MASTER, true>(a, s);
+  else launch<P, G, true, MASTER, false>(a, s);
+}
 template <class P, bool MASTER>
-void launch_p(const AdamwArgs& a, bool g_f32, bool state8, hipStream_t s) {
-  if (g_f32)
-    state8 ? launch<P, float, true, MASTER>(a, s) : launch<P, float, false, MASTER>(a, s);
-  else
-    state8 ? launch<P, uint16_t, true, MASTER>(a, s) : launch<P, uint16_t, false, MASTER>(a, s);
+void launch_p(const AdamwArgs& a, bool g_f32, bool state8, bool random, hipStream_t s) {
+  if (g_f32) launch_g<P, float, MASTER>(a, state8, random, s);
+  else launch_g<P, uint16_t, MASTER>(a, state8, random, s);
 }
 
 }  // namespace
 
-hipError_t launch_adamw(const AdamwArgs& a, bool p_f32, bool g_f32, bool state8, bool master, hipStream_t s) {
+hipError_t launch_adamw(const AdamwArgs& a, bool p_f32, bool g_f32, bool state8, bool master, bool random,
+                        hipStream_t s) {
   if (a.n_chunks == 0) return hipSuccess;
-  if (p_f32) launch_p<float, false>(a, g_f32, state8, s);
-  else if (master) launch_p<uint16_t, true>(a, g_f32, state8, s);
-  else launch_p<uint16_t, false>(a, g_f32, state8, s);
+  if (p_f32) launch_p<float, false>(a, g_f32, state8, random, s);
+  else if (master) launch_p<uint16_t, true>(a, g_f32, state8, random, s);
+  else launch_p<uint16_t, false>(a, g_f32, state8, random, s);
   return hipGetLastError();
 }
 

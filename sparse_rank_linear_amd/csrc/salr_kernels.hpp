@@ -298,14 +298,18 @@ struct AdamwChunk {
 struct AdamwArgs {
   const AdamwTensor* tensors;
   const AdamwChunk* chunks;
-  const float* dyn;        // {lr, grad_scale, 1 / (1 - b1^t), 1 / sqrt(1 - b2^t)} or null
+  const float* dyn;        // {lr, grad_scale, 1 / (1 - b1^t), 1 / sqrt(1 - b2^t), t if random} or null
   float beta1, beta2, rest1, rest2;  // rest = 1 - beta
   float eps, weight_decay;
   // where dyn is null: 1 - lr weight_decay, lr / (1 - b1^t), and as in dyn
   float decay, rate, grad_scale, inv_sqrt_bias2;
   int64_t n_chunks;
+  // random rounding of 8-bit states: its seed, and t where dyn is null
+  uint32_t seed;
+  float step;
 };
-hipError_t launch_adamw(const AdamwArgs& a, bool p_f32, bool g_f32, bool state8, bool master, hipStream_t s);
+hipError_t launch_adamw(const AdamwArgs& a, bool p_f32, bool g_f32, bool state8, bool master, bool random,
+                        hipStream_t s);
 
 // ----------------------------------------------------------------------------
 // Encode kernels.

@@ -340,6 +340,7 @@ int salr_adamw_step(const salr_adamw_plan_t* plan, const salr_adamw_step_args_t*
   if (!nonneg(args->eps) || !nonneg(args->weight_decay)) return SALR_ERR_INVALID_ARG;
   if (!(args->beta1 >= 0 && args->beta1 < 1) || !(args->beta2 >= 0 && args->beta2 < 1)) return SALR_ERR_INVALID_ARG;
   if (!dyn && (args->step < 1 || !nonneg(args->lr))) return SALR_ERR_INVALID_ARG;
+  if (args->rounding != SALR_ROUND_NEAREST && args->rounding != SALR_ROUND_RANDOM) return SALR_ERR_INVALID_ARG;
   if (!aligned4(dyn)) return SALR_ERR_INVALID_ARG;
   salr::AdamwArgs a{};
   a.tensors = static_cast<const salr::AdamwTensor*>(plan->table);
@@ -353,6 +354,8 @@ int salr_adamw_step(const salr_adamw_plan_t* plan, const salr_adamw_step_args_t*
   a.rest2 = (float)(1.0 - args->beta2);
   a.eps = (float)args->eps;
   a.weight_decay = (float)args->weight_decay;
+  a.seed = args->seed;
+  a.step = (float)args->step;
   if (!dyn) {
     a.grad_scale = (float)args->grad_scale;
     a.decay = (float)(1.0 - args->lr * args->weight_decay);
@@ -361,7 +364,7 @@ int salr_adamw_step(const salr_adamw_plan_t* plan, const salr_adamw_step_args_t*
   }
   return status(salr::launch_adamw(a, plan->p_type == SALR_TYPE_F32, plan->g_type == SALR_TYPE_F32,
                                    plan->state_type == SALR_STATE_8BIT, plan->has_master != 0,
-                                   static_cast<hipStream_t>(stream)));
+                                   args->rounding == SALR_ROUND_RANDOM, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

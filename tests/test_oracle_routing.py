@@ -155,3 +155,49 @@ def test_route_backward_of_rows_without_ids():
         d = orr.route_backward(x, ids, np.ones((3, 2)), renorm)
         assert (d[:2] == 0).all() and np.isfinite(d).all()
     assert (orr.route_backward(x, ids, np.ones((3, 2)), False)[2] != 0).all()
+
+
+def test_e4m3_codes_by_chance():
+    """encode_random: codes themselves stay, the values around a number come
+    in the shares that keep its mean (its square's, for roots)."""
+    rng = np.random.default_rng(7)
+    table = oa.code_values()
+    exact = np.concatenate([table[:127], -table[1:127]]) * 2.0 ** -20
+    for u in (0.0, 0.5, 1 - 2.0 ** -53):
+        c, s = oa.encode_random(exact, np.full(exact.size, u))
+        assert np.array_equal(oa.decode(c, s), exact)
+    n, steps = 256, 4096
+    x = np.abs(rng.standard_normal(n)) * np.exp(rng.standard_normal(n) * 3)
+    u = (np.arange(steps) + 0.5) / steps                  # every share, to half a grid step
+    for root in (False, True):
+        power = 2 if root else 1
+        c, s = zip(*(oa.encode_random(x, np.full(n, q), root) for q in u))
+        vals = np.stack([oa.decode(a, b) for a, b in zip(c, s)])
+        gap = vals.max(0) ** power - vals.min(0) ** power
+        want = np.maximum(x, s[0][0] * 2.0 ** -9) ** power if root else x
+        assert (np.abs((vals ** power).mean(0) - want) <= gap * 0.51 / steps + 1e-12 * want).all()
+        step = np.maximum(want ** (1 / power) / 8, s[0][0] * 2.0 ** -9)     # codes beside x: at most this apart,
+        apart = step * (2 * want ** 0.5 + step) if root else step         # their squares (x + step)^2 - x^2
+        assert (gap <= apart * (1 + 1e-9)).all()
+    with pytest.raises(AssertionError):                   # the chance of the values is not that of the squares
+        c, s = zip(*(oa.encode_random(x, np.full(n, q), False) for q in u))
+        vals = np.stack([oa.decode(a, b) for a, b in zip(c, s)])
+        assert (np.abs((vals ** 2).mean(0) - x ** 2) <= gap * 0.51 / steps + 1e-12).all()
+
+
+def test_stored_root_follows_only_by_chance():
+    """v = b2 v + (1 - b2) g^2 with its root stored as codes at every step,
+    gradients of half the elements 20 times smaller after a third: by chance
+    the mean of v is the formula's; at the nearest code it stays."""
+    rng = np.random.default_rng(8)
+    n, b2, ends = 256 * 16, 0.99, {}
+    for how in ("chance", "near"):
+        v, want = np.zeros(n), np.zeros(n)
+        for t in range(900):
+            g2 = np.where((np.arange(n) % 2 == 0) & (t >= 300), 0.05, 1.0) ** 2
+            v, want = b2 * v + (1 - b2) * g2, b2 * want + (1 - b2) * g2
+            c, s = oa.encode_random(np.sqrt(v), rng.random(n) if how == "chance" else np.full(n, 0.5), True)
+            v = oa.decode(c, s) ** 2
+        ends[how] = v[::2].mean() / want[::2].mean()
+    # (an element's v has a standard deviation of the size of its mean at most here: 2048 of them, 6 of the mean's)
+    assert abs(ends["chance"] - 1) < 6 / 2048 ** 0.5 and ends["near"] > 50, ends

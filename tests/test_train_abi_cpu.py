@@ -170,3 +170,18 @@ def test_binding_refuses_host_tensors():
     assert st["m"][0].dtype == torch.float8_e4m3fn and st["m_scale"][1].numel() == 1 and len(st["master"]) == 2
     with pytest.raises(ValueError, match="scale"):
         srl.adamw_plan([h], [h], [h.float()], [h.float()], m_scale=[h.float()], v_scale=[h.float()])
+
+
+def test_adamw_rounding_refusals():
+    lib = srl.lib()
+    d = B.salr_adamw_plan_t(P, 0, 1, 0, 1, 1, 0)
+    args = lambda rounding, seed=5: B.salr_adamw_step_args_t(1, 1e-3, 0.9, 0.999, 1e-8, 0.01, 1.0, rounding, seed)
+    run = lambda a, dyn=None: lib.salr_adamw_step(C.byref(d), C.byref(a), dyn, None)
+    assert run(args(0)) == 0 and run(args(1)) == 0 and run(args(1, 2 ** 32 - 1), dyn=P) == 0
+    assert run(args(2)) == -1 and run(args(-1)) == -1 and run(args(1), dyn=P + 2) == -1
+    # the binding's record has the header's layout: 64 bytes in all
+    assert C.sizeof(B.salr_adamw_step_args_t) == 64 and B.salr_adamw_step_args_t.seed.offset == 60
+    for seed in (-1, 2 ** 32):
+        with pytest.raises(ValueError, match="seed"):
+            srl.adamw_step(None, 1, 1e-3, seed=seed)
+    assert srl.adamw_dyn(3, 0.5, seeded=True) == srl.adamw_dyn(3, 0.5) + [3.0]
