@@ -657,8 +657,9 @@ typedef struct salr_adamw_step_args {
 } salr_adamw_step_args_t;
 
 /* Bytes of the plan's device buffer for `count` tensors of n[i] elements (`n`
- * and `out` host; count <= 2^20, at most 2^24 - 1 runs of 2048 elements in
- * all).  Errors: INVALID_ARG. */
+ * and `out` host; count <= 2^20; at most 2^24 - 1 runs of 2048 elements and
+ * 2^23 - 1 of 4096 in all, each tensor's last run counted whole).  Errors:
+ * INVALID_ARG. */
 int salr_adamw_plan_bytes(const int64_t* n, int32_t count, size_t* out);
 
 /*

@@ -19,7 +19,8 @@ constexpr int64_t kMaxSlots = (int64_t(1) << 31) - 65536;  // (int32 rows, with 
 constexpr int64_t kMaxColumns = int64_t(1) << 20;
 constexpr int64_t kMaxTensorElements = int64_t(1) << 40;
 constexpr int32_t kMaxTensors = 1 << 20;
-constexpr int64_t kMaxChunks = (int64_t(1) << 24) - 1;  // workgroups of one launch
+// Workgroups of one launch: its threads, 8 elements each, stay below 2^32.
+constexpr int64_t max_chunks(int64_t chunk) { return ((int64_t(1) << 32) - 1) / (chunk / 8); }
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -260,16 +261,24 @@ int adamw_fill(const salr_adamw_tensor_t* t, int32_t count, int32_t p_type, int3
   return overlaps(ranges, nw, read, nr) ? SALR_ERR_INVALID_ARG : SALR_OK;
 }
 
-// The chunks of `count` tensors, or -1.
+// The chunks of `count` tensors, or -1 (a tensor too long, or too many).
 template <class F>
 int64_t adamw_chunks(int32_t count, int64_t chunk, F n) {
   int64_t chunks = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (n(i) < 0 || n(i) >= kMaxTensorElements) return -1;
     chunks += cdiv(n(i), chunk);
-    if (chunks > kMaxChunks) return -1;
+    if (chunks > max_chunks(chunk)) return -1;
   }
   return chunks;
+}
+
+// The chunks in small ones, which size the table, where both kinds can be
+// launched, or -1.
+template <class F>
+int64_t adamw_small_chunks(int32_t count, F n) {
+  const int64_t chunks = adamw_chunks(count, salr::kAdamwSmallChunk, n);
+  return adamw_chunks(count, salr::adamw_chunk(false, false), n) < 0 ? -1 : chunks;
 }
 
 }  // namespace
@@ -278,7 +287,7 @@ extern "C" {
 
 int salr_adamw_plan_bytes(const int64_t* n, int32_t count, size_t* out) {
   if (!out || count < 0 || count > kMaxTensors || (count > 0 && !n)) return SALR_ERR_INVALID_ARG;
-  const int64_t chunks = adamw_chunks(count, salr::kAdamwSmallChunk, [&](int32_t i) { return n[i]; });
+  const int64_t chunks = adamw_small_chunks(count, [&](int32_t i) { return n[i]; });
   if (chunks < 0) return SALR_ERR_INVALID_ARG;
   *out = table_bytes_for(count, chunks);
   return SALR_OK;
@@ -293,7 +302,7 @@ int salr_adamw_plan(const salr_adamw_tensor_t* tensors, int32_t count, int32_t p
   bool master = false;
   for (int32_t i = 0; i < count && !master; ++i) master = tensors[i].n > 0 && tensors[i].master != nullptr;
   const auto size = [&](int32_t i) { return tensors[i].n; };
-  if (adamw_chunks(count, salr::kAdamwSmallChunk, size) < 0) return SALR_ERR_INVALID_ARG;  // (as the table's size says)
+  if (adamw_small_chunks(count, size) < 0) return SALR_ERR_INVALID_ARG;  // (as the table's size says)
   const int64_t chunks = adamw_chunks(count, salr::adamw_chunk(state8, master), size);
   if (master && p_type != SALR_TYPE_BF16) return SALR_ERR_INVALID_ARG;
   const size_t bytes = table_bytes_for(count, chunks);
@@ -332,7 +341,8 @@ int salr_adamw_step(const salr_adamw_plan_t* plan, const salr_adamw_step_args_t*
                     void* stream) {
   if (!plan || !args) return SALR_ERR_INVALID_ARG;
   if (!plan->table || !aligned16(plan->table) || plan->count < 0 || plan->count > kMaxTensors || plan->chunks < 0 ||
-      plan->chunks > kMaxChunks || !type_ok(plan->p_type) || !type_ok(plan->g_type) ||
+      plan->chunks > max_chunks(salr::adamw_chunk(plan->state_type == SALR_STATE_8BIT, plan->has_master != 0)) ||
+      !type_ok(plan->p_type) || !type_ok(plan->g_type) ||
       (plan->state_type != SALR_STATE_F32 && plan->state_type != SALR_STATE_8BIT) ||
       (plan->has_master && plan->p_type != SALR_TYPE_BF16))
     return SALR_ERR_INVALID_ARG;

@@ -185,3 +185,22 @@ def test_adamw_rounding_refusals():
         with pytest.raises(ValueError, match="seed"):
             srl.adamw_step(None, 1, 1e-3, seed=seed)
     assert srl.adamw_dyn(3, 0.5, seeded=True) == srl.adamw_dyn(3, 0.5) + [3.0]
+
+
+def test_adamw_plans_stay_within_a_launch():
+    """Workgroups of 2048 elements have 256 threads, of 4096 elements 512: a
+    launch's threads stay below 2^32 in either."""
+    count = 1 << 20
+    n = (C.c_int64 * count)(*([7 * 4096] * count))
+    out, size = C.c_size_t(), srl.lib().salr_adamw_plan_bytes
+    assert size(n, count, C.byref(out)) == 0                            # 14 x 2^20 runs of 2048, 7 x 2^20 of 4096
+    n = (C.c_int64 * count)(*([7 * 4096 + 1] * count))
+    assert size(n, count, C.byref(out)) == -1                           # 15 x 2^20, and 2^23
+    n[0] = 7 * 4096
+    assert size(n, count, C.byref(out)) == 0                            # 2^23 - 1
+    args = B.salr_adamw_step_args_t(1, 1e-3, 0.9, 0.999, 1e-8, 0.01, 1.0)
+    for state, master in ((0, 0), (0, 1), (1, 1)):
+        d = B.salr_adamw_plan_t(P, 1 << 23, 1, 0, 1, state, master)
+        assert srl.lib().salr_adamw_step(C.byref(d), C.byref(args), None, None) == -1
+    d = B.salr_adamw_plan_t(P, 1 << 24, 1, 0, 1, 1, 0)
+    assert srl.lib().salr_adamw_step(C.byref(d), C.byref(args), None, None) == -1
