@@ -943,6 +943,8 @@ def moe_dispatch(ids, E: int, X=None, Xs=None, offsets=None, rows=None, slots=No
         ws = torch.empty(moe_dispatch_ws_bytes(T, k, E), dtype=torch.uint8, device=dev)
     elif ws.device != dev:
         raise ValueError(f"ws must be on {dev} (is on {ws.device})")
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     _check(_lib().salr_moe_dispatch(_ptr(ids, "ids", torch.int32, (T, k), index), T, k, E, x, D,
                                     _ptr(offsets, "offsets", torch.int32, (E + 1,), index),
                                     _ptr(rows, "rows", torch.int32, (T, k), index),

@@ -516,3 +516,17 @@ def test_route_backward_rows_without_ids(E, k, half):
         assert torch.count_nonzero(got[dead]) == 0
         alive = [t for t in range(T) if t not in dead]
         assert torch.isfinite(got).all() and torch.equal(got[alive], clean[renorm][alive])
+
+
+def test_dispatch_workspace_is_as_long_as_it_says():
+    """A workspace whose elements share bytes or leave some out is refused."""
+    import torch
+
+    srl = _srl()
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    n = srl.moe_dispatch_ws_bytes(4, 2, 8)
+    for ws in (torch.zeros(16, dtype=torch.uint8, device="cuda").repeat(1, 1).expand(n, 16),
+               torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="ws"):
+            srl.moe_dispatch(ids, 8, ws=ws)
+    assert srl.moe_dispatch(ids, 8, ws=torch.zeros(n // 4, dtype=torch.int32, device="cuda"))[1].tolist() == [0] + [8] * 8
