@@ -530,3 +530,125 @@ def test_dispatch_workspace_is_as_long_as_it_says():
         with pytest.raises(ValueError, match="ws"):
             srl.moe_dispatch(ids, 8, ws=ws)
     assert srl.moe_dispatch(ids, 8, ws=torch.zeros(n // 4, dtype=torch.int32, device="cuda"))[1].tolist() == [0] + [8] * 8
+
+
+# Slots around the sizes where another form of the dispatch takes over: 12288
+# slots (one launch), 16384 chunk counts (12289 slots in 13 chunks of 1260 or
+# 1261 experts), 2^20 slots.
+@pytest.mark.parametrize("T,k,E", [(12287, 1, 64), (12288, 1, 64), (12289, 1, 64), (4095, 3, 8), (4096, 3, 8),
+                                   (4097, 3, 8), (6143, 2, 2000), (6144, 2, 2000), (6145, 2, 2000), (7001, 1, 300),
+                                   (12289, 1, 1260), (12289, 1, 1261), ((1 << 20) - 1, 1, 8), (1 << 20, 1, 8),
+                                   ((1 << 20) + 1, 1, 8), (1 << 18, 4, 256), ((1 << 18) + 1, 4, 256),
+                                   (174762, 6, 64), (174763, 6, 64), (300000, 8, 1025)])
+def test_dispatch_sort_where_forms_change(T, k, E):
+    import torch
+
+    srl = _srl()
+    say(f"dispatch forms T={T} k={k} E={E}")
+    ids = _ids(T, k, E, T + E)
+    off, rows, slots = _want_dispatch(ids, E)
+    n, D = T * k, 8
+    X = torch.randint(-2 ** 15, 2 ** 15, (T, D), device="cuda", dtype=torch.int16).view(torch.bfloat16)
+    Xs = torch.full((n + 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    gslots = torch.full((n + 8,), -77, dtype=torch.int32, device="cuda")
+    d = torch.from_numpy(ids).cuda()
+    _, goff, grows, _ = srl.moe_dispatch(d, E, X, Xs=Xs[:n], slots=gslots[:n])
+    live = int(off[-1])
+    assert np.array_equal(goff.cpu().numpy(), off) and np.array_equal(grows.cpu().numpy(), rows)
+    assert np.array_equal(gslots.cpu().numpy()[:live], slots) and (gslots[live:] == -77).all()
+    want = X.view(torch.int16)[torch.from_numpy(slots).cuda().long() // k]
+    assert torch.equal(Xs.view(torch.int16)[:live], want) and (Xs[live:] == 7.0).all()
+    _, soff, srows, sslots = srl.moe_dispatch(d, E)       # the sort alone
+    assert torch.equal(soff, goff) and torch.equal(srows, grows)
+    assert np.array_equal(sslots.cpu().numpy()[:live], slots)
+
+
+def _route_many(x, k, renorm):
+    """orr.route for many rows: a stable descending sort (ties to the lower)."""
+    order = np.argsort(-x, axis=1, kind="stable")[:, :k]
+    vals = np.take_along_axis(x, order, 1)
+    ids = np.where(vals > -INF, order, -1).astype(np.int32)
+    top = np.where(vals[:, :1] > -INF, vals[:, :1], 0.0)
+    e = np.exp(vals - top)
+    total = e.sum(1, keepdims=True) if renorm else np.exp(x - top).sum(1, keepdims=True)
+    return ids, e / np.where(total > 0, total, 1.0)
+
+
+@pytest.mark.parametrize("T,E,k", [(16384, 8, 2), (16379, 64, 6), (16384, 256, 8), (4099, 320, 8), (70001, 4, 4)])
+@pytest.mark.parametrize("half", [False, True], ids=["f32", "bf16"])
+def test_route_many_tokens(T, E, k, half):
+    """The router and its gradient over thousands of rows, with ties, masked
+    entries and masked rows; the tolerances of test_route and
+    test_route_backward."""
+    import torch
+
+    srl = _srl()
+    say(f"route many T={T} E={E} k={k} half={half}")
+    x = _logits(T, E, half, seed=T + E + k)
+    d = _up(x, half)
+    dw = np.random.default_rng(T).standard_normal((T, k)).astype(np.float32)
+    for renorm in (False, True):
+        want_ids, want = _route_many(x, k, renorm)
+        few = np.r_[0:40, T // 3, T // 2, T - 1]
+        o_ids, o_w = orr.route(x[few], k, renorm)
+        assert np.array_equal(o_ids, want_ids[few]) and np.allclose(o_w, want[few], rtol=1e-12, atol=0)
+        ids, w = srl.moe_route(d, k, renorm=renorm)
+        assert np.array_equal(ids.cpu().numpy(), want_ids)
+        assert (np.abs(w.double().cpu().numpy() - want) <= 256 * U * want).all()
+        dwd = dw.copy()
+        dwd[want_ids < 0] = NAN                             # never used
+        got = srl.moe_route_backward(d, ids, _up(dwd), renorm=renorm).double().cpu().numpy()
+        chosen, at = want_ids >= 0, np.maximum(want_ids, 0)
+        p, up, mag = (np.zeros((T, E)) for _ in range(3))
+        rows = np.arange(T)[:, None]
+        np.add.at(p, (rows, at), np.where(chosen, want, 0.0))
+        if not renorm:
+            top = x.max(1, keepdims=True)
+            p = np.exp(x - np.where(top > -INF, top, 0.0))
+            p /= np.where(top > -INF, p.sum(1, keepdims=True), 1.0)
+        np.add.at(up, (rows, at), np.where(chosen, dw, 0.0))
+        np.add.at(mag, (rows, at), np.where(chosen, np.abs(dw), 0.0))
+        grad = p * (up - (p * up).sum(1, keepdims=True))
+        assert np.allclose(orr.route_backward(x[few], want_ids[few], dw[few], renorm), grad[few], rtol=1e-9, atol=1e-15)
+        tol = 512 * U * p * (mag + (p * mag).sum(1, keepdims=True)) + (H * np.abs(grad) if half else 0) + 1e-38
+        assert (np.abs(got - grad) <= tol).all(), (np.abs(got - grad) / tol).max()
+
+
+@pytest.mark.parametrize("E,k", [(3, 3), (40, 32), (64, 6), (100, 32), (256, 9), (700, 32), (3000, 8), (4096, 32)])
+def test_route_backward_repeated_ids(E, k):
+    """Choices drawn from at most 2 k experts, so that a row names some of
+    them several times, at a tolerance that goes with each probability (as
+    test_route_backward's): taking the last of a repeated expert's gradients,
+    or leaving out the mean, is far outside it."""
+    import torch
+
+    srl = _srl()
+    rng = np.random.default_rng(E + k)
+    T = 21
+    x = rng.standard_normal((T, E)).astype(np.float32).astype(np.float64)
+    pool = rng.permutation(E)[: 2 * k]
+    ids = pool[rng.integers(0, pool.size, (T, k))].astype(np.int32)
+    ids[:, 1] = ids[:, 0]
+    ids[rng.random((T, k)) < 0.1] = -1
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    for renorm in (False, True):
+        want = orr.route_backward(x, ids, dw, renorm)
+        last, no_mean, p, mag = (np.zeros((T, E)) for _ in range(4))
+        for t in range(T):
+            once = {int(e): d for e, d in zip(ids[t], dw[t]) if e >= 0}
+            if once:
+                last[t] = orr.route_backward(x[t:t + 1], np.array([list(once)]), np.array([list(once.values())]), renorm)
+            keep = np.isin(np.arange(E), ids[t]) if renorm else np.ones(E, bool)
+            if once:
+                v = np.where(keep, x[t], -INF)
+                p[t] = np.exp(v - v.max()) / np.exp(v - v.max()).sum()
+            for e, d in zip(ids[t], dw[t]):
+                if e >= 0:
+                    mag[t, e] += abs(d)
+                    no_mean[t, e] += p[t, e] * d
+        tol = 512 * U * p * (mag + (p * mag).sum(1, keepdims=True)) + 1e-38
+        for wrong in (last, no_mean):
+            assert (np.abs(wrong - want) > 4 * tol).any()
+        got = srl.moe_route_backward(_up(x), torch.from_numpy(ids).cuda(), _up(dw), renorm=renorm)
+        err = np.abs(got.double().cpu().numpy() - want)
+        assert (err <= tol).all(), (err / tol).max()
