@@ -279,12 +279,18 @@ hipError_t launch_moe_combine_backward(const MoeCombineArgs& a, hipStream_t s);
 // records, then one {tensor, chunk of the tensor} pair per adamw_chunk()
 // elements of each tensor.
 // ----------------------------------------------------------------------------
-// Elements per workgroup, whole 8-bit blocks: 4096 where there are float states
-// or masters (a run of 16 KB in each of their arrays opens fewer DRAM pages:
-// 201 M bf16 parameters with masters 1002 us, with 2048 1107), else 2048 (53 M,
-// 8-bit states: 107 us, with 4096 115).
-constexpr int kAdamwSmallChunk = 2048;
-constexpr int adamw_chunk(bool state8, bool master) { return state8 && !master ? kAdamwSmallChunk : 4096; }
+// Elements per workgroup, whole 8-bit blocks: 4096 for float states with
+// masters (runs of 16 KB in four float arrays open fewer DRAM pages), else
+// 2048.  201 M bf16 parameters in us, 2048 / 4096, over several placements of
+// the arrays, which spread as much: float gradients, states and masters
+// 1032-1128 / 1055-1083 (in the mean 1083 / 1068), bf16 gradients 1049-1072 /
+// 996-1056 (1061 / 1026); float states without masters 797-806 / 848-855; 8-bit
+// states 409-427 / 432-457, with masters 653-667 / 644-662 (rounded by chance
+// 627 / 637).
+constexpr int kAdamwSmallChunk = 2048, kAdamwLargeChunk = 4096;
+constexpr int adamw_chunk(bool state8, bool master) {
+  return master && !state8 ? kAdamwLargeChunk : kAdamwSmallChunk;
+}
 struct AdamwTensor {
   void* p;
   const void* g;

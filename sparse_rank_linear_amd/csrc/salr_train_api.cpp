@@ -199,8 +199,8 @@ int salr_moe_combine_backward(const uint16_t* dY, const uint16_t* Ys, int64_t R,
 // AdamW: the plan's table is the tensor records, then the chunk list.
 namespace {
 
-static_assert(salr::kAdamwSmallChunk % SALR_ADAMW_BLOCK == 0 && salr::adamw_chunk(true, true) % SALR_ADAMW_BLOCK == 0 &&
-                  salr::adamw_chunk(false, false) >= salr::kAdamwSmallChunk,
+static_assert(salr::kAdamwSmallChunk % SALR_ADAMW_BLOCK == 0 && salr::kAdamwLargeChunk % SALR_ADAMW_BLOCK == 0 &&
+                  salr::kAdamwLargeChunk >= salr::kAdamwSmallChunk,
               "a chunk holds whole 8-bit runs, and the small one sizes the table");
 
 size_t table_records_bytes(int32_t count) { return align_up((size_t)count * sizeof(salr::AdamwTensor), 256); }
@@ -278,7 +278,7 @@ int64_t adamw_chunks(int32_t count, int64_t chunk, F n) {
 template <class F>
 int64_t adamw_small_chunks(int32_t count, F n) {
   const int64_t chunks = adamw_chunks(count, salr::kAdamwSmallChunk, n);
-  return adamw_chunks(count, salr::adamw_chunk(false, false), n) < 0 ? -1 : chunks;
+  return adamw_chunks(count, salr::kAdamwLargeChunk, n) < 0 ? -1 : chunks;
 }
 
 }  // namespace

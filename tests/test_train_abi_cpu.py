@@ -199,8 +199,6 @@ def test_adamw_plans_stay_within_a_launch():
     n[0] = 7 * 4096
     assert size(n, count, C.byref(out)) == 0                            # 2^23 - 1
     args = B.salr_adamw_step_args_t(1, 1e-3, 0.9, 0.999, 1e-8, 0.01, 1.0)
-    for state, master in ((0, 0), (0, 1), (1, 1)):
-        d = B.salr_adamw_plan_t(P, 1 << 23, 1, 0, 1, state, master)
+    for state, master, chunks in ((0, 1, 1 << 23), (0, 0, 1 << 24), (1, 0, 1 << 24), (1, 1, 1 << 24)):
+        d = B.salr_adamw_plan_t(P, chunks, 1, 0, 1, state, master)
         assert srl.lib().salr_adamw_step(C.byref(d), C.byref(args), None, None) == -1
-    d = B.salr_adamw_plan_t(P, 1 << 24, 1, 0, 1, 1, 0)
-    assert srl.lib().salr_adamw_step(C.byref(d), C.byref(args), None, None) == -1
