@@ -12,9 +12,10 @@
 // 32 bytes and the codes 8 bytes a thread, and an 8-bit run is 32 lanes of one
 // wave.  Bound by HBM: 24 bytes an element with float states, 12 with 8-bit
 // ones (bf16 parameters, float gradients, no master), 6 more with a master.
-// 201 M with float states and masters: 1000 to 1086 us, 5.6 to 6.0 TB/s; 53 M
-// with 8-bit states: 110 us, 5.8 TB/s; rounded by chance 128, then bound by
-// the issue of instructions (201 M: 403 and 473 us, with masters 630 and 637).
+// 201 M with float states and masters: 1047 to 1101 us, 5.5 to 5.8 TB/s by
+// where the arrays lie, without masters 800, 6.0 TB/s; 53 M with 8-bit states:
+// 110 us, 5.8 TB/s; rounded by chance 128, then bound by the issue of
+// instructions (201 M: 410 and 474 us; with masters 660 and 620, HBM in both).
 #include <hip/hip_runtime.h>
 
 #include "salr_device.hpp"
@@ -28,7 +29,8 @@ constexpr int kRunLanes = 256 / kPer;
 constexpr float kTiny = 0x1p-100f;
 
 // Stores past the caches: nothing written is read again before the next step
-// (201 M parameters with masters: 1114 us, cached 1143).
+// (201 M parameters with masters, mean over eight placements: 1072 us, cached
+// 1097; without masters 803 either way).
 template <class V>
 __device__ __forceinline__ void stream_store(V* p, V v) {
   __builtin_nontemporal_store(v, p);

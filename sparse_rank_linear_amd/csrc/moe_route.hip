@@ -14,10 +14,12 @@
 // DPP row rotations, without the LDS round trips of a shuffle.
 //
 // Bound by the launch up to a few thousand rows, then by the issue of
-// instructions (16384 rows of 64 floats, top 6: 4.2 us, backward 4.1, where
-// reading and writing them takes 0.8 and 1.5; 16384 of 256, top 8: 8.7 and
-// 9.7).  A wave per row took 18.6 us for the first, float maxima (which
-// quiet NaNs) and the library's exp 4.9.
+// instructions (calls in a graph, over four sets of inputs: 16384 rows of 64
+// floats, top 6: 4.4 us, backward 4.3, where reading and writing them takes
+// 0.8 and 1.5; 16384 of 256, top 8: 10.4 and 11.2; of 1024, top 8: 28.7 and
+// 32.7).  For the first, a wave per row took 18.6 us where 16 lanes took 5.9,
+// and float maxima (which quiet NaNs) with the library's exp 4.9 where these
+// took 4.2.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -84,8 +86,10 @@ __device__ __forceinline__ int order_of(float x) {
 }
 __device__ __forceinline__ float value_of(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7FFFFFFF)); }
 
-// exp(x) for x <= 0 to 2 ulp, 0 below -150 (NaN stays): 2^y for y = x log2(e),
-// times 1 + ln(2) (x log2(e) - y) for what y's rounding dropped.
+// exp(x) for x <= 0 to 2 ulp, 0 below about -87.3, where it is no normal float
+// any more (the instruction gives no subnormals; NaN stays): 2^y for y = x
+// log2(e), times 1 + ln(2) (x log2(e) - y) for what y's rounding dropped.  x is
+// cut at -150, since -inf would leave NaN in the rest.
 __device__ __forceinline__ float exp_down(float x) {
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
   x = x < -150.f ? -150.f : x;

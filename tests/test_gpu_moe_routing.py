@@ -652,3 +652,27 @@ def test_route_backward_repeated_ids(E, k):
         got = srl.moe_route_backward(_up(x), torch.from_numpy(ids).cuda(), _up(dw), renorm=renorm)
         err = np.abs(got.double().cpu().numpy() - want)
         assert (err <= tol).all(), (err / tol).max()
+
+
+def test_route_far_apart():
+    """Logits 0 to 200 below the largest: the exponent is off by 2^-24 of the
+    distance, so the weights by 256 u as far as floats are normal (2^-126);
+    smaller ones may be 0.  A mask of the type's lowest value is a logit like
+    others: weight 0 beside finite ones, an even share among themselves."""
+    import torch
+
+    srl = _srl()
+    gap = np.arange(0, 200, 0.25)
+    for half in (False, True):
+        x = np.stack([np.full(gap.size, 3.0), 3.0 - gap], 1)
+        x = _bf16(x)[0] if half else x
+        for renorm in (False, True):
+            want_ids, want = orr.route(x, 2, renorm)
+            ids, w = srl.moe_route(_up(x, half), 2, renorm=renorm)
+            assert np.array_equal(ids.cpu().numpy(), want_ids)
+            err = np.abs(w.double().cpu().numpy() - want)
+            assert (err <= 256 * U * want + 2.0 ** -126).all()
+        low = torch.finfo(torch.bfloat16 if half else torch.float32).min
+        ids, w = srl.moe_route(torch.tensor([[low, 1.0, low, 0.0], [low] * 4], device="cuda")
+                               .to(torch.bfloat16 if half else torch.float32), 4)
+        assert ids.tolist() == [[1, 3, 0, 2], [0, 1, 2, 3]] and w[0, 2:].tolist() == [0, 0] and w[1].tolist() == [0.25] * 4
