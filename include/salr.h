@@ -601,28 +601,28 @@ int salr_moe_combine_backward(const uint16_t* dY, const uint16_t* Ys, int64_t R,
  * A NaN gradient makes its own element NaN; an infinite one (or one whose
  * square is) its element, and in 8 bits its whole run.
  *
- * Which code (`rounding` of the step's arguments, 8-bit states only):
- *   SALR_ROUND_NEAREST  the nearest, ties to even.  Right for one step, not
+ * Which code of 8-bit states:
+ *   salr_adamw_step         the nearest, ties to even.  Right for one step, not
  *       for training: codes lie 6 to 13% apart, so one that a step changes by
  *       less than half of that is rounded back to where it was.  At beta2 =
  *       0.999 a step lowers s by 0.05% at most: v then STAYS where it is (but
  *       for its run's largest, and what the run's scale does to all of it),
  *       too large after gradients shrink (20 times smaller for half of a
  *       run: s there near 6 times too large 4000 steps on) and wrong after they
- *       grow (v by a third to a half).  The same holds for m from beta1 = 0.94 on.
- *   SALR_ROUND_RANDOM   one of the two codes around the value, by chance, so
- *       that the expected m and v are the values themselves: m and v follow
- *       the formulas above in the mean, over any number of steps; an
- *       element's v scatters by about a third of it while the gradients keep
- *       their size (by all of it after they shrink).  The chance is a hash of
- *       `seed`, the step number, the tensor's place in the plan and the
- *       element's place in the tensor: the same call gives the same bits.
+ *       grow (v by a third or more).  The same holds for m from beta1 = 0.94
+ *       on.
+ *   salr_adamw_step_random  one of the two codes around the value, by chance,
+ *       so that the expected m and v are the values themselves: m and v follow
+ *       the formulas above in the mean, over any number of steps (but an s
+ *       below the smallest code takes that, as said); an element's v scatters
+ *       by about a third of it while the gradients keep their size (by all of
+ *       it after they shrink).  The chance is a hash of `seed`, the step
+ *       number, the tensor's place in the plan and the element's place in the
+ *       tensor: the same call gives the same bits.
  */
 #define SALR_STATE_F32 0
 #define SALR_STATE_8BIT 1
 #define SALR_ADAMW_BLOCK 256
-#define SALR_ROUND_NEAREST 0
-#define SALR_ROUND_RANDOM 1
 
 /* One tensor of n elements: plain device pointers (scales: 4-byte aligned, so
  * that the runs of many tensors may lie in one array). */
@@ -646,14 +646,10 @@ typedef struct salr_adamw_plan {
 } salr_adamw_plan_t;
 
 /* What one step uses.  step >= 1; lr, eps, weight_decay >= 0 and finite, 0 <=
- * beta1, beta2 < 1.  rounding and seed: see above; of no effect on float
- * states.  (As a number of the hash the step is a float: steps past 2^24 that
- * round to the same float share their chances.) */
+ * beta1, beta2 < 1. */
 typedef struct salr_adamw_step_args {
   int64_t step;
   double lr, beta1, beta2, eps, weight_decay, grad_scale;
-  int32_t rounding;
-  uint32_t seed;
 } salr_adamw_step_args_t;
 
 /* Bytes of the plan's device buffer for `count` tensors of n[i] elements (`n`
@@ -685,13 +681,26 @@ int salr_adamw_plan(const salr_adamw_tensor_t* tensors, int32_t count,
  * dyn   NULL, or device float [4] that replaces args' step, lr and grad_scale
  *       (for steps in a captured graph, whose host arguments are fixed):
  *       {lr, grad_scale, 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)}, read
- *       when the step runs; with SALR_ROUND_RANDOM and 8-bit states float
- *       [5], the last the step number t.
+ *       when the step runs.
  * Asynchronous on `stream`, capturable.  Errors: INVALID_ARG, HIP.
  */
 int salr_adamw_step(const salr_adamw_plan_t* plan,
                     const salr_adamw_step_args_t* args, const float* dyn,
                     void* stream);
+
+/*
+ * salr_adamw_step_random - the same with 8-bit states rounded by chance (see
+ * above); on float states salr_adamw_step.
+ * seed  one for a whole training (another for each plan, or their tensors of
+ *       the same place share their chances).
+ * dyn   NULL, or as for salr_adamw_step, but float [5]: the last is the step
+ *       number t.  (Either way the hash takes t as a float: steps past 2^24
+ *       that round to the same float share their chances.)
+ * Asynchronous on `stream`, capturable.  Errors: INVALID_ARG, HIP.
+ */
+int salr_adamw_step_random(const salr_adamw_plan_t* plan,
+                           const salr_adamw_step_args_t* args, uint32_t seed,
+                           const float* dyn, void* stream);
 
 /* Static English text for a status code (never NULL). */
 const char* salr_status_string(int status);

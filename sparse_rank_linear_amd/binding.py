@@ -53,6 +53,7 @@ EXPORTS = (
     "salr_adamw_plan_bytes",
     "salr_adamw_plan",
     "salr_adamw_step",
+    "salr_adamw_step_random",
     # include/salr_probe.h
     "salr_probe_stream_read",
     "salr_probe_mfma",
@@ -148,7 +149,7 @@ class salr_adamw_plan_t(C.Structure):
 
 class salr_adamw_step_args_t(C.Structure):
     _fields_ = [("step", C.c_int64)] + [(n, C.c_double) for n in (
-        "lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + [("rounding", C.c_int32), ("seed", C.c_uint32)]
+        "lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")]
 
 
 _LIB = None
@@ -234,6 +235,9 @@ def _lib():
         lib.salr_adamw_step.argtypes = [C.POINTER(salr_adamw_plan_t), C.POINTER(salr_adamw_step_args_t), C.c_void_p,
                                         C.c_void_p]
         lib.salr_adamw_step.restype = C.c_int
+        lib.salr_adamw_step_random.argtypes = [C.POINTER(salr_adamw_plan_t), C.POINTER(salr_adamw_step_args_t),
+                                               C.c_uint32, C.c_void_p, C.c_void_p]
+        lib.salr_adamw_step_random.restype = C.c_int
         lib.salr_probe_stream_read.argtypes = [C.c_void_p, C.c_size_t, C.c_void_p, C.c_int32, C.c_void_p]
         lib.salr_probe_stream_read.restype = C.c_int
         lib.salr_probe_mfma.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]
@@ -1121,8 +1125,8 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     """One AdamW step (number `step`, from 1) over every tensor of the plan,
     in place and in one launch (salr_adamw_step).
 
-    seed (0 .. 2^32 - 1, one for a whole training): 8-bit states are rounded
-    by chance, so that m and v follow their formulas in the mean (the chance
+    seed (0 .. 2^32 - 1, one for each plan and a whole training): 8-bit states
+    are rounded by chance (salr_adamw_step_random), so that m and v follow their formulas in the mean (the chance
     is fixed by the seed and the step's number).  Without it each takes the
     nearest code, which is right for one step only: over many, v stays where
     it is, as a step changes it by less than half a code.  Float states are
@@ -1134,15 +1138,17 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
     torch = _torch()
     if seed is not None and not 0 <= seed < 1 << 32:
         raise ValueError("seed must be in [0, 2^32)")
-    args, dev = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed is not None,
-                                       seed or 0), plan.device
+    args, dev = salr_adamw_step_args_t(step, lr, beta1, beta2, eps, weight_decay, grad_scale), plan.device
     index = dev.index
     at = _stream_here(index, stream)
     if at is None:
         with _Place(dev, stream):
             return adamw_step(plan, step, lr, beta1, beta2, eps, weight_decay, grad_scale, dyn, seed=seed)
     d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (4 if seed is None else 5,), index)
-    _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, at), "salr_adamw_step")
+    if seed is None:
+        _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, at), "salr_adamw_step")
+    else:
+        _check(_lib().salr_adamw_step_random(C.byref(plan.desc), C.byref(args), seed, d, at), "salr_adamw_step_random")
 
 
 def probe_stream_read(src, sink, workgroups: int, stream=None):

@@ -281,6 +281,45 @@ int64_t adamw_small_chunks(int32_t count, F n) {
   return adamw_chunks(count, salr::kAdamwLargeChunk, n) < 0 ? -1 : chunks;
 }
 
+int adamw_step(const salr_adamw_plan_t* plan, const salr_adamw_step_args_t* args, bool random, uint32_t seed,
+               const float* dyn, void* stream) {
+  if (!plan || !args) return SALR_ERR_INVALID_ARG;
+  if (!plan->table || !aligned16(plan->table) || plan->count < 0 || plan->count > kMaxTensors || plan->chunks < 0 ||
+      plan->chunks > max_chunks(salr::adamw_chunk(plan->state_type == SALR_STATE_8BIT, plan->has_master != 0)) ||
+      !type_ok(plan->p_type) || !type_ok(plan->g_type) ||
+      (plan->state_type != SALR_STATE_F32 && plan->state_type != SALR_STATE_8BIT) ||
+      (plan->has_master && plan->p_type != SALR_TYPE_BF16))
+    return SALR_ERR_INVALID_ARG;
+  const auto nonneg = [](double v) { return v >= 0 && std::isfinite(v); };
+  if (!nonneg(args->eps) || !nonneg(args->weight_decay)) return SALR_ERR_INVALID_ARG;
+  if (!(args->beta1 >= 0 && args->beta1 < 1) || !(args->beta2 >= 0 && args->beta2 < 1)) return SALR_ERR_INVALID_ARG;
+  if (!dyn && (args->step < 1 || !nonneg(args->lr))) return SALR_ERR_INVALID_ARG;
+  if (!aligned4(dyn)) return SALR_ERR_INVALID_ARG;
+  salr::AdamwArgs a{};
+  a.tensors = static_cast<const salr::AdamwTensor*>(plan->table);
+  a.chunks = reinterpret_cast<const salr::AdamwChunk*>(static_cast<const char*>(plan->table) +
+                                                       table_records_bytes(plan->count));
+  a.n_chunks = plan->chunks;
+  a.dyn = dyn;
+  a.beta1 = (float)args->beta1;
+  a.beta2 = (float)args->beta2;
+  a.rest1 = (float)(1.0 - args->beta1);
+  a.rest2 = (float)(1.0 - args->beta2);
+  a.eps = (float)args->eps;
+  a.weight_decay = (float)args->weight_decay;
+  a.seed = seed;
+  a.step = (float)args->step;
+  if (!dyn) {
+    a.grad_scale = (float)args->grad_scale;
+    a.decay = (float)(1.0 - args->lr * args->weight_decay);
+    a.rate = (float)(args->lr / (1.0 - std::pow(args->beta1, (double)args->step)));
+    a.inv_sqrt_bias2 = (float)(1.0 / std::sqrt(1.0 - std::pow(args->beta2, (double)args->step)));
+  }
+  return status(salr::launch_adamw(a, plan->p_type == SALR_TYPE_F32, plan->g_type == SALR_TYPE_F32,
+                                   plan->state_type == SALR_STATE_8BIT, plan->has_master != 0,
+                                   random, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -339,42 +378,12 @@ int salr_adamw_plan(const salr_adamw_tensor_t* tensors, int32_t count, int32_t p
 
 int salr_adamw_step(const salr_adamw_plan_t* plan, const salr_adamw_step_args_t* args, const float* dyn,
                     void* stream) {
-  if (!plan || !args) return SALR_ERR_INVALID_ARG;
-  if (!plan->table || !aligned16(plan->table) || plan->count < 0 || plan->count > kMaxTensors || plan->chunks < 0 ||
-      plan->chunks > max_chunks(salr::adamw_chunk(plan->state_type == SALR_STATE_8BIT, plan->has_master != 0)) ||
-      !type_ok(plan->p_type) || !type_ok(plan->g_type) ||
-      (plan->state_type != SALR_STATE_F32 && plan->state_type != SALR_STATE_8BIT) ||
-      (plan->has_master && plan->p_type != SALR_TYPE_BF16))
-    return SALR_ERR_INVALID_ARG;
-  const auto nonneg = [](double v) { return v >= 0 && std::isfinite(v); };
-  if (!nonneg(args->eps) || !nonneg(args->weight_decay)) return SALR_ERR_INVALID_ARG;
-  if (!(args->beta1 >= 0 && args->beta1 < 1) || !(args->beta2 >= 0 && args->beta2 < 1)) return SALR_ERR_INVALID_ARG;
-  if (!dyn && (args->step < 1 || !nonneg(args->lr))) return SALR_ERR_INVALID_ARG;
-  if (args->rounding != SALR_ROUND_NEAREST && args->rounding != SALR_ROUND_RANDOM) return SALR_ERR_INVALID_ARG;
-  if (!aligned4(dyn)) return SALR_ERR_INVALID_ARG;
-  salr::AdamwArgs a{};
-  a.tensors = static_cast<const salr::AdamwTensor*>(plan->table);
-  a.chunks = reinterpret_cast<const salr::AdamwChunk*>(static_cast<const char*>(plan->table) +
-                                                       table_records_bytes(plan->count));
-  a.n_chunks = plan->chunks;
-  a.dyn = dyn;
-  a.beta1 = (float)args->beta1;
-  a.beta2 = (float)args->beta2;
-  a.rest1 = (float)(1.0 - args->beta1);
-  a.rest2 = (float)(1.0 - args->beta2);
-  a.eps = (float)args->eps;
-  a.weight_decay = (float)args->weight_decay;
-  a.seed = args->seed;
-  a.step = (float)args->step;
-  if (!dyn) {
-    a.grad_scale = (float)args->grad_scale;
-    a.decay = (float)(1.0 - args->lr * args->weight_decay);
-    a.rate = (float)(args->lr / (1.0 - std::pow(args->beta1, (double)args->step)));
-    a.inv_sqrt_bias2 = (float)(1.0 / std::sqrt(1.0 - std::pow(args->beta2, (double)args->step)));
-  }
-  return status(salr::launch_adamw(a, plan->p_type == SALR_TYPE_F32, plan->g_type == SALR_TYPE_F32,
-                                   plan->state_type == SALR_STATE_8BIT, plan->has_master != 0,
-                                   args->rounding == SALR_ROUND_RANDOM, static_cast<hipStream_t>(stream)));
+  return adamw_step(plan, args, false, 0, dyn, stream);
+}
+
+int salr_adamw_step_random(const salr_adamw_plan_t* plan, const salr_adamw_step_args_t* args, uint32_t seed,
+                           const float* dyn, void* stream) {
+  return adamw_step(plan, args, true, seed, dyn, stream);
 }
 
 }  // extern "C"

@@ -172,15 +172,19 @@ def test_binding_refuses_host_tensors():
         srl.adamw_plan([h], [h], [h.float()], [h.float()], m_scale=[h.float()], v_scale=[h.float()])
 
 
-def test_adamw_rounding_refusals():
+def test_adamw_step_random_refusals():
     lib = srl.lib()
     d = B.salr_adamw_plan_t(P, 0, 1, 0, 1, 1, 0)
-    args = lambda rounding, seed=5: B.salr_adamw_step_args_t(1, 1e-3, 0.9, 0.999, 1e-8, 0.01, 1.0, rounding, seed)
-    run = lambda a, dyn=None: lib.salr_adamw_step(C.byref(d), C.byref(a), dyn, None)
-    assert run(args(0)) == 0 and run(args(1)) == 0 and run(args(1, 2 ** 32 - 1), dyn=P) == 0
-    assert run(args(2)) == -1 and run(args(-1)) == -1 and run(args(1), dyn=P + 2) == -1
-    # the binding's record has the header's layout: 64 bytes in all
-    assert C.sizeof(B.salr_adamw_step_args_t) == 64 and B.salr_adamw_step_args_t.seed.offset == 60
+    args = lambda **kw: B.salr_adamw_step_args_t(*{**dict(step=1, lr=1e-3, b1=.9, b2=.999, eps=1e-8, wd=.01, gs=1.),
+                                                   **kw}.values())
+    run = lambda a, dyn=None, seed=5: lib.salr_adamw_step_random(C.byref(d), C.byref(a), seed, dyn, None)
+    assert run(args()) == 0 and run(args(), dyn=P) == 0 and run(args(), seed=2 ** 32 - 1) == 0
+    for bad in (dict(step=0), dict(lr=-1.), dict(b1=1.), dict(b2=1.), dict(eps=-1.), dict(wd=-1.)):
+        assert run(args(**bad)) == -1, bad
+    assert run(args(), dyn=P + 2) == -1
+    assert lib.salr_adamw_step_random(None, C.byref(args()), 5, None, None) == -1
+    assert lib.salr_adamw_step_random(C.byref(d), None, 5, None, None) == -1
+    assert C.sizeof(B.salr_adamw_step_args_t) == 56         # (as callers of salr_adamw_step were built)
     for seed in (-1, 2 ** 32):
         with pytest.raises(ValueError, match="seed"):
             srl.adamw_step(None, 1, 1e-3, seed=seed)
