@@ -46,6 +46,9 @@ Parity status of each function (what pins it, see tests/test_oracle_*.py):
                                    pinned: torch's e4m3 conversion over all
                                    codes, exact round trips, the half-step
                                    bound, planted mistakes
+  adamw.encode_random              pinned: codes stay, means over a grid of
+                                   chances, the recurrence of v over 900
+                                   steps, a planted chance
   The pages print no worked example and no intermediate values, so no
   function is pinned to a number printed on the pages.
 """
