@@ -702,6 +702,105 @@ int salr_adamw_step_random(const salr_adamw_plan_t* plan,
                            const salr_adamw_step_args_t* args, uint32_t seed,
                            const float* dyn, void* stream);
 
+/*
+ * Adapters of many requests: one frozen layer serves (or trains) many
+ * fine-tuned low-rank adapters at once, each token its own request's.  Next to
+ * salr_linear_forward, whose layer all of them share, with a = ids[t]:
+ *     Y[t]  = base[t] + scale_a (X[t] A_a) B_a
+ * and next to salr_linear_backward, for the upstream gradient dY = dL/dY:
+ *     G[t]  = scale_a dY[t] B_a^T
+ *     dX[t] = base[t] + G[t] A_a^T
+ *     dA_a  = sum_t X[t]^T G[t]      dB_a = scale_a sum_t (X[t] A_a)^T dY[t]
+ * (sums over the tokens of adapter a).  A token whose id is outside [0,
+ * count) has no adapter: its output is base, and its inputs are not used.
+ * Products accumulate in fp32 and every output is rounded once: X A and G meet
+ * the next product as sums of bf16 values that hold 16 bits of them (24 for the
+ * float gradients).  Results do not depend on timing: no sums by
+ * floating-point atomics.
+ */
+#define SALR_ADAPTERS_MAX 4096
+
+/* `count` adapters of one N x K layer, stacked, each as a layer stores its
+ * own.  Unused ranks of an adapter may hold anything. */
+typedef struct salr_adapters {
+  int32_t count;         /* 1 .. SALR_ADAPTERS_MAX                          */
+  int32_t r;             /* ranks stored per adapter: 8 .. 256, in eights   */
+  int64_t N;             /* outputs, 1 .. 2^20                              */
+  int64_t K;             /* inputs, 8 .. 2^20, in eights                    */
+  const uint16_t* a;     /* device bf16 [count][r][K]                       */
+  const uint16_t* b;     /* device bf16 [count][N][r]                       */
+  const int32_t* ranks;  /* device [count]: adapter a uses its first ranks[a]
+                          * ranks (0: none; clamped to r); NULL: all of r   */
+  const float* scales;   /* device [count], or NULL: ones                   */
+} salr_adapters_t;
+
+/* A batch's tokens sorted by adapter: the entries are salr_adapters_plan's. */
+typedef struct salr_adapters_plan {
+  void* buffer;          /* device, the caller's                            */
+  int64_t M;
+  int32_t count;
+} salr_adapters_plan_t;
+
+/* Bytes of the buffer of a plan for M tokens and `count` adapters (`out` host;
+ * 0 <= M < 2^31 - 65536).  Errors: INVALID_ARG. */
+int salr_adapters_plan_bytes(int64_t M, int32_t count, size_t* out);
+
+/*
+ * salr_adapters_plan - lay a batch out: once a batch, for every projection of
+ * every layer that runs it with `count` adapters.
+ * ids     device int32 [M], any values (see above); read when the plan runs.
+ * buffer  device, at least salr_adapters_plan_bytes; it belongs to the plan
+ *         until the last call that uses it has run.  A captured plan lays out
+ *         the ids of each replay.
+ * out     host.
+ * Asynchronous on `stream`, capturable.  Errors: INVALID_ARG, WORKSPACE, HIP.
+ */
+int salr_adapters_plan(const int32_t* ids, int64_t M, int32_t count,
+                       void* buffer, size_t buffer_bytes,
+                       salr_adapters_plan_t* out, void* stream);
+
+/* Workspace bytes of salr_adapters_forward, or with backward != 0 of
+ * salr_adapters_backward, for plans of at most M_max tokens (`out` host).
+ * Errors: INVALID_ARG, UNSUPPORTED (as the calls). */
+int salr_adapters_ws_bytes(int32_t count, int64_t N, int64_t K, int32_t r,
+                           int64_t M_max, int32_t backward, size_t* out);
+
+/*
+ * salr_adapters_forward - Y = base + scale (X A) B, each token its adapter's.
+ * A     host pointer to the adapters; P host pointer to a plan of as many.
+ * X     device bf16 [P->M][K].
+ * base  device bf16 [P->M][N] (the shared projection's output; may be Y
+ *       itself), or NULL: zeros.
+ * Y     device bf16 [P->M][N]; overlaps nothing else of the call.
+ * ws    device, salr_adapters_ws_bytes for some M_max >= P->M; contents on
+ *       entry do not matter.  Calls that share it (or captured graphs of such
+ *       calls) must be ordered.
+ * Asynchronous on `stream`, capturable.  Errors: INVALID_ARG, WORKSPACE, HIP.
+ */
+int salr_adapters_forward(const salr_adapters_t* A,
+                          const salr_adapters_plan_t* P, const uint16_t* X,
+                          const uint16_t* base, uint16_t* Y, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * salr_adapters_backward - dX, dA and dB of every adapter at once (formulas
+ * above).
+ * X, dY  device bf16 [P->M][K] and [P->M][N].
+ * base   device bf16 [P->M][K] (the shared projection's dX, from
+ *        salr_linear_backward; may be dX itself), or NULL: zeros.
+ * dX     device bf16 [P->M][K], or NULL to skip it.
+ * dA, dB device float [count][r][K] and [count][N][r], the layout of a and b;
+ *        overwritten: adapters without tokens and unused ranks get zeros.
+ * ws     as for the forward, with backward != 0.
+ * Limits: N % 8 == 0 (else UNSUPPORTED).  Asynchronous on `stream`,
+ * capturable.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP.
+ */
+int salr_adapters_backward(const salr_adapters_t* A,
+                           const salr_adapters_plan_t* P, const uint16_t* X,
+                           const uint16_t* dY, const uint16_t* base,
+                           uint16_t* dX, float* dA, float* dB, void* ws,
+                           size_t ws_bytes, void* stream);
+
 /* Static English text for a status code (never NULL). */
 const char* salr_status_string(int status);
 

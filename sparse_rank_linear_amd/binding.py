@@ -54,6 +54,11 @@ EXPORTS = (
     "salr_adamw_plan",
     "salr_adamw_step",
     "salr_adamw_step_random",
+    "salr_adapters_plan_bytes",
+    "salr_adapters_plan",
+    "salr_adapters_ws_bytes",
+    "salr_adapters_forward",
+    "salr_adapters_backward",
     # include/salr_probe.h
     "salr_probe_stream_read",
     "salr_probe_mfma",
@@ -152,6 +157,23 @@ class salr_adamw_step_args_t(C.Structure):
         "lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")]
 
 
+class salr_adapters_t(C.Structure):
+    _fields_ = [
+        ("count", C.c_int32),
+        ("r", C.c_int32),
+        ("N", C.c_int64),
+        ("K", C.c_int64),
+        ("a", C.c_void_p),
+        ("b", C.c_void_p),
+        ("ranks", C.c_void_p),
+        ("scales", C.c_void_p),
+    ]
+
+
+class salr_adapters_plan_t(C.Structure):
+    _fields_ = [("buffer", C.c_void_p), ("M", C.c_int64), ("count", C.c_int32)]
+
+
 _LIB = None
 
 
@@ -238,6 +260,20 @@ def _lib():
         lib.salr_adamw_step_random.argtypes = [C.POINTER(salr_adamw_plan_t), C.POINTER(salr_adamw_step_args_t),
                                                C.c_uint32, C.c_void_p, C.c_void_p]
         lib.salr_adamw_step_random.restype = C.c_int
+        lib.salr_adapters_plan_bytes.argtypes = [C.c_int64, C.c_int32, C.POINTER(C.c_size_t)]
+        lib.salr_adapters_plan_bytes.restype = C.c_int
+        lib.salr_adapters_plan.argtypes = [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_size_t,
+                                           C.POINTER(salr_adapters_plan_t), C.c_void_p]
+        lib.salr_adapters_plan.restype = C.c_int
+        lib.salr_adapters_ws_bytes.argtypes = [C.c_int32, C.c_int64, C.c_int64, C.c_int32, C.c_int64, C.c_int32,
+                                               C.POINTER(C.c_size_t)]
+        lib.salr_adapters_ws_bytes.restype = C.c_int
+        lib.salr_adapters_forward.argtypes = [C.POINTER(salr_adapters_t), C.POINTER(salr_adapters_plan_t), C.c_void_p,
+                                              C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+        lib.salr_adapters_forward.restype = C.c_int
+        lib.salr_adapters_backward.argtypes = [C.POINTER(salr_adapters_t), C.POINTER(salr_adapters_plan_t)] + [
+            C.c_void_p] * 7 + [C.c_size_t, C.c_void_p]
+        lib.salr_adapters_backward.restype = C.c_int
         lib.salr_probe_stream_read.argtypes = [C.c_void_p, C.c_size_t, C.c_void_p, C.c_int32, C.c_void_p]
         lib.salr_probe_stream_read.restype = C.c_int
         lib.salr_probe_mfma.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]
@@ -1149,6 +1185,185 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
         _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, at), "salr_adamw_step")
     else:
         _check(_lib().salr_adamw_step_random(C.byref(plan.desc), C.byref(args), seed, d, at), "salr_adamw_step_random")
+
+
+# ----------------------------------------------------------------------------
+# Adapters of many requests (device, stream and allocation as for the calls
+# around the experts).
+ADAPTERS_MAX = 4096
+
+
+@dataclass
+class SalrAdapters:
+    """`count` low-rank adapters of one layer, stacked as include/salr.h lays
+    them out (salr_adapters_t): a bf16 [count][r][K], b bf16 [count][N][r];
+    optionally how many ranks each uses (ranks, device int32 [count]) and its
+    scale (scales, device float [count])."""
+
+    a: object
+    b: object
+    ranks: object = None
+    scales: object = None
+
+    def __post_init__(self):
+        torch = _torch()
+        a, b = self.a, self.b
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError("a must be [count][r][K] and b [count][N][r]")
+        (self.count, self.r, self.K), self.N = a.shape, b.shape[1]
+        index = a.get_device()
+        check = lambda t, name, dtype, shape: None if t is None else _ptr(t, name, dtype, shape, index)
+        self._desc = salr_adapters_t(self.count, self.r, self.N, self.K,
+                                     check(a, "a", torch.bfloat16, (self.count, self.r, self.K)),
+                                     check(b, "b", torch.bfloat16, (self.count, self.N, self.r)),
+                                     check(self.ranks, "ranks", torch.int32, (self.count,)),
+                                     check(self.scales, "scales", torch.float32, (self.count,)))
+        self._held = (a, b, self.ranks, self.scales)   # what the descriptor points to
+
+    @classmethod
+    def empty(cls, count, N, K, r, device="cuda"):
+        """Zeroed adapters (the zero adapter adds nothing)."""
+        torch = _torch()
+        return cls(torch.zeros((count, r, K), dtype=torch.bfloat16, device=device),
+                   torch.zeros((count, N, r), dtype=torch.bfloat16, device=device))
+
+    def descriptor(self) -> salr_adapters_t:
+        a, b, ranks, scales = self._held
+        if a is not self.a or b is not self.b or ranks is not self.ranks or scales is not self.scales:
+            self.__post_init__()
+        return self._desc
+
+
+@dataclass
+class AdaptersPlan:
+    """A batch's tokens sorted by adapter (include/salr.h,
+    salr_adapters_plan_t); holds its buffer."""
+
+    desc: salr_adapters_plan_t
+    buffer: object
+
+    @property
+    def M(self):
+        return self.desc.M
+
+
+def adapters_plan_bytes(M: int, count: int) -> int:
+    out = C.c_size_t()
+    _check(_lib().salr_adapters_plan_bytes(M, count, C.byref(out)), "salr_adapters_plan_bytes")
+    return out.value
+
+
+def adapters_plan(ids, count: int, plan: AdaptersPlan | None = None, stream=None) -> AdaptersPlan:
+    """The batch whose token t belongs to adapter ids[t] (device int32 [M]; an
+    id outside [0, count): to none), laid out for adapters_forward and
+    adapters_backward of any layer with `count` adapters (salr_adapters_plan).
+    plan: an earlier one of a batch at least as long, whose buffer is used
+    again (asynchronous; it then describes this batch)."""
+    torch = _torch()
+    if ids.dim() != 1:
+        raise ValueError("ids must be [M]")
+    M, dev = ids.shape[0], ids.device
+    index = dev.index
+    at = _stream_here(index, stream)
+    if at is None:
+        with _Place(dev, stream):
+            return adapters_plan(ids, count, plan)
+    ids_at = _ptr(ids, "ids", torch.int32, (M,), index)
+    if plan is None:
+        buffer = torch.empty(adapters_plan_bytes(M, count), dtype=torch.uint8, device=dev)
+        plan = AdaptersPlan(salr_adapters_plan_t(), buffer)
+    else:
+        buffer = plan.buffer
+        if buffer.get_device() != index:
+            raise ValueError(f"plan must be on cuda:{index} (is on {buffer.device})")
+    _check(_lib().salr_adapters_plan(ids_at if M else None, M, count, buffer.data_ptr(), buffer.numel(),
+                                     C.byref(plan.desc), at), "salr_adapters_plan")
+    return plan
+
+
+def adapters_ws_bytes(count: int, N: int, K: int, r: int, M_max: int, backward: bool = False) -> int:
+    out = C.c_size_t()
+    _check(_lib().salr_adapters_ws_bytes(count, N, K, r, M_max, bool(backward), C.byref(out)),
+           "salr_adapters_ws_bytes")
+    return out.value
+
+
+def adapters_workspace(adapters: SalrAdapters, M_max: int, backward: bool = False):
+    """A workspace for adapters_forward (or adapters_backward) of at most M_max
+    tokens."""
+    torch = _torch()
+    return torch.empty(adapters_ws_bytes(adapters.count, adapters.N, adapters.K, adapters.r, M_max, backward),
+                       dtype=torch.uint8, device=adapters.a.device)
+
+
+def _adapters_ws(ws, adapters, M, backward, index):
+    if ws is None:
+        ws = adapters_workspace(adapters, M, backward)
+    elif ws.get_device() != index:
+        raise ValueError(f"ws must be on cuda:{index} (is on {ws.device})")
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws
+
+
+def adapters_forward(adapters: SalrAdapters, plan: AdaptersPlan, X, base=None, Y=None, ws=None, stream=None):
+    """Y[t] = base[t] + scale_a (X[t] A_a) B_a with a token t's adapter (bf16
+    [M][N]): the adapters of many requests beside the projection they share,
+    whose output is base (may be Y; None: zeros) (salr_adapters_forward)."""
+    torch = _torch()
+    M, dev = plan.desc.M, X.device
+    index = dev.index
+    at = _stream_here(index, stream)
+    if at is None:
+        with _Place(dev, stream):
+            return adapters_forward(adapters, plan, X, base, Y, ws)
+    d, bf16, out = adapters.descriptor(), torch.bfloat16, (M, adapters.N)
+    if adapters.a.get_device() != index or plan.buffer.get_device() != index:
+        raise ValueError(f"adapters and plan must be on cuda:{index}")
+    if Y is None:
+        Y = torch.empty(out, dtype=bf16, device=dev)
+    ws = _adapters_ws(ws, adapters, M, False, index)
+    _check(_lib().salr_adapters_forward(
+        C.byref(d), C.byref(plan.desc), _ptr(X, "X", bf16, (M, adapters.K), index),
+        None if base is None else _ptr(base, "base", bf16, out, index), _ptr(Y, "Y", bf16, out, index),
+        ws.data_ptr(), ws.numel() * ws.element_size(), at), "salr_adapters_forward")
+    return Y
+
+
+def adapters_backward(adapters: SalrAdapters, plan: AdaptersPlan, X, dY, base=None, dX=None, dA=None, dB=None,
+                      need_dx: bool = True, ws=None, stream=None):
+    """The gradients of adapters_forward, of every adapter at once: (dX bf16
+    [M][K], to which base, the shared projection's own dX, is added; dA float
+    [count][r][K]; dB float [count][N][r]) (salr_adapters_backward).  Adapters
+    without tokens and unused ranks get zeros; need_dx = False skips dX (it is
+    then None)."""
+    torch = _torch()
+    M, dev = plan.desc.M, X.device
+    index = dev.index
+    at = _stream_here(index, stream)
+    if at is None:
+        with _Place(dev, stream):
+            return adapters_backward(adapters, plan, X, dY, base, dX, dA, dB, need_dx, ws)
+    d, bf16, f32, inp = adapters.descriptor(), torch.bfloat16, torch.float32, (M, adapters.K)
+    if adapters.a.get_device() != index or plan.buffer.get_device() != index:
+        raise ValueError(f"adapters and plan must be on cuda:{index}")
+    if not need_dx:
+        dX = base = None
+    elif dX is None:
+        dX = torch.empty(inp, dtype=bf16, device=dev)
+    if dA is None:
+        dA = torch.empty(adapters.a.shape, dtype=f32, device=dev)
+    if dB is None:
+        dB = torch.empty(adapters.b.shape, dtype=f32, device=dev)
+    ws = _adapters_ws(ws, adapters, M, True, index)
+    _check(_lib().salr_adapters_backward(
+        C.byref(d), C.byref(plan.desc), _ptr(X, "X", bf16, inp, index),
+        _ptr(dY, "dY", bf16, (M, adapters.N), index),
+        None if base is None else _ptr(base, "base", bf16, inp, index),
+        None if dX is None else _ptr(dX, "dX", bf16, inp, index), _ptr(dA, "dA", f32, adapters.a.shape, index),
+        _ptr(dB, "dB", f32, adapters.b.shape, index), ws.data_ptr(), ws.numel() * ws.element_size(), at),
+        "salr_adapters_backward")
+    return dX, dA, dB
 
 
 def probe_stream_read(src, sink, workgroups: int, stream=None):

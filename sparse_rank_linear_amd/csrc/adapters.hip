@@ -1,0 +1,637 @@
+// Adapters of many requests beside a shared projection, and their gradients
+// (include/salr.h, salr_adapters_forward and salr_adapters_backward).
+//
+// With a = ids[t] and s_a its scale:
+//   T[t][j] = sum_k X[t][k] A_a[j][k],   Y[t][n] = base[t][n] + s_a sum_j T[t][j] B_a[n][j]
+//   G[t][j] = s_a sum_n dY[t][n] B_a[n][j],   dX[t][k] = base[t][k] + sum_j G[t][j] A_a[j][k]
+//   dA_a[j][k] = sum_t G[t][j] X[t][k],   dB_a[n][j] = s_a sum_t dY[t][n] T[t][j]
+// A plan sorts the tokens by adapter once for all the projections of a batch
+// and cuts them into tiles of up to 64 tokens of one adapter, so every product
+// is a matrix product of one adapter with a tile's (gathered) rows on the
+// matrix cores.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "salr_adapters.hpp"
+#include "salr_device.hpp"
+
+namespace salr {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kSubs = kAdapterTile / 16;  // 16-token sides of a tile
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+// ---- the plan ----
+
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v, int lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_up((int)v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// The largest g in [0, n] with start[g] <= x, of those the last (start
+// ascending, start[0] = 0): the group that item x belongs to.
+__device__ __forceinline__ int group_of(const uint32_t* start, int n, uint32_t x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// One workgroup sorts: a stable counting sort over the groups 0..count (the
+// last: no adapter), each wave on its own stretch of the tokens.  One pass of
+// LDS atomics counts, prefix sums place the groups and the waves within them,
+// and a second pass places 64 tokens at a time, one ballot for each adapter
+// among them.  Then the lists of tiles and chunks.
+__global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_t* ids, AdapterPlan p, int waves) {
+  extern __shared__ uint32_t sm[];
+  const int G = p.count + 1;
+  uint32_t* cnt = sm;                          // [waves][G]
+  uint32_t* off = cnt + waves * G;             // [G + 1] tokens before each group
+  uint32_t* tile = off + G + 1;                // [G + 1] tiles before each group
+  uint32_t* chunk = tile + G + 1;              // [G + 1] chunks
+  uint32_t* part = chunk + G + 1;              // [G + 1] partial sums
+  __shared__ uint32_t wsum[4][kPlanWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < waves * G; i += kPlanThreads) cnt[i] = 0;
+  __syncthreads();
+  const int64_t M = p.M;
+  const int64_t each = ((M + waves - 1) / waves + 63) / 64 * 64;
+  const int64_t t0 = min(M, wave * each), t1 = min(M, t0 + each);  // (no tokens from wave `waves` on)
+  const auto group = [&](int64_t t) -> int {
+    const uint32_t id = (uint32_t)ids[t];
+    return id < (uint32_t)p.count ? (int)id : p.count;
+  };
+  for (int64_t t = t0 + lane; t < t1; t += 64) atomicAdd(&cnt[wave * G + group(t)], 1u);
+  __syncthreads();
+  // each thread a run of groups: their totals, then what lies before them
+  const int per = (G + kPlanThreads - 1) / kPlanThreads;
+  const int g0 = min(G, tid * per), g1 = min(G, g0 + per);
+  uint32_t n[4] = {0, 0, 0, 0};
+  const auto add = [&](int g, uint32_t c) {
+    const uint32_t ch = g < p.count ? (c + p.chunk - 1) / p.chunk : 0;
+    n[0] += c;
+    n[1] += (c + kAdapterTile - 1) / kAdapterTile;
+    n[2] += ch;
+    n[3] += ch > 1 ? ch : 0;
+  };
+  for (int g = g0; g < g1; ++g) {
+    uint32_t run = 0;
+    for (int w = 0; w < waves; ++w) {
+      const uint32_t c = cnt[w * G + g];
+      cnt[w * G + g] = run;
+      run += c;
+    }
+    off[g] = run;  // (the group's own count until it is placed below)
+    add(g, run);
+  }
+  uint32_t before[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t incl = wave_prefix(n[q], lane);
+    if (lane == 63) wsum[q][wave] = incl;
+    before[q] = incl - n[q];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    for (int w = 0; w < wave; ++w) before[q] += wsum[q][w];
+    n[q] = before[q];
+  }
+  for (int g = g0; g < g1; ++g) {
+    const uint32_t c = off[g];
+    off[g] = n[0];
+    tile[g] = n[1];
+    chunk[g] = n[2];
+    part[g] = n[3];
+    for (int w = 0; w < waves; ++w) cnt[w * G + g] += n[0];
+    add(g, c);
+    if (g == G - 1) {
+      off[G] = n[0];
+      tile[G] = n[1];
+      chunk[G] = n[2];
+      part[G] = n[3];
+    }
+  }
+  __syncthreads();
+  for (int g = tid; g <= G; g += kPlanThreads) {
+    p.offsets[g] = (int32_t)off[g];
+    p.parts[g] = (int32_t)part[g];
+  }
+  if (tid == 0) {
+    p.head[0] = (int32_t)tile[G];
+    p.head[1] = (int32_t)chunk[G];
+  }
+  // place the tokens
+  for (int64_t b = t0; b < t1; b += 64) {
+    const int64_t t = b + lane;
+    const bool live = t < t1;
+    const int g = live ? group(t) : -1;
+    uint64_t todo = __ballot(live);
+    while (todo) {
+      const int first = __builtin_ctzll(todo);
+      const int cur = __builtin_amdgcn_readlane(g, first);
+      const uint64_t same = __ballot(g == cur);
+      uint32_t* at = &cnt[wave * G + cur];
+      if (g == cur) p.order[*at + __popcll(same & ((1ull << lane) - 1ull))] = (int32_t)t;
+      __builtin_amdgcn_wave_barrier();
+      if (lane == first) *at += (uint32_t)__popcll(same);
+      __builtin_amdgcn_wave_barrier();
+      todo &= ~same;
+    }
+  }
+  // the lists
+  for (uint32_t i = tid; i < tile[G]; i += kPlanThreads) {
+    const int g = group_of(tile, G, i);
+    const uint32_t b = off[g] + (i - tile[g]) * kAdapterTile;
+    p.tiles[i] = AdapterTile{g, (int32_t)b, (int32_t)min(off[g + 1], b + kAdapterTile), -1};
+  }
+  for (uint32_t i = tid; i < chunk[G]; i += kPlanThreads) {
+    const int g = group_of(chunk, G, i);
+    const uint32_t b = off[g] + (i - chunk[g]) * p.chunk;
+    const bool alone = chunk[g + 1] - chunk[g] == 1;
+    p.chunks[i] = AdapterTile{g, (int32_t)b, (int32_t)min(off[g + 1], b + (uint32_t)p.chunk),
+                              alone ? -1 : (int32_t)(part[g] + i - chunk[g])};
+  }
+}
+
+__device__ __forceinline__ int live_ranks(const AdapterCommon& c, int adapter) {
+  return c.ranks ? min(max(c.ranks[adapter], 0), c.r) : c.r;
+}
+__device__ __forceinline__ float scale_of(const AdapterCommon& c, int adapter) {
+  return c.scales ? c.scales[adapter] : 1.f;
+}
+
+// x as a sum of bf16 values, the first the nearest to it: two of them hold 16
+// of a float's 24 bits, three all of them.  An infinite first one is all.
+__device__ __forceinline__ void limbs(float x, uint16_t* w, int n) {
+  w[0] = f32_to_bf16(x);
+  float rest = x - bf16_to_f32(w[0]);
+  if ((w[0] & 0x7F80u) == 0x7F80u) rest = 0.f;
+  for (int i = 1; i < n; ++i) {
+    w[i] = f32_to_bf16(rest);
+    rest -= bf16_to_f32(w[i]);
+  }
+}
+
+// ---- down: T = X W^T for one tile, RT x 16 ranks, one piece of the columns ----
+//
+// D[rank][token] tiles; both operands run along the columns and come straight
+// from memory, 16 bytes a lane.  Each wave takes every kWaves-th 64 columns of
+// the piece; the waves' sums meet in LDS, in wave order.
+template <int RT>
+__global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterCommon c, AdapterDown j0, AdapterDown j1,
+                                                                int groups) {
+  __shared__ f32x4_t sums[kWaves][RT][64];
+  const AdapterPlan& p = c.plan;
+  if ((int)blockIdx.x >= p.head[0]) return;
+  const AdapterTile t = p.tiles[blockIdx.x];
+  if (t.adapter >= p.count) return;
+  const AdapterDown j = blockIdx.z ? j1 : j0;
+  const int split = blockIdx.y / groups, rank0 = (blockIdx.y % groups) * RT * 16;
+  const int live = live_ranks(c, t.adapter);
+  if (split >= j.splits || rank0 >= live) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int n = t.end - t.begin, subs = (n + 15) / 16;
+  // (tokens past the tile's last and ranks past the live ones repeat those:
+  // what comes of them is not used)
+  const uint16_t* xr[kSubs];
+#pragma unroll
+  for (int s = 0; s < kSubs; ++s)
+    xr[s] = j.X + (int64_t)p.order[t.begin + min(16 * s + i, n - 1)] * j.K + 8 * g;
+  const uint16_t* wr[RT];
+#pragma unroll
+  for (int a = 0; a < RT; ++a)
+    wr[a] = j.W + ((int64_t)t.adapter * c.r + min(rank0 + 16 * a + i, live - 1)) * j.K + 8 * g;
+  f32x4_t acc[RT][kSubs];
+#pragma unroll
+  for (int a = 0; a < RT; ++a)
+#pragma unroll
+    for (int s = 0; s < kSubs; ++s) acc[a][s] = zero4();
+  const int64_t k0 = (int64_t)split * j.cols, k1 = min(j.K, k0 + j.cols);
+  const auto body = [&](auto nsubs) __attribute__((always_inline)) {
+    constexpr int NS = decltype(nsubs)::value;
+    for (int64_t k = k0 + 64 * wave; k < k1; k += 64 * kWaves) {
+      u32x4_t x[2][NS], w[2][RT];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = k + 32 * h + 8 * g < k1;
+#pragma unroll
+        for (int a = 0; a < RT; ++a) w[h][a] = in ? load16(wr[a] + k + 32 * h) : zero_u4();
+#pragma unroll
+        for (int s = 0; s < NS; ++s) x[h][s] = in ? load16(xr[s] + k + 32 * h) : zero_u4();
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+          for (int s = 0; s < NS; ++s) acc[a][s] = mfma_16x16x32(w[h][a], x[h][s], acc[a][s]);
+    }
+  };
+  if (subs == 1) body(std::integral_constant<int, 1>{});
+  else if (subs == 2) body(std::integral_constant<int, 2>{});
+  else body(std::integral_constant<int, kSubs>{});
+  float* out = j.T + (int64_t)split * p.M * c.r;
+#pragma unroll
+  for (int s = 0; s < kSubs; ++s) {
+    if (s >= subs) break;
+#pragma unroll
+    for (int a = 0; a < RT; ++a) sums[wave][a][lane] = acc[a][s];
+    __syncthreads();
+    for (int q = tid; q < RT * 64; q += kThreads) {
+      const int a = q >> 6, l = q & 63;
+      f32x4_t v = sums[0][a][l];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += sums[w][a][l];
+      const int row = 16 * s + (l & 15), rank = rank0 + 16 * a + 4 * (l >> 4);
+      if (row < n && rank < c.r) *reinterpret_cast<f32x4_t*>(out + (int64_t)(t.begin + row) * c.r + rank) = v;
+    }
+    __syncthreads();
+  }
+}
+
+// ---- finish: the pieces' sums as bf16 planes (for the gradients) ----
+__global__ __launch_bounds__(kThreads) void adapter_finish_kernel(AdapterCommon c, AdapterFinish x, AdapterFinish y) {
+  const AdapterPlan& p = c.plan;
+  if ((int)blockIdx.x >= p.head[0]) return;
+  const AdapterTile t = p.tiles[blockIdx.x];
+  if (t.adapter >= p.count) return;
+  const AdapterFinish f = blockIdx.y ? y : x;
+  const int live = live_ranks(c, t.adapter), rq = c.r / 4;
+  const float scale = scale_of(c, t.adapter);
+  const int64_t plane = p.M * c.r;
+  for (int q = threadIdx.x; q < (t.end - t.begin) * rq; q += kThreads) {
+    const int rank = q % rq * 4;
+    const int64_t at = (int64_t)(t.begin + q / rq) * c.r + rank;
+    f32x4_t v = zero4();
+    if (rank < live)
+      for (int s = 0; s < f.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(f.T + s * plane + at);
+    uint16_t w[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) limbs(rank + e < live ? v[e] * scale : 0.f, w[e], 3);
+#pragma unroll
+    for (int l = 0; l < 3; ++l)
+      *reinterpret_cast<u32x2_t*>(f.planes + l * plane + at) =
+          u32x2_t{w[0][l] | (uint32_t)w[1][l] << 16, w[2][l] | (uint32_t)w[3][l] << 16};
+  }
+}
+
+// ---- up: out = base + V W^T for one tile and a slice of the outputs ----
+//
+// D[output][token] tiles.  V (two bf16 planes: its rounding stays below 2^-16
+// of it) waits in LDS.  A wave takes 64 outputs at a time; row m of the four
+// tiles q is output 16 (m / 4) + 4 q + m % 4, so that a lane ends up with 16
+// consecutive outputs of one token: 32-byte accesses, 128 bytes a token.
+template <int RC, bool PLANES>
+__global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, AdapterUp u) {
+  constexpr int kPitch = RC * 32 + 8;
+  __shared__ __attribute__((aligned(16))) uint16_t v[2][kAdapterTile][kPitch];
+  const AdapterPlan& p = c.plan;
+  if ((int)blockIdx.x >= p.head[0]) return;
+  const AdapterTile t = p.tiles[blockIdx.x];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int n = t.end - t.begin, subs = (n + 15) / 16;
+  const bool bare = t.adapter >= p.count;
+  const int live = bare ? 0 : live_ranks(c, t.adapter);
+  if (live == 0 && u.base == u.out) return;
+  const bool vec = (u.N & 7) == 0;
+  const int64_t n0 = (int64_t)blockIdx.y * u.slice, n1 = min(u.N, n0 + u.slice);
+  if (live > 0) {
+    const float scale = scale_of(c, t.adapter);
+    const int64_t plane = p.M * c.r;
+    constexpr int kQuads = RC * 8;
+    for (int q = tid; q < subs * 16 * kQuads; q += kThreads) {
+      const int row = q / kQuads, rank = q % kQuads * 4;
+      const bool in = row < n && rank < live;
+      const int64_t at = (int64_t)(t.begin + row) * c.r + rank;
+      u32x2_t hi = {0u, 0u}, lo = {0u, 0u};
+      if constexpr (PLANES) {
+        if (in) {
+          hi = *reinterpret_cast<const u32x2_t*>(u.planes + at);
+          lo = *reinterpret_cast<const u32x2_t*>(u.planes + plane + at);
+        }
+      } else if (in) {
+        f32x4_t x = zero4();
+        for (int s = 0; s < u.splits; ++s) x += *reinterpret_cast<const f32x4_t*>(u.T + s * plane + at);
+        uint16_t w[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) limbs(rank + e < live ? x[e] * scale : 0.f, w[e], 2);
+        hi = u32x2_t{w[0][0] | (uint32_t)w[1][0] << 16, w[2][0] | (uint32_t)w[3][0] << 16};
+        lo = u32x2_t{w[0][1] | (uint32_t)w[1][1] << 16, w[2][1] | (uint32_t)w[3][1] << 16};
+      }
+      *reinterpret_cast<u32x2_t*>(&v[0][row][rank]) = hi;
+      *reinterpret_cast<u32x2_t*>(&v[1][row][rank]) = lo;
+    }
+    __syncthreads();
+  }
+  int64_t row[kSubs];
+#pragma unroll
+  for (int s = 0; s < kSubs; ++s) row[s] = (int64_t)p.order[t.begin + min(16 * s + i, n - 1)] * u.N;
+  const uint16_t* W = u.W + (int64_t)(bare ? 0 : t.adapter) * u.N * c.r;
+  for (int64_t nb = n0 + 64 * wave; nb < n1; nb += 64 * kWaves) {
+    u32x4_t w[4][RC];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t o = min(nb + 16 * (i >> 2) + 4 * q + (i & 3), u.N - 1);
+#pragma unroll
+      for (int k = 0; k < RC; ++k) {
+        // (past the live ranks the weights may hold anything: zeros there)
+        const int rank = 32 * k + 8 * g, left = live - rank;
+        w[q][k] = left > 0 ? load16(W + o * c.r + rank) : zero_u4();
+        if (left > 0 && left < 8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[q][k][e] &= (2 * e < left ? 0xFFFFu : 0u) | (2 * e + 1 < left ? 0xFFFF0000u : 0u);
+        }
+      }
+    }
+    const int64_t o0 = nb + 16 * g;  // this lane's 16 outputs
+#pragma unroll
+    for (int s = 0; s < kSubs; ++s) {
+      if (s >= subs) break;
+      f32x4_t acc[4] = {zero4(), zero4(), zero4(), zero4()};
+      if (live > 0) {
+#pragma unroll
+        for (int k = 0; k < RC; ++k)
+#pragma unroll
+          for (int l = 0; l < 2; ++l) {
+            const u32x4_t x = load16(&v[l][16 * s + i][32 * k + 8 * g]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q] = mfma_16x16x32(w[q][k], x, acc[q]);
+          }
+      }
+      if (16 * s + i >= n) continue;
+      const uint16_t* b = u.base ? u.base + row[s] : nullptr;
+      uint16_t* out = u.out + row[s];
+      if (vec) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t o = o0 + 8 * h;
+          if (o >= n1) break;
+          const u32x4_t x = b ? load16(b + o) : zero_u4();
+          u32x4_t y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float lo = bf16_to_f32((uint16_t)x[e]) + acc[2 * h + e / 2][2 * (e & 1)];
+            const float hi = bf16_to_f32((uint16_t)(x[e] >> 16)) + acc[2 * h + e / 2][2 * (e & 1) + 1];
+            y[e] = f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
+          }
+          *reinterpret_cast<u32x4_t*>(out + o) = live > 0 ? y : x;
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int64_t o = o0 + 4 * q + e;
+            if (o >= n1) continue;
+            const uint16_t x = b ? b[o] : (uint16_t)0;
+            out[o] = live > 0 ? f32_to_bf16(bf16_to_f32(x) + acc[q][e]) : x;
+          }
+      }
+    }
+  }
+}
+
+// ---- the adapters transposed (for the gradients): [R][C] -> [C][R], those
+// with tokens only ----
+__global__ __launch_bounds__(kThreads) void adapter_transpose_kernel(AdapterCommon c, const uint16_t* a, uint16_t* at,
+                                                                     int64_t K, const uint16_t* b, uint16_t* bt,
+                                                                     int64_t N) {
+  __shared__ uint16_t tile[64][66];
+  const int adapter = blockIdx.z >> 1;
+  const bool second = blockIdx.z & 1;
+  if (c.plan.offsets[adapter] == c.plan.offsets[adapter + 1]) return;
+  const int64_t R = second ? N : c.r, C = second ? c.r : K;
+  const uint16_t* src = (second ? b : a) + (int64_t)adapter * R * C;
+  uint16_t* dst = (second ? bt : at) + (int64_t)adapter * R * C;
+  // (blockIdx.x along the long side, blockIdx.y along the ranks)
+  const int64_t r0 = (int64_t)(second ? blockIdx.x : blockIdx.y) * 64, c0 = (int64_t)(second ? blockIdx.y : blockIdx.x) * 64;
+  if (r0 >= R || c0 >= C) return;
+  const int ch = threadIdx.x & 7;  // 8 values
+  for (int y = threadIdx.x >> 3; y < 64; y += kThreads / 8) {
+    const bool in = r0 + y < R && c0 + 8 * ch < C;
+    const u32x4_t x = in ? load16(src + (r0 + y) * C + c0 + 8 * ch) : zero_u4();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(&tile[y][8 * ch + 2 * e]) = x[e];
+  }
+  __syncthreads();
+  for (int y = threadIdx.x >> 3; y < 64; y += kThreads / 8) {
+    if (c0 + y >= C || r0 + 8 * ch >= R) continue;
+    u32x4_t x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = tile[8 * ch + 2 * e][y] | (uint32_t)tile[8 * ch + 2 * e + 1][y] << 16;
+    *reinterpret_cast<u32x4_t*>(dst + (c0 + y) * R + r0 + 8 * ch) = x;
+  }
+}
+
+// ---- gradients of the adapters: sums over a chunk's tokens ----
+//
+// Both operands run along the tokens while memory runs along the columns, so
+// 32 tokens at a time go to LDS as they are and come back transposed (4 x 16
+// values a 16 lanes).  T and G are three bf16 planes each: the float sums see
+// all their bits.
+constexpr int kGradCols = 128;
+
+__device__ __forceinline__ u32x4_t read_transposed(const uint16_t* tile, int pitch, int lane) {
+  // lane (i, g) gets column i of rows 4g..4g+3 and 16+4g..16+4g+3
+  typedef __attribute__((address_space(3))) s16x4_t lds_t;
+  const int q = lane & 15, g = lane >> 4;
+  const uint16_t* at = tile + (4 * g + (q >> 2)) * pitch + 4 * (q & 3);
+  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)at);
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(at + 16 * pitch));
+  const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
+  return u32x4_t{a.x, a.y, b.x, b.y};
+}
+
+template <int RT>
+__global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c, AdapterGrad ga, AdapterGrad gb,
+                                                                int blocks_a, int groups) {
+  constexpr int kColPitch = kGradCols + 8, kRankPitch = RT * 16 + 8;
+  __shared__ __attribute__((aligned(16))) uint16_t cols[32 * kColPitch];
+  __shared__ __attribute__((aligned(16))) uint16_t rank[3][32 * kRankPitch];
+  const AdapterPlan& p = c.plan;
+  if ((int)blockIdx.y >= p.head[1]) return;
+  const AdapterTile t = p.chunks[blockIdx.y];
+  const int by = blockIdx.x / groups, rank0 = (blockIdx.x % groups) * RT * 16;
+  const bool is_a = by < blocks_a;
+  const AdapterGrad j = is_a ? ga : gb;
+  const int64_t c0 = (int64_t)(is_a ? by : by - blocks_a) * kGradCols;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int64_t plane = p.M * c.r;
+  f32x4_t acc[RT][2];
+#pragma unroll
+  for (int a = 0; a < RT; ++a) acc[a][0] = acc[a][1] = zero4();
+  // staging: 16 bytes of 16 rows' columns a pass, two passes; 8 ranks of a plane's row
+  const int row = tid >> 4, col = 8 * (tid & 15);
+  const bool col_in = c0 + col < j.C;
+  constexpr int kRankPieces = 3 * 32 * RT * 2, kRankPasses = (kRankPieces + kThreads - 1) / kThreads;
+  u32x4_t vc[2], vr[kRankPasses];
+  const auto load = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = b + row + 16 * h;
+      vc[h] = at < t.end && col_in ? load16(j.cols + (int64_t)p.order[at] * j.C + c0 + col) : zero_u4();
+    }
+#pragma unroll
+    for (int q = 0; q < kRankPasses; ++q) {
+      const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = rank0 + x % (RT * 2) * 8;
+      vr[q] = x < kRankPieces && b + y < t.end && z < c.r ? load16(j.planes + l * plane + (int64_t)(b + y) * c.r + z)
+                                                         : zero_u4();
+    }
+  };
+  load(t.begin);
+  for (int b = t.begin; b < t.end; b += 32) {
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4_t*>(&cols[(row + 16 * h) * kColPitch + col]) = vc[h];
+#pragma unroll
+    for (int q = 0; q < kRankPasses; ++q) {
+      const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = x % (RT * 2) * 8;
+      if (x < kRankPieces) *reinterpret_cast<u32x4_t*>(&rank[l][y * kRankPitch + z]) = vr[q];
+    }
+    __syncthreads();
+    if (b + 32 < t.end) load(b + 32);
+    u32x4_t x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x[h] = read_transposed(cols + 32 * wave + 16 * h, kColPitch, lane);
+#pragma unroll
+    for (int a = 0; a < RT; ++a)
+#pragma unroll
+      for (int l = 0; l < 3; ++l) {
+        const u32x4_t y = read_transposed(rank[l] + 16 * a, kRankPitch, lane);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc[a][h] = is_a ? mfma_16x16x32(x[h], y, acc[a][h]) : mfma_16x16x32(y, x[h], acc[a][h]);
+      }
+  }
+  // dA: the lane holds four columns of rank i; dB: four ranks of column i
+  float* out = t.part < 0 ? j.out + (int64_t)t.adapter * c.r * j.C : j.parts + (int64_t)t.part * c.r * j.C;
+#pragma unroll
+  for (int a = 0; a < RT; ++a)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t cc = c0 + 32 * wave + 16 * h + (is_a ? 4 * g : i);
+      const int rr = rank0 + 16 * a + (is_a ? i : 4 * g);
+      if (cc < j.C && rr < c.r)
+        *reinterpret_cast<f32x4_t*>(is_a ? out + (int64_t)rr * j.C + cc : out + cc * c.r + rr) = acc[a][h];
+    }
+}
+
+// The chunks' sums in order, for adapters with several; zeros for those
+// without tokens.
+__global__ __launch_bounds__(kThreads) void adapter_grad_sum_kernel(AdapterCommon c, AdapterGrad ga, AdapterGrad gb,
+                                                                    int blocks_a) {
+  const AdapterPlan& p = c.plan;
+  const int adapter = blockIdx.y;
+  const int n = p.offsets[adapter + 1] - p.offsets[adapter], chunks = (n + p.chunk - 1) / p.chunk;
+  if (chunks == 1) return;
+  const bool is_a = (int)blockIdx.x < blocks_a;
+  const AdapterGrad j = is_a ? ga : gb;
+  const int64_t size = (int64_t)c.r * j.C, e = ((int64_t)(is_a ? blockIdx.x : blockIdx.x - blocks_a) * kThreads + threadIdx.x) * 4;
+  if (e >= size) return;
+  const float* part = j.parts + p.parts[adapter] * size + e;
+  f32x4_t v = zero4();
+  for (int q = 0; q < chunks; ++q) v += *reinterpret_cast<const f32x4_t*>(part + q * size);
+  *reinterpret_cast<f32x4_t*>(j.out + (int64_t)adapter * size + e) = v;
+}
+
+// The rank tiles of 16 in groups of up to five, as even as they go.
+inline int rank_groups(int r) { return ((r + 15) / 16 + 4) / 5; }
+template <class F>
+void with_rank_tiles(int r, F f) {
+  const int groups = rank_groups(r), rt = ((r + 15) / 16 + groups - 1) / groups;
+  if (rt == 1) f(std::integral_constant<int, 1>{}, groups);
+  else if (rt == 2) f(std::integral_constant<int, 2>{}, groups);
+  else if (rt == 3) f(std::integral_constant<int, 3>{}, groups);
+  else if (rt == 4) f(std::integral_constant<int, 4>{}, groups);
+  else f(std::integral_constant<int, 5>{}, groups);
+}
+template <class F>
+void with_rank_chunks(int r, F f) {
+  if (r <= 32) f(std::integral_constant<int, 1>{});
+  else if (r <= 64) f(std::integral_constant<int, 2>{});
+  else if (r <= 96) f(std::integral_constant<int, 3>{});
+  else if (r <= 128) f(std::integral_constant<int, 4>{});
+  else f(std::integral_constant<int, 8>{});
+}
+
+}  // namespace
+
+hipError_t launch_adapter_plan(const int32_t* ids, const AdapterPlan& p, hipStream_t s) {
+  // (each wave's counters: 4 waves keep 4096 adapters within 132 KB of LDS)
+  const int waves = p.count <= 1024 ? kPlanWaves : 4;
+  const size_t lds = ((size_t)waves * (p.count + 1) + 4 * (size_t)(p.count + 2)) * 4;
+  hipLaunchKernelGGL(adapter_plan_kernel, dim3(1), dim3(kPlanThreads), lds, s, ids, p, waves);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_down(const AdapterCommon& c, const AdapterDown* jobs, int n_jobs, hipStream_t s) {
+  int splits = 0;
+  for (int q = 0; q < n_jobs; ++q) splits = std::max(splits, jobs[q].splits);
+  with_rank_tiles(c.r, [&](auto rt, int groups) {
+    hipLaunchKernelGGL((adapter_down_kernel<decltype(rt)::value>),
+                       dim3((unsigned)c.plan.max_tiles, (unsigned)(splits * groups), (unsigned)n_jobs), dim3(kThreads), 0,
+                       s, c, jobs[0], jobs[n_jobs - 1], groups);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_finish(const AdapterCommon& c, const AdapterFinish& x, const AdapterFinish& y,
+                                 hipStream_t s) {
+  hipLaunchKernelGGL(adapter_finish_kernel, dim3((unsigned)c.plan.max_tiles, 2), dim3(kThreads), 0, s, c, x, y);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_up(const AdapterCommon& c, const AdapterUp& u, hipStream_t s) {
+  const dim3 grid((unsigned)c.plan.max_tiles, (unsigned)((u.N + u.slice - 1) / u.slice));
+  with_rank_chunks(c.r, [&](auto rc) {
+    constexpr int RC = decltype(rc)::value;
+    if (u.planes)
+      hipLaunchKernelGGL((adapter_up_kernel<RC, true>), grid, dim3(kThreads), 0, s, c, u);
+    else
+      hipLaunchKernelGGL((adapter_up_kernel<RC, false>), grid, dim3(kThreads), 0, s, c, u);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_transpose(const AdapterCommon& c, const uint16_t* a, uint16_t* at, int64_t K,
+                                    const uint16_t* b, uint16_t* bt, int64_t N, hipStream_t s) {
+  hipLaunchKernelGGL(adapter_transpose_kernel,
+                     dim3((unsigned)((std::max(K, N) + 63) / 64), (unsigned)((c.r + 63) / 64), (unsigned)(2 * c.plan.count)),
+                     dim3(kThreads), 0, s, c, a, at, K, b, bt, N);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_grads(const AdapterCommon& c, const AdapterGrad& d_a, const AdapterGrad& d_b,
+                                hipStream_t s) {
+  const auto blocks = [](int64_t n, int64_t per) { return (int)((n + per - 1) / per); };
+  if (c.plan.M > 0) {
+    const int ba = blocks(d_a.C, kGradCols), bb = blocks(d_b.C, kGradCols);
+    with_rank_tiles(c.r, [&](auto rt, int groups) {
+      hipLaunchKernelGGL((adapter_grad_kernel<decltype(rt)::value>),
+                         dim3((unsigned)((ba + bb) * groups), (unsigned)c.plan.max_chunks), dim3(kThreads), 0, s, c, d_a,
+                         d_b, ba, groups);
+    });
+  }
+  const int sa = blocks(d_a.C * c.r, 4 * kThreads), sb = blocks(d_b.C * c.r, 4 * kThreads);
+  hipLaunchKernelGGL(adapter_grad_sum_kernel, dim3((unsigned)(sa + sb), (unsigned)c.plan.count), dim3(kThreads), 0, s, c,
+                     d_a, d_b, sa);
+  return hipGetLastError();
+}
+
+}  // namespace salr
