@@ -801,6 +801,97 @@ int salr_adapters_backward(const salr_adapters_t* A,
                            uint16_t* dX, float* dA, float* dB, void* ws,
                            size_t ws_bytes, void* stream);
 
+/*
+ * Muon over many matrices at once (Jordan et al. 2024): momentum whose
+ * direction is orthogonalised, for the adapters of any number of layers,
+ * experts or requests, beside salr_adamw_step.  For every matrix, with g =
+ * grad * grad_scale:
+ *   m = momentum m + g
+ *   u = g + momentum m  (nesterov != 0), or m
+ *   X = u / (|u| + eps)             (|u|: the root of the sum of squares)
+ *   X = a X + (b A + c A^2) X,  A = X X^T            `steps` times
+ *   p = p (1 - lr weight_decay) - lr lr_scale X
+ * (A is taken over the shorter side; it is the same X.)  a, b, c = 3.4445,
+ * -4.7750, 2.0315 and five steps bring all but the smallest singular values
+ * into about 0.7 .. 1.2.  p is rounded to its type at the end; a bf16
+ * parameter may have a float master copy, which is then what the step
+ * updates, p being its rounding.  m is float.
+ *
+ * The steps run on the product of u with itself, summed and iterated in
+ * double (float products of its pieces): X is as exact as by float steps on
+ * X itself up to a few 1e-5 of it (its smallest singular values; 1e-6 where
+ * they are of one size).  u's sum of squares has to fit a float.  A matrix
+ * with a NaN or an infinity among its gradients gets NaN everywhere; others
+ * do not see it.
+ */
+#define SALR_MUON_MAX_SIDE 256 /* the shorter side: the largest adapter rank */
+#define SALR_MUON_CLASSES 11
+
+/* One matrix [rows][cols], dense: plain device pointers. */
+typedef struct salr_muon_tensor {
+  void* p;          /* parameters (p_type)                                  */
+  const void* g;    /* gradients (g_type)                                   */
+  float* m;         /* momentum; zeros at the start                         */
+  float* master;    /* float copy of a bf16 parameter, or NULL in all       */
+  int64_t rows;     /* 0 .. 2^30 each, the shorter at most                  */
+  int64_t cols;     /*   SALR_MUON_MAX_SIDE                                 */
+  double lr_scale;  /* this matrix's share of lr                            */
+} salr_muon_tensor_t;
+
+/* A plan: matrices laid out for the step, with what the step works in. */
+typedef struct salr_muon_plan {
+  void* table;      /* device, the caller's buffer                          */
+  int32_t count;    /* the entries below are salr_muon_plan's               */
+  int32_t p_type, g_type, has_master;
+  int32_t matrices[SALR_MUON_CLASSES];
+  int32_t chunks[SALR_MUON_CLASSES];
+} salr_muon_plan_t;
+
+/* What one step uses.  lr, weight_decay >= 0, eps > 0, 0 <= momentum < 1, 1 <=
+ * steps <= 6, all finite. */
+typedef struct salr_muon_step_args {
+  double lr, momentum, weight_decay, eps, grad_scale;
+  double a, b, c;
+  int32_t steps;
+  int32_t nesterov;
+} salr_muon_step_args_t;
+
+/* Bytes of the plan's device buffer for `count` matrices (`rows`, `cols` and
+ * `out` host; count <= 2^20).  Errors: INVALID_ARG, UNSUPPORTED (a shorter
+ * side above SALR_MUON_MAX_SIDE; more than 2^40 elements in all, or more
+ * matrices and pieces of them than one launch takes). */
+int salr_muon_plan_bytes(const int64_t* rows, const int64_t* cols,
+                         int32_t count, size_t* out);
+
+/*
+ * salr_muon_plan - build a plan: once, for tensors that stay where they are.
+ * tensors  host array of `count` records (all with a master, or none; masters
+ *          only for bf16 parameters).  Everything that a step writes (p, m,
+ *          master) must be disjoint, over all matrices.
+ * table    device buffer of at least salr_muon_plan_bytes; it belongs to the
+ *          plan until its last step, and each step works in it: steps of one
+ *          plan (or captured graphs of them) must be ordered.
+ * out      host.
+ * SYNCHRONOUS on `stream` (the table is copied from host memory); not under
+ * graph capture (UNSUPPORTED).  Errors: INVALID_ARG (nulls, alignment,
+ * types, sizes, overlaps), UNSUPPORTED (as salr_muon_plan_bytes; host memory
+ * ran out), WORKSPACE, HIP.
+ */
+int salr_muon_plan(const salr_muon_tensor_t* tensors, int32_t count,
+                   int32_t p_type, int32_t g_type, void* table,
+                   size_t table_bytes, salr_muon_plan_t* out, void* stream);
+
+/*
+ * salr_muon_step - one step over every matrix of the plan, in place.
+ * args  host.
+ * dyn   NULL, or device float [2] that replaces args' lr and grad_scale (for
+ *       steps in a captured graph): {lr, grad_scale}, read when the step runs.
+ * Asynchronous on `stream`, capturable.  Errors: INVALID_ARG, HIP.
+ */
+int salr_muon_step(const salr_muon_plan_t* plan,
+                   const salr_muon_step_args_t* args, const float* dyn,
+                   void* stream);
+
 /* Static English text for a status code (never NULL). */
 const char* salr_status_string(int status);
 

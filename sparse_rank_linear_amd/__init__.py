@@ -16,9 +16,12 @@ from .binding import (  # noqa: F401
     EXPORTS,
     LIB_PATH,
     MOE_MAX_TOPK,
+    MUON_COEFFICIENTS,
+    MUON_MAX_SIDE,
     NOALLOC_SCRATCH_BYTES,
     AdamWPlan,
     AdaptersPlan,
+    MuonPlan,
     SalrAdapters,
     SalrError,
     SalrLayer,
@@ -55,6 +58,9 @@ from .binding import (  # noqa: F401
     moe_route,
     moe_route_backward,
     moe_workspace,
+    muon_plan,
+    muon_states,
+    muon_step,
     nf4_levels,
     probe_mfma,
     probe_stream_read,
@@ -68,13 +74,14 @@ from .binding import (  # noqa: F401
 )
 
 __all__ = [
-    "ADAMW_BLOCK", "ADAPTERS_MAX", "AdamWPlan", "AdaptersPlan", "EXPORTS", "LIB_PATH", "MOE_MAX_TOPK",
-    "NOALLOC_SCRATCH_BYTES", "SalrAdapters", "SalrError", "SalrLayer", "SalrMoE", "WaitTimeout", "adamw_dyn",
-    "adamw_plan", "adamw_states", "adamw_step", "adapters_backward", "adapters_forward", "adapters_plan",
-    "adapters_plan_bytes", "adapters_workspace", "adapters_ws_bytes", "backward_workspace", "backward_ws_bytes",
-    "encode", "forward_workspace", "fuse", "lib", "linear_backward", "linear_forward", "linear_forward_noalloc",
-    "moe_combine", "moe_combine_backward", "moe_dispatch", "moe_dispatch_backward", "moe_dispatch_workspace",
-    "moe_dispatch_ws_bytes", "moe_encode_expert", "moe_forward", "moe_query_sizes", "moe_route", "moe_route_backward",
-    "moe_workspace", "nf4_levels", "probe_mfma", "probe_stream_read", "quantize_nf4", "query_sizes",
-    "transpose_count", "transpose_layer", "transpose_ws_bytes", "wait_error", "workspace",
+    "ADAMW_BLOCK", "ADAPTERS_MAX", "EXPORTS", "LIB_PATH", "MOE_MAX_TOPK", "MUON_COEFFICIENTS", "MUON_MAX_SIDE",
+    "NOALLOC_SCRATCH_BYTES", "AdamWPlan", "AdaptersPlan", "MuonPlan", "SalrAdapters", "SalrError", "SalrLayer",
+    "SalrMoE", "WaitTimeout", "adamw_dyn", "adamw_plan", "adamw_states", "adamw_step", "adapters_backward",
+    "adapters_forward", "adapters_plan", "adapters_plan_bytes", "adapters_workspace", "adapters_ws_bytes",
+    "backward_workspace", "backward_ws_bytes", "encode", "forward_workspace", "fuse", "lib", "linear_backward",
+    "linear_forward", "linear_forward_noalloc", "moe_combine", "moe_combine_backward", "moe_dispatch",
+    "moe_dispatch_backward", "moe_dispatch_workspace", "moe_dispatch_ws_bytes", "moe_encode_expert", "moe_forward",
+    "moe_query_sizes", "moe_route", "moe_route_backward", "moe_workspace", "muon_plan", "muon_states", "muon_step",
+    "nf4_levels", "probe_mfma", "probe_stream_read", "quantize_nf4", "query_sizes", "transpose_count",
+    "transpose_layer", "transpose_ws_bytes", "wait_error", "workspace",
 ]

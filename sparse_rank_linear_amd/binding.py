@@ -59,6 +59,9 @@ EXPORTS = (
     "salr_adapters_ws_bytes",
     "salr_adapters_forward",
     "salr_adapters_backward",
+    "salr_muon_plan_bytes",
+    "salr_muon_plan",
+    "salr_muon_step",
     # include/salr_probe.h
     "salr_probe_stream_read",
     "salr_probe_mfma",
@@ -174,6 +177,21 @@ class salr_adapters_plan_t(C.Structure):
     _fields_ = [("buffer", C.c_void_p), ("M", C.c_int64), ("count", C.c_int32)]
 
 
+class salr_muon_tensor_t(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("p", "g", "m", "master")] + [("rows", C.c_int64), ("cols", C.c_int64),
+                                                                     ("lr_scale", C.c_double)]
+
+
+class salr_muon_plan_t(C.Structure):
+    _fields_ = [("table", C.c_void_p)] + [(n, C.c_int32) for n in ("count", "p_type", "g_type", "has_master")] + [
+        ("matrices", C.c_int32 * 11), ("chunks", C.c_int32 * 11)]
+
+
+class salr_muon_step_args_t(C.Structure):
+    _fields_ = [(n, C.c_double) for n in ("lr", "momentum", "weight_decay", "eps", "grad_scale", "a", "b", "c")] + [
+        ("steps", C.c_int32), ("nesterov", C.c_int32)]
+
+
 _LIB = None
 
 
@@ -274,6 +292,15 @@ def _lib():
         lib.salr_adapters_backward.argtypes = [C.POINTER(salr_adapters_t), C.POINTER(salr_adapters_plan_t)] + [
             C.c_void_p] * 7 + [C.c_size_t, C.c_void_p]
         lib.salr_adapters_backward.restype = C.c_int
+        lib.salr_muon_plan_bytes.argtypes = [C.POINTER(C.c_int64), C.POINTER(C.c_int64), C.c_int32,
+                                             C.POINTER(C.c_size_t)]
+        lib.salr_muon_plan_bytes.restype = C.c_int
+        lib.salr_muon_plan.argtypes = [C.POINTER(salr_muon_tensor_t), C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
+                                       C.c_size_t, C.POINTER(salr_muon_plan_t), C.c_void_p]
+        lib.salr_muon_plan.restype = C.c_int
+        lib.salr_muon_step.argtypes = [C.POINTER(salr_muon_plan_t), C.POINTER(salr_muon_step_args_t), C.c_void_p,
+                                       C.c_void_p]
+        lib.salr_muon_step.restype = C.c_int
         lib.salr_probe_stream_read.argtypes = [C.c_void_p, C.c_size_t, C.c_void_p, C.c_int32, C.c_void_p]
         lib.salr_probe_stream_read.restype = C.c_int
         lib.salr_probe_mfma.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]
@@ -1185,6 +1212,100 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
         _check(_lib().salr_adamw_step(C.byref(plan.desc), C.byref(args), d, at), "salr_adamw_step")
     else:
         _check(_lib().salr_adamw_step_random(C.byref(plan.desc), C.byref(args), seed, d, at), "salr_adamw_step_random")
+
+
+MUON_MAX_SIDE = 256
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+@dataclass
+class MuonPlan:
+    """Matrices laid out for muon_step (include/salr.h, salr_muon_plan_t).
+    Holds on to them: they and the plan outlive every step and captured
+    graph that uses them."""
+
+    desc: salr_muon_plan_t
+    table: object
+    tensors: list
+    device: object
+
+
+def muon_states(params, master: bool = False) -> dict:
+    """Fresh states of muon_step for the matrices in `params`: the list m and,
+    with master, float copies of bf16 parameters; keywords of muon_plan."""
+    torch = _torch()
+    params = list(params)
+    return {"m": [torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in params],
+            "master": [p.detach().float() for p in params] if master else None}
+
+
+def muon_plan(params, grads, m, master=None, lr_scale=None, stream=None) -> MuonPlan:
+    """A plan for muon_step over the matrices in `params` (all bf16 or all
+    float, 2-D, the shorter side at most MUON_MAX_SIDE) with their gradients
+    (all bf16 or all float), momenta (float) and float master copies of bf16
+    parameters, element i of every list belonging together; all contiguous and
+    16-byte aligned, written ones disjoint.  lr_scale: each matrix's share of
+    the learning rate (default: sqrt(max(1, rows / cols)), which gives updates
+    the same size on the outputs whatever the shape).  Synchronous."""
+    torch = _torch()
+    lists = {"params": params, "grads": grads, "m": m, "master": master}
+    lists = {name: list(ts) for name, ts in lists.items() if ts is not None}
+    params, count = lists["params"], len(lists["params"])
+    if count == 0:
+        raise ValueError("muon_plan needs at least one matrix")
+    for name, ts in lists.items():
+        if len(ts) != count:
+            raise ValueError(f"{name} has {len(ts)} tensors for {count} parameters")
+    dev = params[0].device
+    index = dev.index
+    at = _stream_here(index, stream)
+    if at is None:
+        with _Place(dev, stream):
+            return muon_plan(**lists, lr_scale=lr_scale)
+    for i, p in enumerate(params):
+        if p.dim() != 2:
+            raise ValueError(f"params[{i}] must be a matrix (has {p.dim()} dimensions)")
+    dtypes = {"params": params[0].dtype, "grads": lists["grads"][0].dtype, "m": torch.float32, "master": torch.float32}
+    address = {name: [_ptr(t, f"{name}[{i}]", dtypes[name], params[i].shape, index) for i, t in enumerate(ts)]
+               for name, ts in lists.items()}
+    address.setdefault("master", [None] * count)
+    rows, cols = ([p.shape[k] for p in params] for k in (0, 1))
+    if lr_scale is None:
+        lr_scale = [max(1.0, r / max(c, 1)) ** 0.5 for r, c in zip(rows, cols)]
+    else:
+        lr_scale = [float(v) for v in lr_scale]
+        if len(lr_scale) != count:
+            raise ValueError(f"lr_scale has {len(lr_scale)} values for {count} parameters")
+    recs = (salr_muon_tensor_t * count)(*zip(address["params"], address["grads"], address["m"], address["master"],
+                                             rows, cols, lr_scale))
+    p_type, g_type = _float_type(params[0], "params"), _float_type(lists["grads"][0], "grads")
+    desc, nbytes = salr_muon_plan_t(), C.c_size_t()
+    _check(_lib().salr_muon_plan_bytes((C.c_int64 * count)(*rows), (C.c_int64 * count)(*cols), count, C.byref(nbytes)),
+           "salr_muon_plan_bytes")
+    table = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+    _check(_lib().salr_muon_plan(recs, count, p_type, g_type, table.data_ptr(), nbytes.value, C.byref(desc), at),
+           "salr_muon_plan")
+    return MuonPlan(desc, table, [t for ts in lists.values() for t in ts], dev)
+
+
+def muon_step(plan: MuonPlan, lr: float, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+              eps: float = 1e-7, steps: int = 5, coefficients=MUON_COEFFICIENTS, grad_scale: float = 1.0, dyn=None,
+              stream=None):
+    """One Muon step over every matrix of the plan, in place: momentum,
+    `steps` Newton-Schulz steps that orthogonalise its direction, the update
+    (salr_muon_step).  dyn: a device float tensor [lr, grad_scale], read when
+    the step runs instead of lr and grad_scale (for captured graphs)."""
+    torch = _torch()
+    dev = plan.device
+    index = dev.index
+    at = _stream_here(index, stream)
+    if at is None:
+        with _Place(dev, stream):
+            return muon_step(plan, lr, momentum, nesterov, weight_decay, eps, steps, coefficients, grad_scale, dyn)
+    a, b, c = coefficients
+    args = salr_muon_step_args_t(lr, momentum, weight_decay, eps, grad_scale, a, b, c, steps, bool(nesterov))
+    d = None if dyn is None else _ptr(dyn, "dyn", torch.float32, (2,), index)
+    _check(_lib().salr_muon_step(C.byref(plan.desc), C.byref(args), d, at), "salr_muon_step")
 
 
 # ----------------------------------------------------------------------------

@@ -7,17 +7,14 @@
 
 #include "salr.h"
 #include "salr_adapters.hpp"
+#include "salr_api_checks.hpp"
 
 namespace {
 
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 65536;
 constexpr int64_t kMaxColumns = int64_t(1) << 20;
 constexpr int32_t kMaxRank = 256;
-
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline int status(hipError_t e) { return e == hipSuccess ? SALR_OK : SALR_ERR_HIP; }
+using namespace salr;
 
 bool plan_shape_ok(int64_t M, int32_t count) {
   return M >= 0 && M <= kMaxTokens && count >= 1 && count <= SALR_ADAPTERS_MAX;
@@ -101,25 +98,6 @@ Workspace lay_out(int64_t count, int64_t N, int64_t K, int32_t r, int64_t M, boo
   }
   w.total = std::max<size_t>(at, 256);
   return w;
-}
-
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-bool apart(const Span& x, const Span& y) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
-  return !x.p || !y.p || !x.bytes || !y.bytes || a + x.bytes <= b || b + y.bytes <= a;
-}
-template <size_t nw, size_t nr>
-bool writes_apart(const Span (&written)[nw], const Span (&read)[nr]) {
-  for (size_t i = 0; i < nw; ++i) {
-    for (size_t j = i + 1; j < nw; ++j)
-      if (!apart(written[i], written[j])) return false;
-    for (const Span& r : read)
-      if (!apart(written[i], r)) return false;
-  }
-  return true;
 }
 
 // What both directions ask of the adapters and the plan.

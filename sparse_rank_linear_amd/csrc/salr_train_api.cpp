@@ -10,6 +10,7 @@
 #include <new>
 
 #include "salr.h"
+#include "salr_api_checks.hpp"
 #include "salr_kernels.hpp"
 
 namespace {
@@ -22,13 +23,7 @@ constexpr int32_t kMaxTensors = 1 << 20;
 // Workgroups of one launch: its threads, 8 elements each, stay below 2^32.
 constexpr int64_t max_chunks(int64_t chunk) { return ((int64_t(1) << 32) - 1) / (chunk / 8); }
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-inline int status(hipError_t e) { return e == hipSuccess ? SALR_OK : SALR_ERR_HIP; }
-
-bool type_ok(int32_t t) { return t == SALR_TYPE_BF16 || t == SALR_TYPE_F32; }
+using namespace salr;
 
 size_t type_bytes(int32_t t) { return t == SALR_TYPE_F32 ? 4 : 2; }
 
@@ -51,27 +46,6 @@ template <size_t n>
 bool all_aligned(const void* const (&p)[n]) {
   for (const void* q : p)
     if (q && !aligned16(q)) return false;
-  return true;
-}
-
-// A buffer of a call, and whether two share no byte.
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-bool apart(const Span& x, const Span& y) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
-  return !x.p || !y.p || a + x.bytes <= b || b + y.bytes <= a;
-}
-// What a call writes shares no byte with anything else of it.
-template <size_t nw, size_t nr>
-bool writes_apart(const Span (&written)[nw], const Span (&read)[nr]) {
-  for (size_t i = 0; i < nw; ++i) {
-    for (size_t j = i + 1; j < nw; ++j)
-      if (!apart(written[i], written[j])) return false;
-    for (const Span& r : read)
-      if (!apart(written[i], r)) return false;
-  }
   return true;
 }
 
@@ -206,25 +180,6 @@ static_assert(salr::kAdamwSmallChunk % SALR_ADAMW_BLOCK == 0 && salr::kAdamwLarg
 size_t table_records_bytes(int32_t count) { return align_up((size_t)count * sizeof(salr::AdamwTensor), 256); }
 size_t table_bytes_for(int32_t count, int64_t chunks) {
   return table_records_bytes(count) + align_up((size_t)std::max<int64_t>(chunks, 1) * sizeof(salr::AdamwChunk), 256);
-}
-
-struct Range {
-  uintptr_t a, b;
-};
-
-// Whether any two of the ranges written share a byte, or any range read
-// shares one with a range written.  Sorts `written`.
-bool overlaps(Range* written, size_t nw, const Range* read, size_t nr) {
-  std::sort(written, written + nw, [](const Range& x, const Range& y) { return x.a < y.a; });
-  for (size_t i = 1; i < nw; ++i)
-    if (written[i].a < written[i - 1].b) return true;
-  for (size_t i = 0; i < nr; ++i) {
-    // the last written range that begins before this one ends
-    const Range* w =
-        std::lower_bound(written, written + nw, read[i].b, [](const Range& x, uintptr_t v) { return x.a < v; });
-    if (w != written && (w - 1)->b > read[i].a) return true;
-  }
-  return false;
 }
 
 // Validates the records and, with `table` (host memory of table_bytes_for),
