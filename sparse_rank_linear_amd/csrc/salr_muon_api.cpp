@@ -23,7 +23,8 @@ constexpr int64_t kMaxChunks = (int64_t(1) << 24) - 1;
 static_assert(SALR_MUON_CLASSES == kMuonClasses, "a plan counts every class");
 
 // Elements of a chunk, by those of all matrices: enough workgroups for the
-// CUs, then fewer and longer ones (each writes one s x s sum).
+// CUs, then fewer and longer ones (each writes one s x s sum, so it has s
+// columns at least).
 int64_t chunk_elements(int64_t total) { return std::min<int64_t>(131072, std::max<int64_t>(8192, total / 1024)); }
 
 int class_of(int64_t s) {
@@ -46,7 +47,7 @@ Shape shape_of(int64_t rows, int64_t cols, int64_t per) {
   if (q.s == 0) return q;
   q.cls = class_of(q.s);
   const int64_t kb = muon_stage(kMuonTiles[q.cls]);
-  const int64_t chunk = std::min(cdiv(q.L, kb), std::max<int64_t>(1, cdiv(per, q.s * kb))) * kb;
+  const int64_t chunk = std::min(cdiv(q.L, kb), cdiv(std::max(q.s, cdiv(per, q.s)), kb)) * kb;
   q.chunk = (int32_t)chunk;
   q.chunks = (int32_t)cdiv(q.L, chunk);
   return q;
