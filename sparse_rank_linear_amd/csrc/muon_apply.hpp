@@ -1,0 +1,134 @@
+// The parameters' step with the orthogonalised update (see muon_iterate.hip for
+// the method): one file for each kind of parameter includes this.
+#pragma once
+
+#include "muon_device.hpp"
+
+namespace salr {
+namespace {
+
+// ---- apply ----
+//
+// Wave w holds row tile w % NT of Q in registers and takes its share of the
+// stage's 16-column tiles; Q u goes through LDS to the threads that hold the
+// parameters.
+template <int NT>
+struct ApplyShape {
+  static constexpr int KB = muon_stage(NT), S = 16 * NT;
+  static constexpr int kWaves = NT <= 2 || NT == 4 ? 8 : NT == 3 ? 6 : NT == 5 ? 10 : NT;
+  static constexpr int kCols = kWaves / NT;  // waves of a row tile
+  // u's pitch and the result's: reads and writes that touch all banks
+  static constexpr int PW = KB + 16, RW = KB + 4, PT = S + 4, RT = S + 4;
+  static constexpr int kU = S * PW > KB * PT ? S * PW : KB * PT, kR = S * RW > KB * RT ? S * RW : KB * RT;
+};
+
+template <int NT, bool GF, bool PF, bool MASTER, bool WIDE>
+__device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, int piece, float* lds) {
+  using Shape = ApplyShape<NT>;
+  constexpr int KB = Shape::KB, S = Shape::S, P = WIDE ? Shape::PW : Shape::PT, R = WIDE ? Shape::RW : Shape::RT;
+  constexpr int kThreads = Shape::kWaves * 64, kNq = (S * KB / 4 + kThreads - 1) / kThreads;
+  constexpr bool kSrc = PF || MASTER;  // what the step updates is float
+  float* res = lds + Shape::kU;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i = lane & 15, g = lane >> 4, tile = wave % NT;
+  const Stage<WIDE, KB, kThreads, kNq> st(M.s, M.L, tid);
+  const int64_t k0 = (int64_t)piece * M.chunk, k1 = min(M.L, k0 + M.chunk);
+  const float gs = a.dyn ? a.dyn[1] : a.grad_scale, lr = a.dyn ? a.dyn[0] : a.lr;
+  const float decay = 1.f - lr * a.weight_decay, rate = lr * M.lr_scale;
+  const auto grad = to_global<const typename Four<GF>::elem>(M.g);
+  const auto mom = to_global<const float>(M.m);
+  const auto param = to_global<typename Four<PF>::elem>(M.p);
+  const auto src = to_global<typename Four<kSrc>::elem>(MASTER ? (void*)M.master : M.p);
+  const auto qm = to_global<const float>(M.q);
+  // (parameters a stage ahead as well, where the registers hold them)
+  constexpr bool kEarly = NT < 16;
+  typename Four<GF>::raw vg[kNq];
+  f32x4_t vm[kNq];
+  typename Four<kSrc>::raw vp[kNq], next_p[kNq];
+  const auto load = [&](int64_t k) __attribute__((always_inline)) {
+    const int left = (int)(k1 - k);
+    if (a.nesterov) st.template load<GF>(grad, k, left, vg);
+    st.template load<true>(mom, k, left, vm);
+    if (kEarly) st.template load<kSrc>(src, k, left, next_p);
+  };
+  load(k0);
+  // Q's rows, columns in the order that the operands of u come in
+  float qa[S / 4];
+#pragma unroll
+  for (int kk = 0; kk < S / 4; ++kk)
+    qa[kk] = qm[(16 * tile + i) * S + (WIDE ? 4 * kk + g : 16 * (kk / 4) + 4 * g + kk % 4)];
+  for (int q = tid; q < Shape::kU; q += kThreads) lds[q] = 0.f;
+  int place[kNq], place_r[kNq];
+#pragma unroll
+  for (int q = 0; q < kNq; ++q) {
+    place[q] = st.template place<P>(q);
+    place_r[q] = st.template place<R>(q);
+  }
+  lds_barrier();
+  for (int64_t k = k0; k < k1; k += KB) {
+#pragma unroll
+    for (int q = 0; q < kNq; ++q) {
+      if (kEarly) vp[q] = next_p[q];
+      if (st.has(q))
+        st.template put<P>(lds, place[q], a.nesterov ? Four<GF>::value(vg[q]) * gs + a.momentum * vm[q] : vm[q]);
+    }
+    lds_barrier();
+    if (k + KB < k1) load(k + KB);
+    for (int c = wave / NT; c < KB / 16; c += Shape::kCols) {
+      f32x4_t acc = zero4();
+      if constexpr (WIDE) {
+        // (Q u)^T, four columns of the long side a lane
+#pragma unroll
+        for (int kk = 0; kk < S / 4; ++kk) acc = mfma_f32(lds[(4 * kk + g) * P + 16 * c + i], qa[kk], acc);
+        *reinterpret_cast<f32x4_t*>(res + (16 * tile + i) * R + 16 * c + 4 * g) = acc;
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < S / 16; ++kk) {
+          const f32x4_t x = *reinterpret_cast<const f32x4_t*>(lds + (16 * c + i) * P + 16 * kk + 4 * g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc = mfma_f32(qa[4 * kk + e], x[e], acc);
+        }
+        *reinterpret_cast<f32x4_t*>(res + (16 * c + i) * R + 16 * tile + 4 * g) = acc;
+      }
+    }
+    const int left = (int)(k1 - k);
+    if (!kEarly) st.template load<kSrc>(src, k, left, vp);
+    lds_barrier();
+#pragma unroll
+    for (int q = 0; q < kNq; ++q) {
+      const int n = st.count(q, left);
+      if (n == 0) continue;
+      const int64_t at = st.element(q, k);
+      const f32x4_t p = Four<kSrc>::value(vp[q]) * decay - rate * st.template get<R>(res, place_r[q]);
+      if (MASTER) store4<true>(to_global<float>(M.master) + at, n, p);
+      store4<PF>(param + at, n, p);
+    }
+  }
+}
+
+template <int NT, bool GF, bool PF, bool MASTER>
+__global__ __launch_bounds__(ApplyShape<NT>::kWaves * 64, 4) void muon_apply_kernel(MuonArgs a, int64_t c0) {
+  extern __shared__ __attribute__((aligned(16))) float lds[];  // u, then Q u
+  const MuonChunk ch = a.chunks[c0 + blockIdx.x];
+  const MuonMatrix& M = a.matrices[ch.matrix];
+  if (M.wide) apply<NT, GF, PF, MASTER, true>(a, M, ch.part, lds);
+  else apply<NT, GF, PF, MASTER, false>(a, M, ch.part, lds);
+}
+
+template <bool PF, bool MASTER>
+hipError_t launch_apply(const MuonArgs& a, int cls, int64_t c0, int64_t chunks, hipStream_t s) {
+  return with_muon_tiles(cls, [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    using Shape = ApplyShape<NT>;
+    constexpr size_t kLds = (size_t)(Shape::kU + Shape::kR) * 4;
+    const dim3 grid((unsigned)chunks), threads(Shape::kWaves * 64);
+    if (a.g_f32)
+      hipLaunchKernelGGL((muon_apply_kernel<NT, true, PF, MASTER>), grid, threads, kLds, s, a, c0);
+    else
+      hipLaunchKernelGGL((muon_apply_kernel<NT, false, PF, MASTER>), grid, threads, kLds, s, a, c0);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+}  // namespace salr

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace salr {
 
 // A matrix's short side in tiles of 16, rounded up to one of these (a class).
@@ -50,8 +52,30 @@ struct MuonArgs {
   bool nesterov, p_f32, g_f32, master;
 };
 
-// One class: its matrices [m0, m0 + n_matrices) and chunks [c0, c0 + n_chunks).
-hipError_t launch_muon(const MuonArgs& a, int cls, int32_t m0, int32_t n_matrices, int64_t c0, int64_t n_chunks,
-                       hipStream_t s);
+// f with a class's tiles as a constant.
+template <class F>
+hipError_t with_muon_tiles(int cls, F f) {
+  switch (cls) {
+    case 0: return f(std::integral_constant<int, kMuonTiles[0]>{});
+    case 1: return f(std::integral_constant<int, kMuonTiles[1]>{});
+    case 2: return f(std::integral_constant<int, kMuonTiles[2]>{});
+    case 3: return f(std::integral_constant<int, kMuonTiles[3]>{});
+    case 4: return f(std::integral_constant<int, kMuonTiles[4]>{});
+    case 5: return f(std::integral_constant<int, kMuonTiles[5]>{});
+    case 6: return f(std::integral_constant<int, kMuonTiles[6]>{});
+    case 7: return f(std::integral_constant<int, kMuonTiles[7]>{});
+    case 8: return f(std::integral_constant<int, kMuonTiles[8]>{});
+    case 9: return f(std::integral_constant<int, kMuonTiles[9]>{});
+    default: return f(std::integral_constant<int, kMuonTiles[10]>{});
+  }
+}
+static_assert(kMuonClasses == 11, "the cases above");
+
+// One class: its matrices [m0, m0 + n_matrices) or its chunks [c0, c0 + chunks).
+hipError_t launch_muon_gram(const MuonArgs& a, int cls, int64_t c0, int64_t chunks, hipStream_t s);
+hipError_t launch_muon_iterate(const MuonArgs& a, int cls, int32_t m0, int32_t n_matrices, hipStream_t s);
+hipError_t launch_muon_apply_f32(const MuonArgs& a, int cls, int64_t c0, int64_t chunks, hipStream_t s);
+hipError_t launch_muon_apply_bf16(const MuonArgs& a, int cls, int64_t c0, int64_t chunks, hipStream_t s);
+hipError_t launch_muon_apply_master(const MuonArgs& a, int cls, int64_t c0, int64_t chunks, hipStream_t s);
 
 }  // namespace salr

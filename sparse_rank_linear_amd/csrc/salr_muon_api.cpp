@@ -245,13 +245,17 @@ int salr_muon_step(const salr_muon_plan_t* plan, const salr_muon_step_args_t* ar
   a.p_f32 = plan->p_type == SALR_TYPE_F32;
   a.g_f32 = plan->g_type == SALR_TYPE_F32;
   a.master = plan->has_master != 0;
+  const auto apply = a.p_f32 ? launch_muon_apply_f32 : a.master ? launch_muon_apply_master : launch_muon_apply_bf16;
+  hipStream_t s = static_cast<hipStream_t>(stream);
   int32_t m0 = 0;
   int64_t c0 = 0;
   for (int c = 0; c < kMuonClasses; ++c) {
-    if (plan->matrices[c] > 0)
-      if (const int e = status(launch_muon(a, c, m0, plan->matrices[c], c0, plan->chunks[c],
-                                           static_cast<hipStream_t>(stream))))
-        return e;
+    if (plan->matrices[c] > 0) {
+      hipError_t e = launch_muon_gram(a, c, c0, plan->chunks[c], s);
+      if (e == hipSuccess) e = launch_muon_iterate(a, c, m0, plan->matrices[c], s);
+      if (e == hipSuccess) e = apply(a, c, c0, plan->chunks[c], s);
+      if (e != hipSuccess) return SALR_ERR_HIP;
+    }
     m0 += plan->matrices[c];
     c0 += plan->chunks[c];
   }
