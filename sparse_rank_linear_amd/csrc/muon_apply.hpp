@@ -41,17 +41,18 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
   const auto src = to_global<typename Four<kSrc>::elem>(MASTER ? (void*)M.master : M.p);
   const auto qm = to_global<const float>(M.q);
   // (parameters a stage ahead as well, where the registers hold them)
-  constexpr bool kEarly = NT < 16;
+  constexpr bool kEarly = NT < 6;
   typename Four<GF>::raw vg[kNq];
   f32x4_t vm[kNq];
   typename Four<kSrc>::raw vp[kNq], next_p[kNq];
-  const auto load = [&](int64_t k) __attribute__((always_inline)) {
+  const auto load = [&](int64_t k, auto full) __attribute__((always_inline)) {
+    constexpr bool FULL = decltype(full)::value;
     const int left = (int)(k1 - k);
-    if (a.nesterov) st.template load<GF>(grad, k, left, vg);
-    st.template load<true>(mom, k, left, vm);
-    if (kEarly) st.template load<kSrc>(src, k, left, next_p);
+    if (a.nesterov) st.template load<FULL, GF>(grad, k, left, vg);
+    st.template load<FULL, true>(mom, k, left, vm);
+    if (kEarly) st.template load<FULL, kSrc>(src, k, left, next_p);
   };
-  load(k0);
+  if (k0 + KB <= k1) load(k0, std::true_type{});
   // Q's rows, columns in the order that the operands of u come in
   float qa[S / 4];
 #pragma unroll
@@ -64,8 +65,11 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
     place[q] = st.template place<P>(q);
     place_r[q] = st.template place<R>(q);
   }
+  wait_memory();
   lds_barrier();
-  for (int64_t k = k0; k < k1; k += KB) {
+  const auto stage = [&](int64_t k, auto full) __attribute__((always_inline)) {
+    constexpr bool FULL = decltype(full)::value;
+    const int left = (int)(k1 - k);
 #pragma unroll
     for (int q = 0; q < kNq; ++q) {
       if (kEarly) vp[q] = next_p[q];
@@ -73,7 +77,8 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
         st.template put<P>(lds, place[q], a.nesterov ? Four<GF>::value(vg[q]) * gs + a.momentum * vm[q] : vm[q]);
     }
     lds_barrier();
-    if (k + KB < k1) load(k + KB);
+    if (!kEarly) st.template load<FULL, kSrc>(src, k, left, vp);
+    if (FULL && k + 2 * KB <= k1) load(k + KB, full);
     for (int c = wave / NT; c < KB / 16; c += Shape::kCols) {
       f32x4_t acc = zero4();
       if constexpr (WIDE) {
@@ -91,18 +96,19 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
         *reinterpret_cast<f32x4_t*>(res + (16 * c + i) * R + 16 * tile + 4 * g) = acc;
       }
     }
-    const int left = (int)(k1 - k);
-    if (!kEarly) st.template load<kSrc>(src, k, left, vp);
     lds_barrier();
 #pragma unroll
     for (int q = 0; q < kNq; ++q) {
-      const int n = st.count(q, left);
-      if (n == 0) continue;
-      const int64_t at = st.element(q, k);
       const f32x4_t p = Four<kSrc>::value(vp[q]) * decay - rate * st.template get<R>(res, place_r[q]);
-      if (MASTER) store4<true>(to_global<float>(M.master) + at, n, p);
-      store4<PF>(param + at, n, p);
+      if (MASTER) st.template store<FULL, true>(to_global<float>(M.master), q, k, left, p);
+      st.template store<FULL, PF>(param, q, k, left, p);
     }
+  };
+  int64_t k = k0;
+  for (; k + KB <= k1; k += KB) stage(k, std::true_type{});
+  if (k < k1) {
+    load(k, std::false_type{});
+    stage(k, std::false_type{});
   }
 }
 

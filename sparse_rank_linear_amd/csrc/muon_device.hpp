@@ -81,16 +81,10 @@ template <bool F32>
 __device__ __forceinline__ typename Four<F32>::raw load4(global<const typename Four<F32>::elem> p) {
   return *(global<const typename Four<F32>::any>)p;
 }
-template <bool F32>
-__device__ __forceinline__ void store4(global<typename Four<F32>::elem> p, int n, f32x4_t x) {
-  if (n == 4) {
-    *(global<typename Four<F32>::any>)p = Four<F32>::pack(x);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 3; ++e)
-      if (e < n) p[e] = Four<F32>::one(x[e]);
-  }
-}
+// Waits for every load and store of the wave.  (Registers that are loaded once
+// before a loop are waited for here: the compiler would wait for them in the
+// loop, and so for the loads in flight there.)
+__device__ __forceinline__ void wait_memory() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 // A stage: KB columns of the long side from k on (`left` of them before the
 // chunk's end), in groups of four elements that lie together in memory: of a
@@ -121,15 +115,24 @@ struct Stage {
     if (!has(q)) return 0;
     return left >= KB ? 4 : max(0, min(4, WIDE ? left - x % (KB / 4) * 4 : left * s - 4 * x));
   }
-  template <bool F32>
+  // A stage's groups: whole stages in one batch without branches, the rest of
+  // the long side piece by piece.
+  template <bool FULL, bool F32>
   __device__ __forceinline__ void load(global<const typename Four<F32>::elem> p, int64_t k, int left,
                                        typename Four<F32>::raw (&v)[NQ]) const {
-    if (left >= KB) {
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) v[q] = load4<F32>(p + element(q, k));
+    for (int q = 0; q < NQ; ++q)
+      v[q] = FULL ? load4<F32>(p + element(q, k)) : Four<F32>::part(p + element(q, k), count(q, left));
+  }
+  template <bool FULL, bool F32>
+  __device__ __forceinline__ void store(global<typename Four<F32>::elem> p, int q, int64_t k, int left, f32x4_t x) const {
+    if (FULL) {
+      if (has(q)) *(global<typename Four<F32>::any>)(p + element(q, k)) = Four<F32>::pack(x);
     } else {
+      const int n = count(q, left);
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) v[q] = Four<F32>::part(p + element(q, k), count(q, left));
+      for (int e = 0; e < 4; ++e)
+        if (e < n) p[element(q, k) + e] = Four<F32>::one(x[e]);
     }
   }
   template <int PITCH>

@@ -39,12 +39,12 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
   const auto parts = to_global<float>(M.parts);
   typename Four<GF>::raw vg[kNq];
   f32x4_t vm[kNq];
-  const auto load = [&](int64_t k) __attribute__((always_inline)) {
+  const auto load = [&](int64_t k, auto full) __attribute__((always_inline)) {
     const int left = (int)(k1 - k);
-    st.template load<GF>(grad, k, left, vg);
-    st.template load<true>((global<const float>)mom, k, left, vm);
+    st.template load<decltype(full)::value, GF>(grad, k, left, vg);
+    st.template load<decltype(full)::value, true>((global<const float>)mom, k, left, vm);
   };
-  load(k0);
+  if (k0 + KB <= k1) load(k0, std::true_type{});
   for (int q = tid; q < Shape::kFloats; q += kThreads) lds[q] = 0.f;  // (past the short side it stays so)
   const int group = wave % Shape::kGroups, part = wave / Shape::kGroups;
   f64x4_t sum[Shape::kPer];
@@ -59,19 +59,18 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
   }
 #pragma unroll
   for (int q = 0; q < kNq; ++q) place[q] = st.template place<P>(q);
-  for (int64_t k = k0; k < k1; k += KB) {
+  const auto stage = [&](int64_t k, auto full) __attribute__((always_inline)) {
+    constexpr bool FULL = decltype(full)::value;
     const int left = (int)(k1 - k);
     lds_barrier();
 #pragma unroll
     for (int q = 0; q < kNq; ++q) {
-      if (!st.has(q)) continue;
-      const int n = st.count(q, left);
       const f32x4_t gg = Four<GF>::value(vg[q]) * gs, mm = a.momentum * vm[q] + gg;
-      store4<true>(mom + st.element(q, k), n, mm);
-      st.template put<P>(lds, place[q], a.nesterov ? gg + a.momentum * mm : mm);
+      st.template store<FULL, true>(mom, q, k, left, mm);
+      if (st.has(q)) st.template put<P>(lds, place[q], a.nesterov ? gg + a.momentum * mm : mm);
     }
     lds_barrier();
-    if (k + KB < k1) load(k + KB);
+    if (FULL && k + 2 * KB <= k1) load(k + KB, full);
 #pragma unroll
     for (int t = 0; t < Shape::kPer; ++t) {
       f32x4_t acc = zero4();
@@ -96,6 +95,12 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[t][e] += (double)acc[e];
     }
+  };
+  int64_t k = k0;
+  for (; k + KB <= k1; k += KB) stage(k, std::true_type{});
+  if (k < k1) {
+    load(k, std::false_type{});
+    stage(k, std::false_type{});
   }
   // the column parts meet in LDS, in order
   const auto out = (global<f32x4_t>)(parts + (int64_t)piece * Shape::kTiles * 256);
