@@ -113,7 +113,7 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
 }
 
 template <int NT, bool GF, bool PF, bool MASTER>
-__global__ __launch_bounds__(ApplyShape<NT>::kWaves * 64, 4) void muon_apply_kernel(MuonArgs a, int64_t c0) {
+__global__ __launch_bounds__(ApplyShape<NT>::kWaves * 64, NT == 3 || NT > 5 ? 4 : 5) void muon_apply_kernel(MuonArgs a, int64_t c0) {
   extern __shared__ __attribute__((aligned(16))) float lds[];  // u, then Q u
   const MuonChunk ch = a.chunks[c0 + blockIdx.x];
   const MuonMatrix& M = a.matrices[ch.matrix];

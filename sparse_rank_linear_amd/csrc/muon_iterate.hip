@@ -57,7 +57,8 @@ __device__ __forceinline__ Operand operand(int t, int tk, int i, int g) {
 
 template <int NT>
 struct IterShape {
-  static constexpr int kTiles = muon_lower(NT), kWaves = NT <= 5 ? 16 : 8, kThreads = 64 * kWaves;
+  static constexpr int kWaves = NT == 1 ? 1 : NT == 2 ? 4 : NT == 3 ? 8 : NT == 7 ? 14 : 16;
+  static constexpr int kTiles = muon_lower(NT), kThreads = 64 * kWaves;
   static constexpr int kPer = (kTiles + kWaves - 1) / kWaves;
 };
 
@@ -70,23 +71,45 @@ __device__ __forceinline__ void sym_products(const TA* A, const TB* B, const int
   constexpr int kPer = IterShape<NT>::kPer;
 #pragma unroll
   for (int t = 0; t < kPer; ++t) acc[t] = typename Acc<T>::type{0, 0, 0, 0};
-  constexpr int kUnroll = kPer == 1 ? NT : 1;  // (several tiles are enough to overlap; more does not fit the registers)
-#pragma unroll kUnroll
-  for (int tk = 0; tk < NT; ++tk) {
-    T u[kPer][4], v[kPer][4];
+  T u[2][kPer][4], v[2][kPer][4];
+  const auto load = [&](int tk, T (&x)[kPer][4], T (&y)[kPer][4]) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < kPer; ++t) {
-      const Operand x = operand(ti[t], tk, i, g), y = operand(tj[t], tk, i, g);
+      const Operand p = operand(ti[t], tk, i, g), q = operand(tj[t], tk, i, g);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        u[t][kk] = (T)A[x.first + kk * x.step];
-        v[t][kk] = (T)B[y.first + kk * y.step];
+        x[t][kk] = (T)A[p.first + kk * p.step];
+        y[t][kk] = (T)B[q.first + kk * q.step];
       }
     }
+  };
+  const auto multiply = [&](const T (&x)[kPer][4], const T (&y)[kPer][4]) __attribute__((always_inline)) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-      for (int t = 0; t < kPer; ++t) acc[t] = Acc<T>::mul(u[t][kk], v[t][kk], acc[t]);
+      for (int t = 0; t < kPer; ++t) acc[t] = Acc<T>::mul(x[t][kk], y[t][kk], acc[t]);
+  };
+  // The next tiles' operands are read while these are multiplied.
+  load(0, u[0], v[0]);
+  if constexpr (kPer == 1) {
+#pragma unroll
+    for (int tk = 0; tk < NT; ++tk) {
+      if (tk + 1 < NT) load(tk + 1, u[(tk + 1) & 1], v[(tk + 1) & 1]);
+      multiply(u[tk & 1], v[tk & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+    // (unrolled, all addresses would be computed first, which the registers do not hold)
+#pragma unroll 1
+    for (int tk = 0; tk + 1 < NT; tk += 2) {
+      load(tk + 1, u[1], v[1]);
+      multiply(u[0], v[0]);
+      __builtin_amdgcn_sched_barrier(0);
+      load(min(tk + 2, NT - 1), u[0], v[0]);
+      multiply(u[1], v[1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (NT % 2 == 1) multiply(u[0], v[0]);
   }
 }
 
