@@ -24,7 +24,6 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kSubs = kAdapterTile / 16;  // 16-token sides of a tile
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
@@ -52,11 +51,12 @@ __device__ __forceinline__ int group_of(const uint32_t* start, int n, uint32_t x
 }
 
 // One workgroup sorts: a stable counting sort over the groups 0..count (the
-// last: no adapter), each wave on its own stretch of the tokens.  One pass of
-// LDS atomics counts, prefix sums place the groups and the waves within them,
-// and a second pass places 64 tokens at a time, one ballot for each adapter
-// among them.  Then the lists of tiles and chunks.
-__global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_t* ids, AdapterPlan p, int waves) {
+// last: no adapter), each wave on its own stretch of the tokens.  One pass
+// counts, prefix sums place the groups and the waves within them, and a second
+// pass places, 64 tokens at a time: those of one adapter find each other by a
+// ballot for each bit of its number.  Then the lists of tiles and chunks.
+__global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_t* ids, AdapterPlan p, int waves,
+                                                                    int bits) {
   extern __shared__ uint32_t sm[];
   const int G = p.count + 1;
   uint32_t* cnt = sm;                          // [waves][G]
@@ -71,11 +71,32 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
   const int64_t M = p.M;
   const int64_t each = ((M + waves - 1) / waves + 63) / 64 * 64;
   const int64_t t0 = min(M, wave * each), t1 = min(M, t0 + each);  // (no tokens from wave `waves` on)
-  const auto group = [&](int64_t t) -> int {
-    const uint32_t id = (uint32_t)ids[t];
-    return id < (uint32_t)p.count ? (int)id : p.count;
+  const uint64_t below = (1ull << lane) - 1ull;
+  // f(token, its group, whether it exists, the lanes of the same group) for 64
+  // tokens at a time, in order; kAhead such batches are read together
+  const auto walk = [&](auto f) __attribute__((always_inline)) {
+    constexpr int kAhead = 8;
+    for (int64_t b = t0; b < t1; b += 64 * kAhead) {
+      int g[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) g[q] = ids[min(b + 64 * q + lane, t1 - 1)];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        if (b + 64 * q >= t1) break;
+        const bool live = b + 64 * q + lane < t1;
+        const int x = (uint32_t)g[q] < (uint32_t)p.count ? g[q] : p.count;
+        uint64_t same = __ballot(live);
+        for (int k = 0; k < bits; ++k) {
+          const uint64_t set = __ballot((x >> k) & 1);
+          same &= (x >> k) & 1 ? set : ~set;
+        }
+        f(b + 64 * q + lane, x, live, same);
+      }
+    }
   };
-  for (int64_t t = t0 + lane; t < t1; t += 64) atomicAdd(&cnt[wave * G + group(t)], 1u);
+  walk([&](int64_t, int g, bool live, uint64_t same) {
+    if (live && (same & below) == 0) cnt[wave * G + g] += (uint32_t)__popcll(same);
+  });
   __syncthreads();
   // each thread a run of groups: their totals, then what lies before them
   const int per = (G + kPlanThreads - 1) / kPlanThreads;
@@ -84,7 +105,7 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
   const auto add = [&](int g, uint32_t c) {
     const uint32_t ch = g < p.count ? (c + p.chunk - 1) / p.chunk : 0;
     n[0] += c;
-    n[1] += (c + kAdapterTile - 1) / kAdapterTile;
+    n[1] += (c + p.tile - 1) / p.tile;
     n[2] += ch;
     n[3] += ch > 1 ? ch : 0;
   };
@@ -136,28 +157,20 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
     p.head[1] = (int32_t)chunk[G];
   }
   // place the tokens
-  for (int64_t b = t0; b < t1; b += 64) {
-    const int64_t t = b + lane;
-    const bool live = t < t1;
-    const int g = live ? group(t) : -1;
-    uint64_t todo = __ballot(live);
-    while (todo) {
-      const int first = __builtin_ctzll(todo);
-      const int cur = __builtin_amdgcn_readlane(g, first);
-      const uint64_t same = __ballot(g == cur);
-      uint32_t* at = &cnt[wave * G + cur];
-      if (g == cur) p.order[*at + __popcll(same & ((1ull << lane) - 1ull))] = (int32_t)t;
-      __builtin_amdgcn_wave_barrier();
-      if (lane == first) *at += (uint32_t)__popcll(same);
-      __builtin_amdgcn_wave_barrier();
-      todo &= ~same;
-    }
-  }
+  walk([&](int64_t t, int g, bool live, uint64_t same) {
+    if (!live) return;
+    uint32_t* at = &cnt[wave * G + g];
+    const uint32_t first = *at;
+    __builtin_amdgcn_wave_barrier();
+    if ((same & below) == 0) *at = first + (uint32_t)__popcll(same);
+    p.order[first + __popcll(same & below)] = (int32_t)t;
+    __builtin_amdgcn_wave_barrier();
+  });
   // the lists
   for (uint32_t i = tid; i < tile[G]; i += kPlanThreads) {
     const int g = group_of(tile, G, i);
-    const uint32_t b = off[g] + (i - tile[g]) * kAdapterTile;
-    p.tiles[i] = AdapterTile{g, (int32_t)b, (int32_t)min(off[g + 1], b + kAdapterTile), -1};
+    const uint32_t b = off[g] + (i - tile[g]) * p.tile;
+    p.tiles[i] = AdapterTile{g, (int32_t)b, (int32_t)min(off[g + 1], b + (uint32_t)p.tile), -1};
   }
   for (uint32_t i = tid; i < chunk[G]; i += kPlanThreads) {
     const int g = group_of(chunk, G, i);
@@ -187,19 +200,31 @@ __device__ __forceinline__ void limbs(float x, uint16_t* w, int n) {
   }
 }
 
+// The sum of T's pieces at one place, eight loads at a time.
+__device__ __forceinline__ f32x4_t sum_pieces(const float* at, int64_t plane, int splits) {
+  f32x4_t v = zero4();
+  for (int s = 0; s < splits; s += 8) {
+    f32x4_t x[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = *reinterpret_cast<const f32x4_t*>(at + min(s + q, splits - 1) * plane);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v += s + q < splits ? x[q] : zero4();
+  }
+  return v;
+}
+
 // ---- down: T = X W^T for one tile, RT x 16 ranks, one piece of the columns ----
 //
 // D[rank][token] tiles; both operands run along the columns and come straight
 // from memory, 16 bytes a lane.  Each wave takes every kWaves-th 64 columns of
 // the piece; the waves' sums meet in LDS, in wave order.
-template <int RT>
+template <int RT, int NS>
 __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterCommon c, AdapterDown j0, AdapterDown j1,
                                                                 int groups) {
   __shared__ f32x4_t sums[kWaves][RT][64];
   const AdapterPlan& p = c.plan;
-  if ((int)blockIdx.x >= p.head[0]) return;
-  const AdapterTile t = p.tiles[blockIdx.x];
-  if (t.adapter >= p.count) return;
+  const AdapterTile t = p.tiles[blockIdx.x];  // (past the last: whatever was there)
+  if ((int)blockIdx.x >= p.head[0] || t.adapter >= p.count) return;
   const AdapterDown j = blockIdx.z ? j1 : j0;
   const int split = blockIdx.y / groups, rank0 = (blockIdx.y % groups) * RT * 16;
   const int live = live_ranks(c, t.adapter);
@@ -208,50 +233,79 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterCommon c,
   const int n = t.end - t.begin, subs = (n + 15) / 16;
   // (tokens past the tile's last and ranks past the live ones repeat those:
   // what comes of them is not used)
-  const uint16_t* xr[kSubs];
+  const uint16_t* xr[NS];
 #pragma unroll
-  for (int s = 0; s < kSubs; ++s)
-    xr[s] = j.X + (int64_t)p.order[t.begin + min(16 * s + i, n - 1)] * j.K + 8 * g;
-  const uint16_t* wr[RT];
-#pragma unroll
-  for (int a = 0; a < RT; ++a)
-    wr[a] = j.W + ((int64_t)t.adapter * c.r + min(rank0 + 16 * a + i, live - 1)) * j.K + 8 * g;
-  f32x4_t acc[RT][kSubs];
-#pragma unroll
-  for (int a = 0; a < RT; ++a)
-#pragma unroll
-    for (int s = 0; s < kSubs; ++s) acc[a][s] = zero4();
+  for (int s = 0; s < NS; ++s) xr[s] = j.X + (int64_t)p.order[t.begin + min(16 * s + i, n - 1)] * j.K;
   const int64_t k0 = (int64_t)split * j.cols, k1 = min(j.K, k0 + j.cols);
-  const auto body = [&](auto nsubs) __attribute__((always_inline)) {
-    constexpr int NS = decltype(nsubs)::value;
-    for (int64_t k = k0 + 64 * wave; k < k1; k += 64 * kWaves) {
-      u32x4_t x[2][NS], w[2][RT];
+  constexpr int64_t kStep = 64 * kWaves;
+  f32x4_t acc[RT][NS];
+#pragma unroll
+  for (int a = 0; a < RT; ++a)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) acc[a][s] = zero4();
+  // RL rank tiles: those with live ranks, as far as they are told apart
+  const auto body = [&](auto ranks) __attribute__((always_inline)) {
+    constexpr int RL = decltype(ranks)::value;
+    const uint16_t* wr[RL];
+#pragma unroll
+    for (int a = 0; a < RL; ++a)
+      wr[a] = j.W + ((int64_t)t.adapter * c.r + min(rank0 + 16 * a + i, live - 1)) * j.K;
+    const auto load = [&](int64_t k, u32x4_t (&xs)[2][NS], u32x4_t (&ws)[2][RL]) __attribute__((always_inline)) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool in = k + 32 * h + 8 * g < k1;
+        // (a lane past the piece reads its first columns instead, and takes zeros)
+        const int64_t at = k + 32 * h + 8 * g < k1 ? k + 32 * h + 8 * g : k0;
 #pragma unroll
-        for (int a = 0; a < RT; ++a) w[h][a] = in ? load16(wr[a] + k + 32 * h) : zero_u4();
+        for (int a = 0; a < RL; ++a) ws[h][a] = load16(wr[a] + at);
 #pragma unroll
-        for (int s = 0; s < NS; ++s) x[h][s] = in ? load16(xr[s] + k + 32 * h) : zero_u4();
+        for (int s = 0; s < NS; ++s) xs[h][s] = load16(xr[s] + at);
       }
+    };
+    const auto multiply = [&](int64_t k, u32x4_t (&xs)[2][NS], u32x4_t (&ws)[2][RL]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        if (k + 64 > k1) {
+          const bool in = k + 32 * h + 8 * g < k1;
 #pragma unroll
-        for (int a = 0; a < RT; ++a)
+          for (int a = 0; a < RL; ++a) ws[h][a] = in ? ws[h][a] : zero_u4();
 #pragma unroll
-          for (int s = 0; s < NS; ++s) acc[a][s] = mfma_16x16x32(w[h][a], x[h][s], acc[a][s]);
+          for (int s = 0; s < NS; ++s) xs[h][s] = in ? xs[h][s] : zero_u4();
+        }
+#pragma unroll
+        for (int a = 0; a < RL; ++a)
+#pragma unroll
+          for (int s = 0; s < NS; ++s) acc[a][s] = mfma_16x16x32(ws[h][a], xs[h][s], acc[a][s]);
+      }
+    };
+    if constexpr (NS == 1) {
+      // (few registers a step: the next step's loads ahead)
+      u32x4_t x[2][2][NS], w[2][2][RL];
+      int64_t k = k0 + 64 * wave;
+      if (k < k1) load(k, x[0], w[0]);
+      for (; k < k1; k += 2 * kStep) {
+        if (k + kStep < k1) load(k + kStep, x[1], w[1]);
+        multiply(k, x[0], w[0]);
+        if (k + kStep >= k1) break;
+        if (k + 2 * kStep < k1) load(k + 2 * kStep, x[0], w[0]);
+        multiply(k + kStep, x[1], w[1]);
+      }
+    } else {
+      u32x4_t x[2][NS], w[2][RL];
+      for (int64_t k = k0 + 64 * wave; k < k1; k += kStep) {
+        load(k, x, w);
+        multiply(k, x, w);
+      }
     }
   };
-  if (subs == 1) body(std::integral_constant<int, 1>{});
-  else if (subs == 2) body(std::integral_constant<int, 2>{});
-  else body(std::integral_constant<int, kSubs>{});
+  if (RT > 1 && live - rank0 <= 16) body(std::integral_constant<int, 1>{});
+  else body(std::integral_constant<int, RT>{});
   float* out = j.T + (int64_t)split * p.M * c.r;
 #pragma unroll
-  for (int s = 0; s < kSubs; ++s) {
+  for (int s = 0; s < NS; ++s) {
     if (s >= subs) break;
 #pragma unroll
     for (int a = 0; a < RT; ++a) sums[wave][a][lane] = acc[a][s];
-    __syncthreads();
+    lds_barrier();
     for (int q = tid; q < RT * 64; q += kThreads) {
       const int a = q >> 6, l = q & 63;
       f32x4_t v = sums[0][a][l];
@@ -260,16 +314,15 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterCommon c,
       const int row = 16 * s + (l & 15), rank = rank0 + 16 * a + 4 * (l >> 4);
       if (row < n && rank < c.r) *reinterpret_cast<f32x4_t*>(out + (int64_t)(t.begin + row) * c.r + rank) = v;
     }
-    __syncthreads();
+    if (NS > 1) lds_barrier();
   }
 }
 
 // ---- finish: the pieces' sums as bf16 planes (for the gradients) ----
 __global__ __launch_bounds__(kThreads) void adapter_finish_kernel(AdapterCommon c, AdapterFinish x, AdapterFinish y) {
   const AdapterPlan& p = c.plan;
-  if ((int)blockIdx.x >= p.head[0]) return;
-  const AdapterTile t = p.tiles[blockIdx.x];
-  if (t.adapter >= p.count) return;
+  const AdapterTile t = p.tiles[blockIdx.x];  // (past the last: whatever was there)
+  if ((int)blockIdx.x >= p.head[0] || t.adapter >= p.count) return;
   const AdapterFinish f = blockIdx.y ? y : x;
   const int live = live_ranks(c, t.adapter), rq = c.r / 4;
   const float scale = scale_of(c, t.adapter);
@@ -278,8 +331,7 @@ __global__ __launch_bounds__(kThreads) void adapter_finish_kernel(AdapterCommon 
     const int rank = q % rq * 4;
     const int64_t at = (int64_t)(t.begin + q / rq) * c.r + rank;
     f32x4_t v = zero4();
-    if (rank < live)
-      for (int s = 0; s < f.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(f.T + s * plane + at);
+    if (rank < live) v = sum_pieces(f.T + at, plane, f.splits);
     uint16_t w[4][3];
 #pragma unroll
     for (int e = 0; e < 4; ++e) limbs(rank + e < live ? v[e] * scale : 0.f, w[e], 3);
@@ -296,73 +348,59 @@ __global__ __launch_bounds__(kThreads) void adapter_finish_kernel(AdapterCommon 
 // of it) waits in LDS.  A wave takes 64 outputs at a time; row m of the four
 // tiles q is output 16 (m / 4) + 4 q + m % 4, so that a lane ends up with 16
 // consecutive outputs of one token: 32-byte accesses, 128 bytes a token.
-template <int RC, bool PLANES>
+template <int RC, int NS, bool PLANES>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, AdapterUp u) {
   constexpr int kPitch = RC * 32 + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t v[2][kAdapterTile][kPitch];
+  __shared__ __attribute__((aligned(16))) uint16_t v[2][16 * NS][kPitch];
   const AdapterPlan& p = c.plan;
+  const AdapterTile t = p.tiles[blockIdx.x];  // (past the last: whatever was there)
   if ((int)blockIdx.x >= p.head[0]) return;
-  const AdapterTile t = p.tiles[blockIdx.x];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
-  const int n = t.end - t.begin, subs = (n + 15) / 16;
+  const int n = t.end - t.begin;
   const bool bare = t.adapter >= p.count;
   const int live = bare ? 0 : live_ranks(c, t.adapter);
   if (live == 0 && u.base == u.out) return;
   const bool vec = (u.N & 7) == 0;
   const int64_t n0 = (int64_t)blockIdx.y * u.slice, n1 = min(u.N, n0 + u.slice);
-  if (live > 0) {
-    const float scale = scale_of(c, t.adapter);
-    const int64_t plane = p.M * c.r;
-    constexpr int kQuads = RC * 8;
-    for (int q = tid; q < subs * 16 * kQuads; q += kThreads) {
-      const int row = q / kQuads, rank = q % kQuads * 4;
-      const bool in = row < n && rank < live;
-      const int64_t at = (int64_t)(t.begin + row) * c.r + rank;
-      u32x2_t hi = {0u, 0u}, lo = {0u, 0u};
-      if constexpr (PLANES) {
-        if (in) {
-          hi = *reinterpret_cast<const u32x2_t*>(u.planes + at);
-          lo = *reinterpret_cast<const u32x2_t*>(u.planes + plane + at);
-        }
-      } else if (in) {
-        f32x4_t x = zero4();
-        for (int s = 0; s < u.splits; ++s) x += *reinterpret_cast<const f32x4_t*>(u.T + s * plane + at);
-        uint16_t w[4][2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) limbs(rank + e < live ? x[e] * scale : 0.f, w[e], 2);
-        hi = u32x2_t{w[0][0] | (uint32_t)w[1][0] << 16, w[2][0] | (uint32_t)w[3][0] << 16};
-        lo = u32x2_t{w[0][1] | (uint32_t)w[1][1] << 16, w[2][1] | (uint32_t)w[3][1] << 16};
-      }
-      *reinterpret_cast<u32x2_t*>(&v[0][row][rank]) = hi;
-      *reinterpret_cast<u32x2_t*>(&v[1][row][rank]) = lo;
-    }
-    __syncthreads();
-  }
-  int64_t row[kSubs];
-#pragma unroll
-  for (int s = 0; s < kSubs; ++s) row[s] = (int64_t)p.order[t.begin + min(16 * s + i, n - 1)] * u.N;
   const uint16_t* W = u.W + (int64_t)(bare ? 0 : t.adapter) * u.N * c.r;
-  for (int64_t nb = n0 + 64 * wave; nb < n1; nb += 64 * kWaves) {
-    u32x4_t w[4][RC];
+  // past the live ranks the weights may hold anything: masked out
+  u32x4_t mask[RC];
+#pragma unroll
+  for (int k = 0; k < RC; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int left = live - 32 * k - 8 * g - 2 * e;
+      mask[k][e] = (left > 0 ? 0xFFFFu : 0u) | (left > 1 ? 0xFFFF0000u : 0u);
+    }
+  int64_t row[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) row[s] = (int64_t)p.order[t.begin + min(16 * s + i, n - 1)] * u.N;
+  // 64 outputs' weights and base (a lane: 16 outputs of each of its tokens)
+  const auto load = [&](int64_t nb, u32x4_t (&w)[4][RC], u32x4_t (&b)[NS][2]) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int64_t o = min(nb + 16 * (i >> 2) + 4 * q + (i & 3), u.N - 1);
 #pragma unroll
       for (int k = 0; k < RC; ++k) {
-        // (past the live ranks the weights may hold anything: zeros there)
-        const int rank = 32 * k + 8 * g, left = live - rank;
-        w[q][k] = left > 0 ? load16(W + o * c.r + rank) : zero_u4();
-        if (left > 0 && left < 8) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[q][k][e] &= (2 * e < left ? 0xFFFFu : 0u) | (2 * e + 1 < left ? 0xFFFF0000u : 0u);
-        }
+        const int rank = 32 * k + 8 * g;
+        w[q][k] = load16(W + o * c.r + (rank < live ? rank : 0));
       }
     }
+    if (vec && u.base) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) b[s][h] = load16(u.base + row[s] + min(nb + 16 * g + 8 * h, u.N - 8));
+    }
+  };
+  const auto finish = [&](int64_t nb, u32x4_t (&w)[4][RC], const u32x4_t (&b)[NS][2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int k = 0; k < RC; ++k) w[q][k] &= mask[k];
     const int64_t o0 = nb + 16 * g;  // this lane's 16 outputs
 #pragma unroll
-    for (int s = 0; s < kSubs; ++s) {
-      if (s >= subs) break;
+    for (int s = 0; s < NS; ++s) {
       f32x4_t acc[4] = {zero4(), zero4(), zero4(), zero4()};
       if (live > 0) {
 #pragma unroll
@@ -375,14 +413,12 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, A
           }
       }
       if (16 * s + i >= n) continue;
-      const uint16_t* b = u.base ? u.base + row[s] : nullptr;
       uint16_t* out = u.out + row[s];
       if (vec) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int64_t o = o0 + 8 * h;
-          if (o >= n1) break;
-          const u32x4_t x = b ? load16(b + o) : zero_u4();
+          const u32x4_t x = u.base ? b[s][h] : zero_u4();
           u32x4_t y;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -390,20 +426,69 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, A
             const float hi = bf16_to_f32((uint16_t)(x[e] >> 16)) + acc[2 * h + e / 2][2 * (e & 1) + 1];
             y[e] = f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
           }
-          *reinterpret_cast<u32x4_t*>(out + o) = live > 0 ? y : x;
+          if (o < n1) *reinterpret_cast<u32x4_t*>(out + o) = live > 0 ? y : x;
         }
       } else {
+        const uint16_t* base = u.base ? u.base + row[s] : nullptr;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int64_t o = o0 + 4 * q + e;
             if (o >= n1) continue;
-            const uint16_t x = b ? b[o] : (uint16_t)0;
+            const uint16_t x = base ? base[o] : (uint16_t)0;
             out[o] = live > 0 ? f32_to_bf16(bf16_to_f32(x) + acc[q][e]) : x;
           }
       }
     }
+  };
+  // (the next outputs' loads ahead, where the registers hold them)
+  constexpr bool kAhead = NS == 1;
+  u32x4_t w[2][4][RC], b[2][NS][2];
+  constexpr int64_t kStep = 64 * kWaves;
+  int64_t nb = n0 + 64 * wave;
+  if (nb < n1) load(nb, w[0], b[0]);
+  // V into LDS while those are under way
+  if (live > 0) {
+    const float scale = scale_of(c, t.adapter);
+    const int64_t plane = p.M * c.r;
+    constexpr int kQuads = RC * 8;
+    for (int q = tid; q < NS * 16 * kQuads; q += kThreads) {
+      const int vr = q / kQuads, rank = q % kQuads * 4;
+      const bool in = vr < n && rank < live;
+      const int64_t at = (int64_t)(t.begin + vr) * c.r + rank;
+      u32x2_t hi = {0u, 0u}, lo = {0u, 0u};
+      if constexpr (PLANES) {
+        if (in) {
+          hi = *reinterpret_cast<const u32x2_t*>(u.planes + at);
+          lo = *reinterpret_cast<const u32x2_t*>(u.planes + plane + at);
+        }
+      } else if (in) {
+        const f32x4_t x = sum_pieces(u.T + at, plane, u.splits);
+        uint16_t h[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) limbs(rank + e < live ? x[e] * scale : 0.f, h[e], 2);
+        hi = u32x2_t{h[0][0] | (uint32_t)h[1][0] << 16, h[2][0] | (uint32_t)h[3][0] << 16};
+        lo = u32x2_t{h[0][1] | (uint32_t)h[1][1] << 16, h[2][1] | (uint32_t)h[3][1] << 16};
+      }
+      *reinterpret_cast<u32x2_t*>(&v[0][vr][rank]) = hi;
+      *reinterpret_cast<u32x2_t*>(&v[1][vr][rank]) = lo;
+    }
+    lds_barrier();
+  }
+  if constexpr (!kAhead) {
+    for (; nb < n1; nb += kStep) {
+      finish(nb, w[0], b[0]);
+      if (nb + kStep < n1) load(nb + kStep, w[0], b[0]);
+    }
+    return;
+  }
+  for (; nb < n1; nb += 2 * kStep) {
+    if (nb + kStep < n1) load(nb + kStep, w[1], b[1]);
+    finish(nb, w[0], b[0]);
+    if (nb + kStep >= n1) break;
+    if (nb + 2 * kStep < n1) load(nb + 2 * kStep, w[0], b[0]);
+    finish(nb + kStep, w[1], b[1]);
   }
 }
 
@@ -465,8 +550,8 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
   __shared__ __attribute__((aligned(16))) uint16_t cols[32 * kColPitch];
   __shared__ __attribute__((aligned(16))) uint16_t rank[3][32 * kRankPitch];
   const AdapterPlan& p = c.plan;
-  if ((int)blockIdx.y >= p.head[1]) return;
   const AdapterTile t = p.chunks[blockIdx.y];
+  if ((int)blockIdx.y >= p.head[1]) return;
   const int by = blockIdx.x / groups, rank0 = (blockIdx.x % groups) * RT * 16;
   const bool is_a = by < blocks_a;
   const AdapterGrad j = is_a ? ga : gb;
@@ -481,12 +566,16 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
   const bool col_in = c0 + col < j.C;
   constexpr int kRankPieces = 3 * 32 * RT * 2, kRankPasses = (kRankPieces + kThreads - 1) / kThreads;
   u32x4_t vc[2], vr[kRankPasses];
+  int tok[2];  // the tokens of the next stage
+  const auto next_tokens = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) tok[h] = p.order[min(b + row + 16 * h, t.end - 1)];
+  };
   const auto load = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at = b + row + 16 * h;
-      vc[h] = at < t.end && col_in ? load16(j.cols + (int64_t)p.order[at] * j.C + c0 + col) : zero_u4();
-    }
+    for (int h = 0; h < 2; ++h)
+      vc[h] = b + row + 16 * h < t.end && col_in ? load16(j.cols + (int64_t)tok[h] * j.C + c0 + col) : zero_u4();
+    if (b + 32 < t.end) next_tokens(b + 32);
 #pragma unroll
     for (int q = 0; q < kRankPasses; ++q) {
       const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = rank0 + x % (RT * 2) * 8;
@@ -494,9 +583,10 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
                                                          : zero_u4();
     }
   };
+  next_tokens(t.begin);
   load(t.begin);
   for (int b = t.begin; b < t.end; b += 32) {
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4_t*>(&cols[(row + 16 * h) * kColPitch + col]) = vc[h];
 #pragma unroll
@@ -504,7 +594,7 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
       const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = x % (RT * 2) * 8;
       if (x < kRankPieces) *reinterpret_cast<u32x4_t*>(&rank[l][y * kRankPitch + z]) = vr[q];
     }
-    __syncthreads();
+    lds_barrier();
     if (b + 32 < t.end) load(b + 32);
     u32x4_t x[2];
 #pragma unroll
@@ -576,7 +666,9 @@ hipError_t launch_adapter_plan(const int32_t* ids, const AdapterPlan& p, hipStre
   // (each wave's counters: 4 waves keep 4096 adapters within 132 KB of LDS)
   const int waves = p.count <= 1024 ? kPlanWaves : 4;
   const size_t lds = ((size_t)waves * (p.count + 1) + 4 * (size_t)(p.count + 2)) * 4;
-  hipLaunchKernelGGL(adapter_plan_kernel, dim3(1), dim3(kPlanThreads), lds, s, ids, p, waves);
+  int bits = 0;
+  while ((1 << bits) <= p.count) ++bits;
+  hipLaunchKernelGGL(adapter_plan_kernel, dim3(1), dim3(kPlanThreads), lds, s, ids, p, waves, bits);
   return hipGetLastError();
 }
 
@@ -584,9 +676,12 @@ hipError_t launch_adapter_down(const AdapterCommon& c, const AdapterDown* jobs, 
   int splits = 0;
   for (int q = 0; q < n_jobs; ++q) splits = std::max(splits, jobs[q].splits);
   with_rank_tiles(c.r, [&](auto rt, int groups) {
-    hipLaunchKernelGGL((adapter_down_kernel<decltype(rt)::value>),
-                       dim3((unsigned)c.plan.max_tiles, (unsigned)(splits * groups), (unsigned)n_jobs), dim3(kThreads), 0,
-                       s, c, jobs[0], jobs[n_jobs - 1], groups);
+    constexpr int RT = decltype(rt)::value;
+    const dim3 grid((unsigned)c.plan.max_tiles, (unsigned)(splits * groups), (unsigned)n_jobs);
+    if (c.plan.tile == kAdapterSmallTile)
+      hipLaunchKernelGGL((adapter_down_kernel<RT, 1>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], groups);
+    else
+      hipLaunchKernelGGL((adapter_down_kernel<RT, 4>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], groups);
   });
   return hipGetLastError();
 }
@@ -601,10 +696,15 @@ hipError_t launch_adapter_up(const AdapterCommon& c, const AdapterUp& u, hipStre
   const dim3 grid((unsigned)c.plan.max_tiles, (unsigned)((u.N + u.slice - 1) / u.slice));
   with_rank_chunks(c.r, [&](auto rc) {
     constexpr int RC = decltype(rc)::value;
-    if (u.planes)
-      hipLaunchKernelGGL((adapter_up_kernel<RC, true>), grid, dim3(kThreads), 0, s, c, u);
-    else
-      hipLaunchKernelGGL((adapter_up_kernel<RC, false>), grid, dim3(kThreads), 0, s, c, u);
+    const auto go = [&](auto ns) {
+      constexpr int NS = decltype(ns)::value;
+      if (u.planes)
+        hipLaunchKernelGGL((adapter_up_kernel<RC, NS, true>), grid, dim3(kThreads), 0, s, c, u);
+      else
+        hipLaunchKernelGGL((adapter_up_kernel<RC, NS, false>), grid, dim3(kThreads), 0, s, c, u);
+    };
+    if (c.plan.tile == kAdapterSmallTile) go(std::integral_constant<int, 1>{});
+    else go(std::integral_constant<int, 4>{});
   });
   return hipGetLastError();
 }

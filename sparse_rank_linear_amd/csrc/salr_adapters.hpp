@@ -8,7 +8,11 @@
 
 namespace salr {
 
-constexpr int kAdapterTile = 64;          // tokens of a tile, all of one adapter
+// Tokens of a tile, all of one adapter: few tokens take small tiles (more
+// workgroups, leaner kernels), many take large ones (the adapter is read once
+// for four times the tokens).
+constexpr int kAdapterSmallTile = 16, kAdapterLargeTile = 64;
+constexpr int64_t kAdapterSmallTokens = 1024;  // the most with small tiles
 constexpr int kAdapterMinChunk = 1024;    // tokens that one workgroup sums a gradient over, at least
 constexpr int kAdapterMaxSplits = 32;     // pieces of a contraction over K (or N)
 
@@ -28,7 +32,7 @@ struct AdapterPlan {
   AdapterTile* tiles;
   AdapterTile* chunks;
   int64_t M;
-  int32_t count, chunk;
+  int32_t count, tile, chunk;
   int32_t max_tiles, max_chunks, max_parts;
 };
 

@@ -38,7 +38,8 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
   p.M = M;
   p.count = count;
   p.chunk = (int32_t)std::max<int64_t>(salr::kAdapterMinChunk, cdiv(cdiv(M, 32), 64) * 64);
-  p.max_tiles = (int32_t)most_pieces(M, count + 1, salr::kAdapterTile);
+  p.tile = M <= salr::kAdapterSmallTokens ? salr::kAdapterSmallTile : salr::kAdapterLargeTile;
+  p.max_tiles = (int32_t)most_pieces(M, count + 1, p.tile);
   p.max_chunks = (int32_t)most_pieces(M, count, p.chunk);
   p.max_parts = (int32_t)std::min<int64_t>(p.max_chunks, 2 * M / p.chunk);
   char* at = static_cast<char*>(buffer);
@@ -60,7 +61,7 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
 // A contraction over K columns in pieces: enough workgroups for the CUs.  Of M
 // tokens the pieces come to at most min(kAdapterMaxSplits M, M + 64 kGroups)
 // rows of T.
-constexpr int64_t kGroups = 1024;
+constexpr int64_t kGroups = 512;
 int64_t t_rows(int64_t M) { return std::min<int64_t>(salr::kAdapterMaxSplits * M, M + 64 * kGroups); }
 void cut(salr::AdapterDown* d, int64_t tiles, int32_t r) {
   const int64_t work = std::max<int64_t>(1, tiles * cdiv(r, 80));
@@ -69,7 +70,7 @@ void cut(salr::AdapterDown* d, int64_t tiles, int32_t r) {
   d->splits = (int32_t)cdiv(d->K, d->cols);
 }
 int32_t up_slice(int64_t N, int64_t tiles) {
-  const int64_t want = std::max<int64_t>(1, cdiv(kGroups, std::max<int64_t>(1, tiles)));
+  const int64_t want = std::max<int64_t>(1, cdiv(2 * kGroups, std::max<int64_t>(1, tiles)));
   return (int32_t)(cdiv(cdiv(N, want), 256) * 256);
 }
 
