@@ -217,16 +217,19 @@ __device__ __forceinline__ f32x4_t sum_pieces(const float* at, int64_t plane, in
 //
 // D[rank][token] tiles; both operands run along the columns and come straight
 // from memory, 16 bytes a lane.  Each wave takes every kWaves-th 64 columns of
-// the piece; the waves' sums meet in LDS, in wave order.
+// the piece; the waves' sums meet in LDS, in wave order.  Neighbouring
+// workgroups take a tile's pieces (they run on different dies: a die then sees
+// the same pieces of the adapters again and again, in its own cache).
 template <int RT, int NS>
 __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterCommon c, AdapterDown j0, AdapterDown j1,
-                                                                int groups) {
+                                                                int parts, int groups) {
   __shared__ f32x4_t sums[kWaves][RT][64];
   const AdapterPlan& p = c.plan;
-  const AdapterTile t = p.tiles[blockIdx.x];  // (past the last: whatever was there)
-  if ((int)blockIdx.x >= p.head[0] || t.adapter >= p.count) return;
-  const AdapterDown j = blockIdx.z ? j1 : j0;
-  const int split = blockIdx.y / groups, rank0 = (blockIdx.y % groups) * RT * 16;
+  const int ti = blockIdx.x / parts, part = blockIdx.x % parts;
+  const AdapterTile t = p.tiles[ti];  // (past the last: whatever was there)
+  if (ti >= p.head[0] || t.adapter >= p.count) return;
+  const AdapterDown j = blockIdx.y ? j1 : j0;
+  const int split = part / groups, rank0 = (part % groups) * RT * 16;
   const int live = live_ranks(c, t.adapter);
   if (split >= j.splits || rank0 >= live) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
@@ -346,22 +349,25 @@ __global__ __launch_bounds__(kThreads) void adapter_finish_kernel(AdapterCommon 
 //
 // D[output][token] tiles.  V (two bf16 planes: its rounding stays below 2^-16
 // of it) waits in LDS.  A wave takes 64 outputs at a time; row m of the four
-// tiles q is output 16 (m / 4) + 4 q + m % 4, so that a lane ends up with 16
-// consecutive outputs of one token: 32-byte accesses, 128 bytes a token.
+// tiles q is output 32 (q / 2) + 8 (m / 4) + 4 (q % 2) + m % 4, so that a lane
+// ends up with twice 8 consecutive outputs of one token, and four lanes with 64
+// bytes that lie together.
 template <int RC, int NS, bool PLANES>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, AdapterUp u) {
   constexpr int kPitch = RC * 32 + 8;
   __shared__ __attribute__((aligned(16))) uint16_t v[2][16 * NS][kPitch];
   const AdapterPlan& p = c.plan;
-  const AdapterTile t = p.tiles[blockIdx.x];  // (past the last: whatever was there)
-  if ((int)blockIdx.x >= p.head[0]) return;
+  const int ti = blockIdx.x / u.slices, slice = blockIdx.x % u.slices;
+  const AdapterTile t = p.tiles[ti];  // (past the last: whatever was there)
+  if (ti >= p.head[0]) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
   const int n = t.end - t.begin;
   const bool bare = t.adapter >= p.count;
   const int live = bare ? 0 : live_ranks(c, t.adapter);
   if (live == 0 && u.base == u.out) return;
   const bool vec = (u.N & 7) == 0;
-  const int64_t n0 = (int64_t)blockIdx.y * u.slice, n1 = min(u.N, n0 + u.slice);
+  const int64_t steps = (u.N + 64 * kWaves - 1) / (64 * kWaves);
+  const int64_t n0 = steps * slice / u.slices * 64 * kWaves, n1 = min(u.N, steps * (slice + 1) / u.slices * 64 * kWaves);
   const uint16_t* W = u.W + (int64_t)(bare ? 0 : t.adapter) * u.N * c.r;
   // past the live ranks the weights may hold anything: masked out
   u32x4_t mask[RC];
@@ -375,11 +381,11 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, A
   int64_t row[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s) row[s] = (int64_t)p.order[t.begin + min(16 * s + i, n - 1)] * u.N;
-  // 64 outputs' weights and base (a lane: 16 outputs of each of its tokens)
+  // 64 outputs' weights and base
   const auto load = [&](int64_t nb, u32x4_t (&w)[4][RC], u32x4_t (&b)[NS][2]) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int64_t o = min(nb + 16 * (i >> 2) + 4 * q + (i & 3), u.N - 1);
+      const int64_t o = min(nb + 32 * (q >> 1) + 8 * (i >> 2) + 4 * (q & 1) + (i & 3), u.N - 1);
 #pragma unroll
       for (int k = 0; k < RC; ++k) {
         const int rank = 32 * k + 8 * g;
@@ -390,7 +396,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, A
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) b[s][h] = load16(u.base + row[s] + min(nb + 16 * g + 8 * h, u.N - 8));
+        for (int h = 0; h < 2; ++h) b[s][h] = load16(u.base + row[s] + min(nb + 32 * h + 8 * g, u.N - 8));
     }
   };
   const auto finish = [&](int64_t nb, u32x4_t (&w)[4][RC], const u32x4_t (&b)[NS][2]) __attribute__((always_inline)) {
@@ -398,7 +404,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, A
     for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int k = 0; k < RC; ++k) w[q][k] &= mask[k];
-    const int64_t o0 = nb + 16 * g;  // this lane's 16 outputs
+    const int64_t o0 = nb + 8 * g;  // this lane's outputs: 8 from here, 8 from 32 on
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       f32x4_t acc[4] = {zero4(), zero4(), zero4(), zero4()};
@@ -417,7 +423,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, A
       if (vec) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t o = o0 + 8 * h;
+          const int64_t o = o0 + 32 * h;
           const u32x4_t x = u.base ? b[s][h] : zero_u4();
           u32x4_t y;
 #pragma unroll
@@ -434,7 +440,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, A
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int64_t o = o0 + 4 * q + e;
+            const int64_t o = o0 + 32 * (q >> 1) + 4 * (q & 1) + e;
             if (o >= n1) continue;
             const uint16_t x = base ? base[o] : (uint16_t)0;
             out[o] = live > 0 ? f32_to_bf16(bf16_to_f32(x) + acc[q][e]) : x;
@@ -677,11 +683,14 @@ hipError_t launch_adapter_down(const AdapterCommon& c, const AdapterDown* jobs, 
   for (int q = 0; q < n_jobs; ++q) splits = std::max(splits, jobs[q].splits);
   with_rank_tiles(c.r, [&](auto rt, int groups) {
     constexpr int RT = decltype(rt)::value;
-    const dim3 grid((unsigned)c.plan.max_tiles, (unsigned)(splits * groups), (unsigned)n_jobs);
+    const int parts = splits * groups;
+    const dim3 grid((unsigned)c.plan.max_tiles * parts, (unsigned)n_jobs);
     if (c.plan.tile == kAdapterSmallTile)
-      hipLaunchKernelGGL((adapter_down_kernel<RT, 1>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], groups);
+      hipLaunchKernelGGL((adapter_down_kernel<RT, 1>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], parts,
+                         groups);
     else
-      hipLaunchKernelGGL((adapter_down_kernel<RT, 4>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], groups);
+      hipLaunchKernelGGL((adapter_down_kernel<RT, 4>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], parts,
+                         groups);
   });
   return hipGetLastError();
 }
@@ -693,7 +702,7 @@ hipError_t launch_adapter_finish(const AdapterCommon& c, const AdapterFinish& x,
 }
 
 hipError_t launch_adapter_up(const AdapterCommon& c, const AdapterUp& u, hipStream_t s) {
-  const dim3 grid((unsigned)c.plan.max_tiles, (unsigned)((u.N + u.slice - 1) / u.slice));
+  const dim3 grid((unsigned)c.plan.max_tiles * u.slices);
   with_rank_chunks(c.r, [&](auto rc) {
     constexpr int RC = decltype(rc)::value;
     const auto go = [&](auto ns) {

@@ -63,7 +63,7 @@ struct AdapterUp {
   const uint16_t* base;
   uint16_t* out;
   int64_t N;
-  int32_t splits, slice;
+  int32_t splits, slices;
 };
 
 // grad[a] = sum over a's tokens of cols[t][c] planes[t][j], stored [r][C]

@@ -61,17 +61,21 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
 // A contraction over K columns in pieces: enough workgroups for the CUs.  Of M
 // tokens the pieces come to at most min(kAdapterMaxSplits M, M + 64 kGroups)
 // rows of T.
-constexpr int64_t kGroups = 512;
+constexpr int64_t kGroups = 1024;
 int64_t t_rows(int64_t M) { return std::min<int64_t>(salr::kAdapterMaxSplits * M, M + 64 * kGroups); }
-void cut(salr::AdapterDown* d, int64_t tiles, int32_t r) {
-  const int64_t work = std::max<int64_t>(1, tiles * cdiv(r, 80));
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(salr::kAdapterMaxSplits, cdiv(kGroups, work)));
+void cut(salr::AdapterDown* d, const salr::AdapterPlan& p, int32_t r) {
+  const int64_t work = std::max<int64_t>(1, p.max_tiles * cdiv(r, 80));
+  const int64_t groups = p.tile == salr::kAdapterSmallTile ? kGroups / 2 : kGroups;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(salr::kAdapterMaxSplits, cdiv(groups, work)));
   d->cols = (int32_t)(cdiv(cdiv(d->K, want), 256) * 256);
   d->splits = (int32_t)cdiv(d->K, d->cols);
 }
-int32_t up_slice(int64_t N, int64_t tiles) {
-  const int64_t want = std::max<int64_t>(1, cdiv(2 * kGroups, std::max<int64_t>(1, tiles)));
-  return (int32_t)(cdiv(cdiv(N, want), 256) * 256);
+// Slices of N outputs: as many as 512 (small tiles) or 2048 workgroups take, in
+// eights where there are eight (one for each die, see adapter_down_kernel).
+int32_t up_slices(int64_t N, const salr::AdapterPlan& p) {
+  const int64_t groups = p.tile == salr::kAdapterSmallTile ? 512 : 2048;
+  const int64_t steps = cdiv(N, 256), want = cdiv(groups, std::max<int64_t>(1, p.max_tiles));
+  return (int32_t)std::min(steps, want < 8 ? want : cdiv(want, 8) * 8);
 }
 
 struct Workspace {
@@ -166,8 +170,8 @@ int salr_adapters_forward(const salr_adapters_t* A, const salr_adapters_plan_t* 
   hipStream_t s = static_cast<hipStream_t>(stream);
   const salr::AdapterCommon c{p, A->ranks, A->scales, A->r};
   salr::AdapterDown d{X, A->a, static_cast<float*>(ws), A->K, 0, 0};
-  cut(&d, p.max_tiles, A->r);
-  const salr::AdapterUp u{d.T, nullptr, A->b, base, Y, A->N, d.splits, up_slice(A->N, p.max_tiles)};
+  cut(&d, p, A->r);
+  const salr::AdapterUp u{d.T, nullptr, A->b, base, Y, A->N, d.splits, up_slices(A->N, p)};
   if (const int e = status(salr::launch_adapter_down(c, &d, 1, s))) return e;
   return status(salr::launch_adapter_up(c, u, s));
 }
@@ -201,13 +205,13 @@ int salr_adapters_backward(const salr_adapters_t* A, const salr_adapters_plan_t*
     uint16_t *a_t = halves(w.a), *b_t = halves(w.b);
     if (const int e = status(salr::launch_adapter_transpose(c, A->a, a_t, A->K, A->b, b_t, A->N, s))) return e;
     salr::AdapterDown d[2] = {{X, A->a, floats(w.t), A->K, 0, 0}, {dY, b_t, floats(w.t + w.t_bytes), A->N, 0, 0}};
-    for (salr::AdapterDown& q : d) cut(&q, p.max_tiles, A->r);
+    for (salr::AdapterDown& q : d) cut(&q, p, A->r);
     if (const int e = status(salr::launch_adapter_down(c, d, 2, s))) return e;
     if (const int e = status(salr::launch_adapter_finish(c, {d[0].T, t_planes, d[0].splits},
                                                          {d[1].T, g_planes, d[1].splits}, s)))
       return e;
     if (dX) {
-      const salr::AdapterUp u{nullptr, g_planes, a_t, base, dX, A->K, 0, up_slice(A->K, p.max_tiles)};
+      const salr::AdapterUp u{nullptr, g_planes, a_t, base, dX, A->K, 0, up_slices(A->K, p)};
       if (const int e = status(salr::launch_adapter_up(c, u, s))) return e;
     }
   }
