@@ -86,9 +86,11 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
         const bool live = b + 64 * q + lane < t1;
         const int x = (uint32_t)g[q] < (uint32_t)p.count ? g[q] : p.count;
         uint64_t same = __ballot(live);
-        for (int k = 0; k < bits; ++k) {
-          const uint64_t set = __ballot((x >> k) & 1);
-          same &= (x >> k) & 1 ? set : ~set;
+        if (__ballot(live && x == __builtin_amdgcn_readfirstlane(x)) != same) {  // (a prompt's tokens are alike)
+          for (int k = 0; k < bits; ++k) {
+            const uint64_t set = __ballot((x >> k) & 1);
+            same &= (x >> k) & 1 ? set : ~set;
+          }
         }
         f(b + 64 * q + lane, x, live, same);
       }
@@ -280,7 +282,7 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterCommon c,
           for (int s = 0; s < NS; ++s) acc[a][s] = mfma_16x16x32(ws[h][a], xs[h][s], acc[a][s]);
       }
     };
-    if constexpr (NS == 1) {
+    if constexpr (NS == 1 || RL == 1) {
       // (few registers a step: the next step's loads ahead)
       u32x4_t x[2][2][NS], w[2][2][RL];
       int64_t k = k0 + 64 * wave;
@@ -300,7 +302,9 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterCommon c,
       }
     }
   };
+  constexpr int kHalf = (RT + 1) / 2;
   if (RT > 1 && live - rank0 <= 16) body(std::integral_constant<int, 1>{});
+  else if (kHalf > 1 && live - rank0 <= 16 * kHalf) body(std::integral_constant<int, kHalf>{});
   else body(std::integral_constant<int, RT>{});
   float* out = j.T + (int64_t)split * p.M * c.r;
 #pragma unroll
@@ -321,7 +325,9 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterCommon c,
   }
 }
 
-// ---- finish: the pieces' sums as bf16 planes (for the gradients) ----
+// ---- finish: the pieces' sums as bf16 planes, for large tiles and gradients,
+// whose many workgroups would each sum the pieces (8191 tokens, 4096 x 11008,
+// ranks 8 to 64: up 109 us with that, 100 and 5 without) ----
 __global__ __launch_bounds__(kThreads) void adapter_finish_kernel(AdapterCommon c, AdapterFinish x, AdapterFinish y) {
   const AdapterPlan& p = c.plan;
   const AdapterTile t = p.tiles[blockIdx.x];  // (past the last: whatever was there)
@@ -536,7 +542,6 @@ __global__ __launch_bounds__(kThreads) void adapter_transpose_kernel(AdapterComm
 // 32 tokens at a time go to LDS as they are and come back transposed (4 x 16
 // values a 16 lanes).  T and G are three bf16 planes each: the float sums see
 // all their bits.
-constexpr int kGradCols = 128;
 
 __device__ __forceinline__ u32x4_t read_transposed(const uint16_t* tile, int pitch, int lane) {
   // lane (i, g) gets column i of rows 4g..4g+3 and 16+4g..16+4g+3
@@ -549,10 +554,14 @@ __device__ __forceinline__ u32x4_t read_transposed(const uint16_t* tile, int pit
   return u32x4_t{a.x, a.y, b.x, b.y};
 }
 
+constexpr int kGradCols = 128;
+
 template <int RT>
 __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c, AdapterGrad ga, AdapterGrad gb,
                                                                 int blocks_a, int groups) {
-  constexpr int kColPitch = kGradCols + 8, kRankPitch = RT * 16 + 8;
+  // (a wave: CT x 16 columns; 256 columns a workgroup, which read T and G half
+  // as often, are slower: 36 to 41 us at 8192 tokens, rank 16, 4096 x 4096)
+  constexpr int kCols = kGradCols, CT = kCols / (16 * kWaves), kColPitch = kCols + 8, kRankPitch = RT * 16 + 8;
   __shared__ __attribute__((aligned(16))) uint16_t cols[32 * kColPitch];
   __shared__ __attribute__((aligned(16))) uint16_t rank[3][32 * kRankPitch];
   const AdapterPlan& p = c.plan;
@@ -561,32 +570,36 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
   const int by = blockIdx.x / groups, rank0 = (blockIdx.x % groups) * RT * 16;
   const bool is_a = by < blocks_a;
   const AdapterGrad j = is_a ? ga : gb;
-  const int64_t c0 = (int64_t)(is_a ? by : by - blocks_a) * kGradCols;
+  const int64_t c0 = (int64_t)(is_a ? by : by - blocks_a) * kCols;
+  const int live = live_ranks(c, t.adapter);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
   const int64_t plane = p.M * c.r;
-  f32x4_t acc[RT][2];
+  f32x4_t acc[RT][CT];
 #pragma unroll
-  for (int a = 0; a < RT; ++a) acc[a][0] = acc[a][1] = zero4();
-  // staging: 16 bytes of 16 rows' columns a pass, two passes; 8 ranks of a plane's row
-  const int row = tid >> 4, col = 8 * (tid & 15);
+  for (int a = 0; a < RT; ++a)
+#pragma unroll
+    for (int h = 0; h < CT; ++h) acc[a][h] = zero4();
+  // staging: 16 bytes of CT rows' columns, and 8 ranks of a plane's row a pass
+  constexpr int kRowThreads = kCols / 8, kRows = kThreads / kRowThreads, kPasses = 32 / kRows;
+  const int row = tid / kRowThreads, col = 8 * (tid % kRowThreads);
   const bool col_in = c0 + col < j.C;
   constexpr int kRankPieces = 3 * 32 * RT * 2, kRankPasses = (kRankPieces + kThreads - 1) / kThreads;
-  u32x4_t vc[2], vr[kRankPasses];
-  int tok[2];  // the tokens of the next stage
+  u32x4_t vc[kPasses], vr[kRankPasses];
+  int tok[kPasses];  // the tokens of the next stage
   const auto next_tokens = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) tok[h] = p.order[min(b + row + 16 * h, t.end - 1)];
+    for (int h = 0; h < kPasses; ++h) tok[h] = p.order[min(b + row + kRows * h, t.end - 1)];
   };
   const auto load = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      vc[h] = b + row + 16 * h < t.end && col_in ? load16(j.cols + (int64_t)tok[h] * j.C + c0 + col) : zero_u4();
+    for (int h = 0; h < kPasses; ++h)
+      vc[h] = b + row + kRows * h < t.end && col_in ? load16(j.cols + (int64_t)tok[h] * j.C + c0 + col) : zero_u4();
     if (b + 32 < t.end) next_tokens(b + 32);
 #pragma unroll
     for (int q = 0; q < kRankPasses; ++q) {
       const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = rank0 + x % (RT * 2) * 8;
-      vr[q] = x < kRankPieces && b + y < t.end && z < c.r ? load16(j.planes + l * plane + (int64_t)(b + y) * c.r + z)
-                                                         : zero_u4();
+      vr[q] = x < kRankPieces && b + y < t.end && z < live ? load16(j.planes + l * plane + (int64_t)(b + y) * c.r + z)
+                                                          : zero_u4();
     }
   };
   next_tokens(t.begin);
@@ -594,7 +607,7 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
   for (int b = t.begin; b < t.end; b += 32) {
     lds_barrier();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4_t*>(&cols[(row + 16 * h) * kColPitch + col]) = vc[h];
+    for (int h = 0; h < kPasses; ++h) *reinterpret_cast<u32x4_t*>(&cols[(row + kRows * h) * kColPitch + col]) = vc[h];
 #pragma unroll
     for (int q = 0; q < kRankPasses; ++q) {
       const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = x % (RT * 2) * 8;
@@ -602,26 +615,28 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
     }
     lds_barrier();
     if (b + 32 < t.end) load(b + 32);
-    u32x4_t x[2];
+    u32x4_t x[CT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) x[h] = read_transposed(cols + 32 * wave + 16 * h, kColPitch, lane);
+    for (int h = 0; h < CT; ++h) x[h] = read_transposed(cols + 16 * (CT * wave + h), kColPitch, lane);
 #pragma unroll
-    for (int a = 0; a < RT; ++a)
+    for (int a = 0; a < RT; ++a) {
+      if (rank0 + 16 * a >= live) break;  // (zeros from here on)
 #pragma unroll
       for (int l = 0; l < 3; ++l) {
         const u32x4_t y = read_transposed(rank[l] + 16 * a, kRankPitch, lane);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < CT; ++h)
           acc[a][h] = is_a ? mfma_16x16x32(x[h], y, acc[a][h]) : mfma_16x16x32(y, x[h], acc[a][h]);
       }
+    }
   }
   // dA: the lane holds four columns of rank i; dB: four ranks of column i
   float* out = t.part < 0 ? j.out + (int64_t)t.adapter * c.r * j.C : j.parts + (int64_t)t.part * c.r * j.C;
 #pragma unroll
   for (int a = 0; a < RT; ++a)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t cc = c0 + 32 * wave + 16 * h + (is_a ? 4 * g : i);
+    for (int h = 0; h < CT; ++h) {
+      const int64_t cc = c0 + 16 * (CT * wave + h) + (is_a ? 4 * g : i);
       const int rr = rank0 + 16 * a + (is_a ? i : 4 * g);
       if (cc < j.C && rr < c.r)
         *reinterpret_cast<f32x4_t*>(is_a ? out + (int64_t)rr * j.C + cc : out + cc * c.r + rr) = acc[a][h];
@@ -695,9 +710,9 @@ hipError_t launch_adapter_down(const AdapterCommon& c, const AdapterDown* jobs, 
   return hipGetLastError();
 }
 
-hipError_t launch_adapter_finish(const AdapterCommon& c, const AdapterFinish& x, const AdapterFinish& y,
-                                 hipStream_t s) {
-  hipLaunchKernelGGL(adapter_finish_kernel, dim3((unsigned)c.plan.max_tiles, 2), dim3(kThreads), 0, s, c, x, y);
+hipError_t launch_adapter_finish(const AdapterCommon& c, const AdapterFinish* jobs, int n_jobs, hipStream_t s) {
+  hipLaunchKernelGGL(adapter_finish_kernel, dim3((unsigned)c.plan.max_tiles, (unsigned)n_jobs), dim3(kThreads), 0, s, c,
+                     jobs[0], jobs[n_jobs - 1]);
   return hipGetLastError();
 }
 

@@ -85,7 +85,7 @@ struct AdapterCommon {
 
 hipError_t launch_adapter_plan(const int32_t* ids, const AdapterPlan& p, hipStream_t s);
 hipError_t launch_adapter_down(const AdapterCommon& c, const AdapterDown* jobs, int n_jobs, hipStream_t s);
-hipError_t launch_adapter_finish(const AdapterCommon& c, const AdapterFinish& x, const AdapterFinish& y, hipStream_t s);
+hipError_t launch_adapter_finish(const AdapterCommon& c, const AdapterFinish* jobs, int n_jobs, hipStream_t s);
 hipError_t launch_adapter_up(const AdapterCommon& c, const AdapterUp& u, hipStream_t s);
 hipError_t launch_adapter_transpose(const AdapterCommon& c, const uint16_t* a, uint16_t* at, int64_t K,
                                     const uint16_t* b, uint16_t* bt, int64_t N, hipStream_t s);

@@ -93,9 +93,9 @@ Workspace lay_out(int64_t count, int64_t N, int64_t K, int32_t r, int64_t M, boo
   w.t_bytes = align_up((size_t)t_rows(M) * r * 4, 256);
   w.planes_bytes = align_up((size_t)M * r * 6, 256);
   w.t = take(w.t_bytes * (backward ? 2 : 1));
+  w.planes = take(w.planes_bytes * (backward ? 2 : 1));
   if (backward) {
     const int64_t parts = std::min<int64_t>(64, 2 * M / salr::kAdapterMinChunk);
-    w.planes = take(w.planes_bytes * 2);
     w.a = take((size_t)count * r * K * 2);
     w.b = take((size_t)count * r * N * 2);
     w.parts_a = take((size_t)parts * r * K * 4);
@@ -169,10 +169,17 @@ int salr_adapters_forward(const salr_adapters_t* A, const salr_adapters_plan_t* 
   if (!ws || !aligned16(ws) || ws_bytes < w.total) return SALR_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const salr::AdapterCommon c{p, A->ranks, A->scales, A->r};
-  salr::AdapterDown d{X, A->a, static_cast<float*>(ws), A->K, 0, 0};
+  char* at = static_cast<char*>(ws);
+  salr::AdapterDown d{X, A->a, reinterpret_cast<float*>(at + w.t), A->K, 0, 0};
   cut(&d, p, A->r);
-  const salr::AdapterUp u{d.T, nullptr, A->b, base, Y, A->N, d.splits, up_slices(A->N, p)};
   if (const int e = status(salr::launch_adapter_down(c, &d, 1, s))) return e;
+  uint16_t* planes = nullptr;
+  if (p.tile == salr::kAdapterLargeTile) {
+    planes = reinterpret_cast<uint16_t*>(at + w.planes);
+    const salr::AdapterFinish f{d.T, planes, d.splits};
+    if (const int e = status(salr::launch_adapter_finish(c, &f, 1, s))) return e;
+  }
+  const salr::AdapterUp u{d.T, planes, A->b, base, Y, A->N, d.splits, up_slices(A->N, p)};
   return status(salr::launch_adapter_up(c, u, s));
 }
 
@@ -207,9 +214,8 @@ int salr_adapters_backward(const salr_adapters_t* A, const salr_adapters_plan_t*
     salr::AdapterDown d[2] = {{X, A->a, floats(w.t), A->K, 0, 0}, {dY, b_t, floats(w.t + w.t_bytes), A->N, 0, 0}};
     for (salr::AdapterDown& q : d) cut(&q, p, A->r);
     if (const int e = status(salr::launch_adapter_down(c, d, 2, s))) return e;
-    if (const int e = status(salr::launch_adapter_finish(c, {d[0].T, t_planes, d[0].splits},
-                                                         {d[1].T, g_planes, d[1].splits}, s)))
-      return e;
+    const salr::AdapterFinish f[2] = {{d[0].T, t_planes, d[0].splits}, {d[1].T, g_planes, d[1].splits}};
+    if (const int e = status(salr::launch_adapter_finish(c, f, 2, s))) return e;
     if (dX) {
       const salr::AdapterUp u{nullptr, g_planes, a_t, base, dX, A->K, 0, up_slices(A->K, p)};
       if (const int e = status(salr::launch_adapter_up(c, u, s))) return e;
