@@ -833,8 +833,8 @@ typedef struct salr_muon_tensor {
   const void* g;    /* gradients (g_type)                                   */
   float* m;         /* momentum; zeros at the start                         */
   float* master;    /* float copy of a bf16 parameter, or NULL in all       */
-  int64_t rows;     /* 0 .. 2^30 each, the shorter at most                  */
-  int64_t cols;     /*   SALR_MUON_MAX_SIDE                                 */
+  int64_t rows;     /* the shorter at most SALR_MUON_MAX_SIDE,              */
+  int64_t cols;     /*   rows * cols < 2^29; 0 allowed                      */
   double lr_scale;  /* this matrix's share of lr                            */
 } salr_muon_tensor_t;
 
@@ -858,8 +858,8 @@ typedef struct salr_muon_step_args {
 
 /* Bytes of the plan's device buffer for `count` matrices (`rows`, `cols` and
  * `out` host; count <= 2^20).  Errors: INVALID_ARG, UNSUPPORTED (a shorter
- * side above SALR_MUON_MAX_SIDE; more than 2^40 elements in all, or more
- * matrices and pieces of them than one launch takes). */
+ * side above SALR_MUON_MAX_SIDE, a matrix of 2^29 elements or more; more than
+ * 2^40 elements in all, or more pieces of matrices than one launch takes). */
 int salr_muon_plan_bytes(const int64_t* rows, const int64_t* cols,
                          int32_t count, size_t* out);
 

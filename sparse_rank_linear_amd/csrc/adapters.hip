@@ -684,8 +684,9 @@ void with_rank_chunks(int r, F f) {
 }  // namespace
 
 hipError_t launch_adapter_plan(const int32_t* ids, const AdapterPlan& p, hipStream_t s) {
-  // (each wave's counters: 4 waves keep 4096 adapters within 132 KB of LDS)
-  const int waves = p.count <= 1024 ? kPlanWaves : 4;
+  // (each wave's counters: 4 waves keep 4096 adapters within 132 KB of LDS; no
+  // more waves than have 128 tokens each, as their counters are added up)
+  const int waves = (int)std::max<int64_t>(1, std::min<int64_t>((p.M + 127) / 128, p.count <= 1024 ? kPlanWaves : 4));
   const size_t lds = ((size_t)waves * (p.count + 1) + 4 * (size_t)(p.count + 2)) * 4;
   int bits = 0;
   while ((1 << bits) <= p.count) ++bits;

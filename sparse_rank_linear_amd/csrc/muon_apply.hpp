@@ -23,7 +23,7 @@ struct ApplyShape {
 };
 
 template <int NT, bool GF, bool PF, bool MASTER, bool WIDE>
-__device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, int piece, float* lds) {
+__device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, int64_t k0, int64_t k1, float* lds) {
   using Shape = ApplyShape<NT>;
   constexpr int KB = Shape::KB, S = Shape::S, P = WIDE ? Shape::PW : Shape::PT, R = WIDE ? Shape::RW : Shape::RT;
   constexpr int kThreads = Shape::kWaves * 64, kNq = (S * KB / 4 + kThreads - 1) / kThreads;
@@ -32,7 +32,6 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4, tile = wave % NT;
   const Stage<WIDE, KB, kThreads, kNq> st(M.s, M.L, tid);
-  const int64_t k0 = (int64_t)piece * M.chunk, k1 = min(M.L, k0 + M.chunk);
   const float gs = a.dyn ? a.dyn[1] : a.grad_scale, lr = a.dyn ? a.dyn[0] : a.lr;
   const float decay = 1.f - lr * a.weight_decay, rate = lr * M.lr_scale;
   const auto grad = to_global<const typename Four<GF>::elem>(M.g);
@@ -59,12 +58,13 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
   for (int kk = 0; kk < S / 4; ++kk)
     qa[kk] = qm[(16 * tile + i) * S + (WIDE ? 4 * kk + g : 16 * (kk / 4) + 4 * g + kk % 4)];
   for (int q = tid; q < Shape::kU; q += kThreads) lds[q] = 0.f;
-  int place[kNq], place_r[kNq];
+  // (tall: both pitches are one, and the places take a division; wide: a shift)
+  static_assert(WIDE || P == R, "one place");
+  int tall_place[kNq];
 #pragma unroll
-  for (int q = 0; q < kNq; ++q) {
-    place[q] = st.template place<P>(q);
-    place_r[q] = st.template place<R>(q);
-  }
+  for (int q = 0; q < kNq; ++q) tall_place[q] = WIDE ? 0 : st.template place<P>(q);
+  const auto place = [&](int q) { return WIDE ? st.template place<P>(q) : tall_place[q]; };
+  const auto place_r = [&](int q) { return WIDE ? st.template place<R>(q) : tall_place[q]; };
   wait_memory();
   lds_barrier();
   const auto stage = [&](int64_t k, auto full) __attribute__((always_inline)) {
@@ -74,7 +74,7 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
     for (int q = 0; q < kNq; ++q) {
       if (kEarly) vp[q] = next_p[q];
       if (st.has(q))
-        st.template put<P>(lds, place[q], a.nesterov ? Four<GF>::value(vg[q]) * gs + a.momentum * vm[q] : vm[q]);
+        st.template put<P>(lds, place(q), a.nesterov ? Four<GF>::value(vg[q]) * gs + a.momentum * vm[q] : vm[q]);
     }
     lds_barrier();
     if (!kEarly) st.template load<FULL, kSrc>(src, k, left, vp);
@@ -99,7 +99,7 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
     lds_barrier();
 #pragma unroll
     for (int q = 0; q < kNq; ++q) {
-      const f32x4_t p = Four<kSrc>::value(vp[q]) * decay - rate * st.template get<R>(res, place_r[q]);
+      const f32x4_t p = Four<kSrc>::value(vp[q]) * decay - rate * st.template get<R>(res, place_r(q));
       if (MASTER) st.template store<FULL, true>(to_global<float>(M.master), q, k, left, p);
       st.template store<FULL, PF>(param, q, k, left, p);
     }
@@ -113,12 +113,18 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
 }
 
 template <int NT, bool GF, bool PF, bool MASTER>
-__global__ __launch_bounds__(ApplyShape<NT>::kWaves * 64, NT == 3 || NT > 5 ? 4 : 5) void muon_apply_kernel(MuonArgs a, int64_t c0) {
+__global__ __launch_bounds__(ApplyShape<NT>::kWaves * 64, NT == 3 || NT > 5 ? 4 : 5) void muon_apply_kernel(MuonArgs a, int64_t c0, int sub) {
   extern __shared__ __attribute__((aligned(16))) float lds[];  // u, then Q u
-  const MuonChunk ch = a.chunks[c0 + blockIdx.x];
+  const MuonChunk ch = a.chunks[c0 + blockIdx.x / sub];
   const MuonMatrix& M = a.matrices[ch.matrix];
-  if (M.wide) apply<NT, GF, PF, MASTER, true>(a, M, ch.part, lds);
-  else apply<NT, GF, PF, MASTER, false>(a, M, ch.part, lds);
+  // (one of the chunk's `sub` parts, whole stages each)
+  constexpr int KB = ApplyShape<NT>::KB;
+  const int part = blockIdx.x % sub, each = (M.chunk / KB + sub - 1) / sub * KB;
+  const int64_t k0 = (int64_t)ch.part * M.chunk + part * each;
+  const int64_t k1 = min(min(M.L, (int64_t)(ch.part + 1) * M.chunk), k0 + each);
+  if (k0 >= k1) return;
+  if (M.wide) apply<NT, GF, PF, MASTER, true>(a, M, k0, k1, lds);
+  else apply<NT, GF, PF, MASTER, false>(a, M, k0, k1, lds);
 }
 
 template <bool PF, bool MASTER>
@@ -127,11 +133,14 @@ hipError_t launch_apply(const MuonArgs& a, int cls, int64_t c0, int64_t chunks, 
     constexpr int NT = decltype(nt)::value;
     using Shape = ApplyShape<NT>;
     constexpr size_t kLds = (size_t)(Shape::kU + Shape::kR) * 4;
-    const dim3 grid((unsigned)chunks), threads(Shape::kWaves * 64);
+    // (few chunks: their parts on workgroups of their own; 80 x 4096 and its
+    // transpose: 13.7 us in 64 workgroups, 11 in 128)
+    const int sub = chunks < 256 ? 2 : 1;
+    const dim3 grid((unsigned)(chunks * sub)), threads(Shape::kWaves * 64);
     if (a.g_f32)
-      hipLaunchKernelGGL((muon_apply_kernel<NT, true, PF, MASTER>), grid, threads, kLds, s, a, c0);
+      hipLaunchKernelGGL((muon_apply_kernel<NT, true, PF, MASTER>), grid, threads, kLds, s, a, c0, sub);
     else
-      hipLaunchKernelGGL((muon_apply_kernel<NT, false, PF, MASTER>), grid, threads, kLds, s, a, c0);
+      hipLaunchKernelGGL((muon_apply_kernel<NT, false, PF, MASTER>), grid, threads, kLds, s, a, c0, sub);
     return hipGetLastError();
   });
 }

@@ -97,18 +97,23 @@ template <bool WIDE, int KB, int THREADS, int NQ>
 struct Stage {
   int s, tid;
   int64_t L;
-  int64_t base[NQ];  // the group's first element, but for k
+  uint32_t base[NQ];  // the group's first element, from the stage's on (a matrix has less than 2^29)
   __device__ __forceinline__ Stage(int s_, int64_t L_, int tid_) : s(s_), tid(tid_), L(L_) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       // (a thread without a group loads the last one's too)
       const int x = min(group(q), s * (KB / 4) - 1);
-      base[q] = WIDE ? (int64_t)(x / (KB / 4)) * L + x % (KB / 4) * 4 : (int64_t)4 * x;
+      base[q] = WIDE ? (uint32_t)(x / (KB / 4)) * (uint32_t)L + x % (KB / 4) * 4 : (uint32_t)(4 * x);
     }
   }
   __device__ __forceinline__ int group(int q) const { return tid + q * THREADS; }
   __device__ __forceinline__ bool has(int q) const { return group(q) < s * (KB / 4); }
-  __device__ __forceinline__ int64_t element(int q, int64_t k) const { return base[q] + (WIDE ? k : k * s); }
+  // (one address for all lanes, and a lane's 32 bits from there)
+  template <class T>
+  __device__ __forceinline__ global<T> element(global<T> p, int q, int64_t k) const {
+    typedef std::conditional_t<std::is_const<T>::value, const char, char> byte;
+    return (global<T>)((global<byte>)(p + (WIDE ? k : k * s)) + (uint32_t)(base[q] * (uint32_t)sizeof(T)));
+  }
   // elements of group q (0 without one)
   __device__ __forceinline__ int count(int q, int left) const {
     const int x = group(q);
@@ -122,22 +127,22 @@ struct Stage {
                                        typename Four<F32>::raw (&v)[NQ]) const {
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
-      v[q] = FULL ? load4<F32>(p + element(q, k)) : Four<F32>::part(p + element(q, k), count(q, left));
+      v[q] = FULL ? load4<F32>(element(p, q, k)) : Four<F32>::part(element(p, q, k), count(q, left));
   }
   template <bool FULL, bool F32>
   __device__ __forceinline__ void store(global<typename Four<F32>::elem> p, int q, int64_t k, int left, f32x4_t x) const {
     if (FULL) {
-      if (has(q)) *(global<typename Four<F32>::any>)(p + element(q, k)) = Four<F32>::pack(x);
+      if (has(q)) *(global<typename Four<F32>::any>)element(p, q, k) = Four<F32>::pack(x);
     } else {
       const int n = count(q, left);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (e < n) p[element(q, k) + e] = Four<F32>::one(x[e]);
+        if (e < n) element(p, q, k)[e] = Four<F32>::one(x[e]);
     }
   }
   template <int PITCH>
   __device__ __forceinline__ int place(int q) const {
-    const int x = min(group(q), s * (KB / 4) - 1);
+    const int x = WIDE ? group(q) : min(group(q), s * (KB / 4) - 1);
     return WIDE ? x / (KB / 4) * PITCH + x % (KB / 4) * 4 : 4 * x / s * PITCH + 4 * x % s;
   }
   template <int PITCH>

@@ -48,7 +48,7 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
   for (int q = tid; q < Shape::kFloats; q += kThreads) lds[q] = 0.f;  // (past the short side it stays so)
   const int group = wave % Shape::kGroups, part = wave / Shape::kGroups;
   f64x4_t sum[Shape::kPer];
-  int row_i[Shape::kPer], row_j[Shape::kPer], place[kNq];
+  int row_i[Shape::kPer], row_j[Shape::kPer], tall_place[kNq];
 #pragma unroll
   for (int t = 0; t < Shape::kPer; ++t) {
     sum[t] = f64x4_t{0, 0, 0, 0};
@@ -58,7 +58,8 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
     row_j[t] = WIDE ? (16 * tj + i) * P + 4 * g : g * P + 16 * tj + i;
   }
 #pragma unroll
-  for (int q = 0; q < kNq; ++q) place[q] = st.template place<P>(q);
+  for (int q = 0; q < kNq; ++q) tall_place[q] = WIDE ? 0 : st.template place<P>(q);
+  const auto place = [&](int q) { return WIDE ? st.template place<P>(q) : tall_place[q]; };
   const auto stage = [&](int64_t k, auto full) __attribute__((always_inline)) {
     constexpr bool FULL = decltype(full)::value;
     const int left = (int)(k1 - k);
@@ -67,7 +68,7 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
     for (int q = 0; q < kNq; ++q) {
       const f32x4_t gg = Four<GF>::value(vg[q]) * gs, mm = a.momentum * vm[q] + gg;
       st.template store<FULL, true>(mom, q, k, left, mm);
-      if (st.has(q)) st.template put<P>(lds, place[q], a.nesterov ? gg + a.momentum * mm : mm);
+      if (st.has(q)) st.template put<P>(lds, place(q), a.nesterov ? gg + a.momentum * mm : mm);
     }
     lds_barrier();
     if (FULL && k + 2 * KB <= k1) load(k + KB, full);

@@ -18,14 +18,10 @@ using namespace salr;
 
 constexpr int32_t kMaxMatrices = 1 << 20;
 constexpr int64_t kMaxSide = int64_t(1) << 30;
+constexpr int64_t kMaxMatrix = int64_t(1) << 29;   // elements of one: the kernels' byte offsets have 32 bits
 constexpr int64_t kMaxElements = int64_t(1) << 40;
 constexpr int64_t kMaxChunks = (int64_t(1) << 24) - 1;
 static_assert(SALR_MUON_CLASSES == kMuonClasses, "a plan counts every class");
-
-// Elements of a chunk, by those of all matrices: enough workgroups for the
-// CUs, then fewer and longer ones (each writes one s x s sum, so it has s
-// columns at least).
-int64_t chunk_elements(int64_t total) { return std::min<int64_t>(131072, std::max<int64_t>(8192, total / 1024)); }
 
 int class_of(int64_t s) {
   int c = 0;
@@ -39,38 +35,59 @@ struct Shape {
   int32_t chunk, chunks;
 };
 
+// Elements of a chunk of each class.
+struct Cut {
+  int64_t per[kMuonClasses];
+};
+
 // The shape of one matrix; chunks 0 for an empty one.
-Shape shape_of(int64_t rows, int64_t cols, int64_t per) {
+Shape shape_of(int64_t rows, int64_t cols, const Cut& cut) {
   Shape q{};
   q.s = std::min(rows, cols);
   q.L = std::max(rows, cols);
   if (q.s == 0) return q;
   q.cls = class_of(q.s);
   const int64_t kb = muon_stage(kMuonTiles[q.cls]);
-  const int64_t chunk = std::min(cdiv(q.L, kb), cdiv(std::max(q.s, cdiv(per, q.s)), kb)) * kb;
+  // (each chunk writes one s x s sum, so it has s columns at least)
+  const int64_t chunk = std::min(cdiv(q.L, kb), cdiv(std::max(q.s, cdiv(cut.per[q.cls], q.s)), kb)) * kb;
   q.chunk = (int32_t)chunk;
   q.chunks = (int32_t)cdiv(q.L, chunk);
   return q;
 }
 
-// Sizes that a plan takes: INVALID_ARG, UNSUPPORTED (a short side over the
-// limit, too many pieces) or 0.
+// How the matrices are cut, and the chunks that makes in all.  Enough
+// workgroups for the CUs, then fewer and longer ones; from ten tiles on a CU
+// holds one workgroup at a time, and a few more than there are CUs would take
+// twice as long (253 x 67584 columns in 267 chunks 139 us, in 237 ones 85).
+// INVALID_ARG, UNSUPPORTED (a short side over the limit, too many chunks) or 0.
+constexpr int64_t kCus = 256;
 template <class R, class C>
-int survey(int32_t count, R rows, C cols, int64_t* per, int64_t* chunks) {
+int survey(int32_t count, R rows, C cols, Cut* cut, int64_t* chunks) {
   int64_t total = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (rows(i) < 0 || cols(i) < 0 || rows(i) > kMaxSide || cols(i) > kMaxSide) return SALR_ERR_INVALID_ARG;
-    if (std::min(rows(i), cols(i)) > SALR_MUON_MAX_SIDE) return SALR_ERR_UNSUPPORTED;
+    if (std::min(rows(i), cols(i)) > SALR_MUON_MAX_SIDE || rows(i) * cols(i) >= kMaxMatrix) return SALR_ERR_UNSUPPORTED;
     total += rows(i) * cols(i);
     if (total > kMaxElements) return SALR_ERR_UNSUPPORTED;
   }
-  *per = chunk_elements(total);
+  for (int64_t& per : cut->per) per = std::min<int64_t>(131072, std::max<int64_t>(8192, total / 1024));
+  const auto chunks_of = [&](int64_t (&n)[kMuonClasses]) {
+    for (int64_t& v : n) v = 0;
+    for (int32_t i = 0; i < count; ++i) {
+      const Shape q = shape_of(rows(i), cols(i), *cut);
+      n[q.cls] += q.chunks;
+    }
+  };
+  int64_t n[kMuonClasses];
+  chunks_of(n);
+  for (int cls = 0; cls < kMuonClasses; ++cls)
+    for (int k = 0; k < 16 && kMuonTiles[cls] >= 10 && n[cls] > kCus && n[cls] < 2 * kCus; ++k) {
+      cut->per[cls] = std::max(cut->per[cls], (int64_t)256 * 16 * kMuonTiles[cls]) * 17 / 16;
+      chunks_of(n);
+    }
   *chunks = 0;
-  for (int32_t i = 0; i < count; ++i) {
-    *chunks += shape_of(rows(i), cols(i), *per).chunks;
-    if (*chunks > kMaxChunks) return SALR_ERR_UNSUPPORTED;
-  }
-  return SALR_OK;
+  for (int64_t v : n) *chunks += v;
+  return *chunks > kMaxChunks ? SALR_ERR_UNSUPPORTED : SALR_OK;
 }
 
 size_t records_bytes(int64_t count) { return align_up((size_t)count * sizeof(MuonMatrix), 256); }
@@ -89,10 +106,10 @@ Own own_bytes(const Shape& q) {
 }
 
 template <class R, class C>
-size_t table_bytes_for(int32_t count, R rows, C cols, int64_t per, int64_t chunks) {
+size_t table_bytes_for(int32_t count, R rows, C cols, const Cut& cut, int64_t chunks) {
   size_t bytes = records_bytes(count) + list_bytes(chunks);
   for (int32_t i = 0; i < count; ++i) {
-    const Own o = own_bytes(shape_of(rows(i), cols(i), per));
+    const Own o = own_bytes(shape_of(rows(i), cols(i), cut));
     bytes += o.parts + o.q + o.work;
   }
   return std::max<size_t>(bytes, 256);
@@ -106,9 +123,10 @@ int salr_muon_plan_bytes(const int64_t* rows, const int64_t* cols, int32_t count
   if (!out || count < 0 || count > kMaxMatrices || (count > 0 && (!rows || !cols))) return SALR_ERR_INVALID_ARG;
   const auto r = [&](int32_t i) { return rows[i]; };
   const auto c = [&](int32_t i) { return cols[i]; };
-  int64_t per = 0, chunks = 0;
-  if (const int e = survey(count, r, c, &per, &chunks)) return e;
-  *out = table_bytes_for(count, r, c, per, chunks);
+  Cut cut;
+  int64_t chunks = 0;
+  if (const int e = survey(count, r, c, &cut, &chunks)) return e;
+  *out = table_bytes_for(count, r, c, cut, chunks);
   return SALR_OK;
 }
 
@@ -118,13 +136,14 @@ int salr_muon_plan(const salr_muon_tensor_t* tensors, int32_t count, int32_t p_t
   if (!type_ok(p_type) || !type_ok(g_type)) return SALR_ERR_INVALID_ARG;
   const auto rows = [&](int32_t i) { return tensors[i].rows; };
   const auto cols = [&](int32_t i) { return tensors[i].cols; };
-  int64_t per = 0, chunks = 0;
-  if (const int e = survey(count, rows, cols, &per, &chunks)) return e;
+  Cut cut;
+  int64_t chunks = 0;
+  if (const int e = survey(count, rows, cols, &cut, &chunks)) return e;
   const auto live = [&](int32_t i) { return tensors[i].rows > 0 && tensors[i].cols > 0; };
   bool master = false;
   for (int32_t i = 0; i < count && !master; ++i) master = live(i) && tensors[i].master != nullptr;
   if (master && p_type != SALR_TYPE_BF16) return SALR_ERR_INVALID_ARG;
-  const size_t bytes = table_bytes_for(count, rows, cols, per, chunks);
+  const size_t bytes = table_bytes_for(count, rows, cols, cut, chunks);
   const size_t head = records_bytes(count) + list_bytes(chunks);
   unsigned char* host = new (std::nothrow) unsigned char[std::max<size_t>(head, 1)];
   Range* ranges = new (std::nothrow) Range[(size_t)count * 4 + 2];
@@ -141,7 +160,7 @@ int salr_muon_plan(const salr_muon_tensor_t* tensors, int32_t count, int32_t p_t
     int32_t k = 0;
     for (int cls = 0; cls < kMuonClasses && rc == SALR_OK; ++cls) {
       for (int32_t i = 0; i < count; ++i) {
-        const Shape q = shape_of(rows(i), cols(i), per);
+        const Shape q = shape_of(rows(i), cols(i), cut);
         if (q.chunks == 0 || q.cls != cls) continue;
         const salr_muon_tensor_t& t = tensors[i];
         const bool ok = t.p && t.g && t.m && aligned16(t.p) && aligned16(t.g) && aligned16(t.m) &&
