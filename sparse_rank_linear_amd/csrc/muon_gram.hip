@@ -8,9 +8,11 @@ namespace {
 // ---- gram ----
 //
 // 8 or 16 waves; kGroups of them share the lower tiles of u u^T, and kParts
-// such groups take every kParts-th 16 columns of a stage.  A stage's sum (KB columns at most) is float,
-// then joins a double: the smallest eigenvalues decide how fast their
-// directions grow, and a float sum over thousands of columns would drown them.
+// such groups take every kParts-th 16 columns of a stage.  Sixteen columns'
+// sums are float, then join a double: the smallest eigenvalues decide how fast
+// their directions grow, and longer float sums drown them (an 80 x 2048 update
+// whose singular values differ 200-fold: X is 2e-5 off; summed in float over
+// 64 columns 6e-5, and over all of them some 1e-3).
 template <int NT>
 struct GramShape {
   static constexpr int KB = muon_stage(NT), S = 16 * NT;
@@ -36,7 +38,7 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
   const float gs = a.dyn ? a.dyn[1] : a.grad_scale;
   const auto grad = to_global<const typename Four<GF>::elem>(M.g);
   const auto mom = to_global<float>(M.m);
-  const auto parts = to_global<float>(M.parts);
+  const auto parts = to_global<double>(M.parts);
   typename Four<GF>::raw vg[kNq];
   f32x4_t vm[kNq];
   const auto load = [&](int64_t k, auto full) __attribute__((always_inline)) {
@@ -74,7 +76,6 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
     if (FULL && k + 2 * KB <= k1) load(k + KB, full);
 #pragma unroll
     for (int t = 0; t < Shape::kPer; ++t) {
-      f32x4_t acc = zero4();
 #pragma unroll
       for (int c = 0; c < KB / 16 / Shape::kParts; ++c) {
         const int col = 16 * (part + c * Shape::kParts);
@@ -90,11 +91,12 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
             y[e] = lds[row_j[t] + (col + 4 * e) * P];
           }
         }
+        f32x4_t acc = zero4();
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc = mfma_f32(x[e], y[e], acc);
-      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[t][e] += (double)acc[e];
+        for (int e = 0; e < 4; ++e) sum[t][e] += (double)acc[e];
+      }
     }
   };
   int64_t k = k0;
@@ -104,7 +106,7 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
     stage(k, std::false_type{});
   }
   // the column parts meet in LDS, in order
-  const auto out = (global<f32x4_t>)(parts + (int64_t)piece * Shape::kTiles * 256);
+  const auto out = (global<f64x4_t>)(parts + (int64_t)piece * Shape::kTiles * 256);
   double* at = reinterpret_cast<double*>(lds) + (group * 64 + lane) * 4;
   for (int q = Shape::kParts - 1; q > 0; --q) {
 #pragma unroll
@@ -123,8 +125,7 @@ __device__ __forceinline__ void gram(const MuonArgs& a, const MuonMatrix& M, int
 #pragma unroll
     for (int t = 0; t < Shape::kPer; ++t) {
       const int tile = group + t * Shape::kGroups;
-      if (tile < Shape::kTiles)
-        out[tile * 64 + lane] = f32x4_t{(float)sum[t][0], (float)sum[t][1], (float)sum[t][2], (float)sum[t][3]};
+      if (tile < Shape::kTiles) out[tile * 64 + lane] = sum[t];
     }
 }
 

@@ -22,10 +22,12 @@ namespace {
 // Symmetric matrices as their lower tiles of 16 x 16 in LDS, a tile or two a
 // wave.  The first kMuonDouble steps in double (see gram): products of float
 // matrices put noise of 2^-24 of the largest eigenvalue on the smallest ones,
-// which grow by a^2 = 12 a step, so what the later steps add counts for 144
-// times less.  Q is float throughout.
+// which grow by a^2 = 12 a step, so what the later steps add counts for 1700
+// times less (an 80 x 2048 update whose singular values differ 200-fold: X is
+// 1e-5 off, after two such steps 5e-5, by float steps on X itself 4e-6; a step
+// in float takes 6 us, in double 9.5).  Q is float throughout.
 constexpr int kTileP = 17, kTileD = 16 * kTileP;  // (rows padded: columns lie on distinct banks)
-constexpr int kMuonDouble = 2;
+constexpr int kMuonDouble = 3;
 
 template <class T>
 struct Acc;
@@ -177,16 +179,16 @@ __global__ __launch_bounds__(IterShape<NT>::kThreads) void muon_iterate_kernel(M
   const int i = lane & 15, g = lane >> 4;
   const int chunks = M.chunks;
   const auto out = to_global<float>(M.q);
-  const auto parts = to_global<const float>(M.parts);
+  const auto parts = to_global<const double>(M.parts);
   // sums of the pieces; a piece's tile holds rows 4g + e of column i by lane
   for (int q = tid; q < kTiles * 64; q += kIterThreads) {
-    const auto at = (global<const f32x4_t>)parts + q;
+    const auto at = (global<const f64x4_t>)parts + q;
     double v[4] = {0, 0, 0, 0};
 #pragma unroll 8
     for (int c = 0; c < chunks; ++c) {
-      const f32x4_t x = at[(int64_t)c * kTiles * 64];
+      const f64x4_t x = at[(int64_t)c * kTiles * 64];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += (double)x[e];
+      for (int e = 0; e < 4; ++e) v[e] += x[e];
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) G[(q >> 6) * kTileD + (4 * ((q & 63) >> 4) + e) * kTileP + (q & 15)] = v[e];
@@ -212,10 +214,11 @@ __global__ __launch_bounds__(IterShape<NT>::kThreads) void muon_iterate_kernel(M
     lower_tile(min(wave + t * Shape::kWaves, kTiles - 1), &ti[t], &tj[t]);
   }
   lds_barrier();
-  static_assert(kMuonDouble == 2, "the steps below");
-  iterate_step<NT, double, double>(a, G, P, Q, true, a.steps == 1, ti, tj, live, wave, i, g);
-  if (a.steps > 1) iterate_step<NT, double, float>(a, G, P, Q, false, a.steps == 2, ti, tj, live, wave, i, g);
-  for (int step = 2; step < a.steps; ++step)
+  for (int step = 0; step < min(kMuonDouble - 1, a.steps); ++step)
+    iterate_step<NT, double, double>(a, G, P, Q, step == 0, step == a.steps - 1, ti, tj, live, wave, i, g);
+  if (a.steps >= kMuonDouble)
+    iterate_step<NT, double, float>(a, G, P, Q, false, a.steps == kMuonDouble, ti, tj, live, wave, i, g);
+  for (int step = kMuonDouble; step < a.steps; ++step)
     iterate_step<NT, float, float>(a, G, P, Q, false, step == a.steps - 1, ti, tj, live, wave, i, g);
   constexpr int S = 16 * NT;
   for (int q = tid; q < S * S; q += kIterThreads) {
@@ -243,14 +246,14 @@ __global__ __launch_bounds__(256) void muon_sum_kernel(MuonArgs a, int32_t m0) {
   const MuonMatrix& M = a.matrices[m0 + blockIdx.y];
   const int q = blockIdx.x * 256 + threadIdx.x, tile = q >> 6;
   if (tile >= kTiles) return;
-  const auto at = to_global<const f32x4_t>(M.parts) + q;
+  const auto at = to_global<const f64x4_t>(M.parts) + q;
   const auto work = to_global<double>(M.work);
   double v[4] = {0, 0, 0, 0};
 #pragma unroll 4
   for (int c = 0; c < M.chunks; ++c) {
-    const f32x4_t x = at[(int64_t)c * kTiles * 64];
+    const f64x4_t x = at[(int64_t)c * kTiles * 64];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += (double)x[e];
+    for (int e = 0; e < 4; ++e) v[e] += x[e];
   }
   int ti, tj;
   lower_tile(tile, &ti, &tj);

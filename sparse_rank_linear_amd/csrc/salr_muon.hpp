@@ -27,7 +27,7 @@ struct MuonMatrix {
   const void* g;
   float* m;
   float* master;
-  float* parts;   // partial products with itself: [chunks][lower tiles][256]
+  double* parts;  // partial products with itself: [chunks][lower tiles][256]
   float* q;       // [S][S]: what the update is multiplied with, S = 16 tiles
   double* work;   // large classes: six [S][S] matrices
   int64_t L;      // long side

@@ -101,7 +101,7 @@ struct Own {
 Own own_bytes(const Shape& q) {
   if (q.chunks == 0) return {0, 0, 0};
   const size_t S = 16 * (size_t)kMuonTiles[q.cls];
-  return {align_up((size_t)q.chunks * muon_lower(kMuonTiles[q.cls]) * 1024, 256), align_up(S * S * 4, 256),
+  return {align_up((size_t)q.chunks * muon_lower(kMuonTiles[q.cls]) * 2048, 256), align_up(S * S * 4, 256),
           q.cls < kMuonLdsClasses ? 0 : S * S * 8 * 6};
 }
 
@@ -183,7 +183,7 @@ int salr_muon_plan(const salr_muon_tensor_t* tensors, int32_t count, int32_t p_t
         m.g = t.g;
         m.m = t.m;
         m.master = t.master;
-        m.parts = reinterpret_cast<float*>(base + at);
+        m.parts = reinterpret_cast<double*>(base + at);
         m.q = reinterpret_cast<float*>(base + at + o.parts);
         m.work = o.work ? reinterpret_cast<double*>(base + at + o.parts + o.q) : nullptr;
         at += o.parts + o.q + o.work;

@@ -185,3 +185,213 @@ def test_plan_order(M, count):
         want = oa.plan(ids, count)
         np.testing.assert_array_equal(off, want[0])
         np.testing.assert_array_equal(order, want[1])
+
+
+def _zeros_like_guarded(shape, dtype, guard=512):
+    """A tensor of `shape` inside a buffer whose ends hold a pattern, and a check of them."""
+    import torch
+
+    n = int(np.prod(shape))
+    buf = torch.full((n + 2 * guard,), 7.0, dtype=dtype, device="cuda")
+    t = buf[guard:guard + n].view(shape)
+    return t, lambda: bool((buf[:guard] == 7).all()) and bool((buf[guard + n:] == 7).all())
+
+
+def test_outputs_end_where_they_end():
+    import torch
+
+    srl = _srl()
+    c = Case(77, 3, 24, 136, 72, "random", seed=5)
+    Y, y_ok = _zeros_like_guarded((77, 72), torch.bfloat16)
+    dX, x_ok = _zeros_like_guarded((77, 136), torch.bfloat16)
+    dA, a_ok = _zeros_like_guarded((3, 24, 136), torch.float32)
+    dB, b_ok = _zeros_like_guarded((3, 72, 24), torch.float32)
+    ws, w_ok = _zeros_like_guarded((srl.adapters_ws_bytes(3, 72, 136, 24, 77, True),), torch.uint8)
+    plan = srl.adapters_plan(c.ids_d, 3)
+    c.check_forward(srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d, Y=Y, ws=ws))
+    c.check_backward(*srl.adapters_backward(c.ad, plan, c.X_d, c.dY_d, base=c.bx_d, dX=dX, dA=dA, dB=dB, ws=ws))
+    assert y_ok() and x_ok() and a_ok() and b_ok() and w_ok()
+
+
+@pytest.mark.parametrize("M", [9, 70, 1300])
+def test_base_in_place_none_and_skipped_dx(M):
+    srl = _srl()
+    c = Case(M, 3, 16, 72, 40, "runs", seed=M)
+    plan = srl.adapters_plan(c.ids_d, 3)
+    want = srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d)
+    Y = c.by_d.clone()
+    assert srl.adapters_forward(c.ad, plan, c.X_d, base=Y, Y=Y) is Y and (Y == want).all()
+    dx, da, db = srl.adapters_backward(c.ad, plan, c.X_d, c.dY_d, base=c.bx_d)
+    none, da2, db2 = srl.adapters_backward(c.ad, plan, c.X_d, c.dY_d, need_dx=False)
+    assert none is None and (da2 == da).all() and (db2 == db).all()
+    x = c.bx_d.clone()
+    assert (srl.adapters_backward(c.ad, plan, c.X_d, c.dY_d, base=x, dX=x)[0] == dx).all()
+    z = Case(M, 3, 16, 72, 40, "runs", base=False, seed=M)
+    z.check_forward(srl.adapters_forward(z.ad, plan, z.X_d))
+    z.check_backward(*srl.adapters_backward(z.ad, plan, z.X_d, z.dY_d))
+
+
+def test_no_tokens():
+    import torch
+
+    srl = _srl()
+    ad = srl.SalrAdapters.empty(2, 16, 24, 8)
+    plan = srl.adapters_plan(torch.empty(0, dtype=torch.int32, device="cuda"), 2)
+    X = torch.empty((0, 24), dtype=torch.bfloat16, device="cuda")
+    dY = torch.empty((0, 16), dtype=torch.bfloat16, device="cuda")
+    assert srl.adapters_forward(ad, plan, X).shape == (0, 16)
+    dA, dB = (torch.ones(s, device="cuda") for s in (ad.a.shape, ad.b.shape))
+    srl.adapters_backward(ad, plan, X, dY, dA=dA, dB=dB)
+    assert (dA == 0).all() and (dB == 0).all()
+
+
+def test_infinite_values_reach_their_own_outputs_only():
+    """An infinite product is an infinite output (its bf16 parts are not inf -
+    inf), and only its token's."""
+    import torch
+
+    srl = _srl()
+    a = torch.zeros((1, 8, 8), dtype=torch.bfloat16, device="cuda")
+    a[0, 0, 0] = 1.0
+    b = torch.zeros((1, 8, 8), dtype=torch.bfloat16, device="cuda")
+    b[0, :, 0] = 2.0
+    X = torch.ones((20, 8), dtype=torch.bfloat16, device="cuda")
+    X[3, 0] = float("inf")
+    X[7, 0] = NAN
+    plan = srl.adapters_plan(torch.zeros(20, dtype=torch.int32, device="cuda"), 1)
+    Y = srl.adapters_forward(srl.SalrAdapters(a, b), plan, X).float()
+    # (0 * inf of the other ranks is NaN by the formula where b's row has them; here rank 0 alone counts)
+    assert torch.isnan(Y[7]).all() and not torch.isfinite(Y[3]).any()
+    assert (Y[[t for t in range(20) if t not in (3, 7)]] == 2.0).all()
+
+
+@pytest.mark.parametrize("M", [40, 1500])
+def test_same_bits_every_time_and_any_workspace(M):
+    """Results do not depend on timing, on what the workspace held, or on the
+    plan's buffer being one of a longer batch."""
+    import torch
+
+    srl = _srl()
+    c = Case(M, 5, 40, 264, 136, "runs", seed=M)
+    plan = srl.adapters_plan(torch.zeros(2 * M, dtype=torch.int32, device="cuda"), 5)
+    srl.adapters_plan(c.ids_d, 5, plan=plan)
+    ws = srl.adapters_workspace(c.ad, 2 * M, backward=True)
+    first = None
+    for fill in (0, 255, 127):
+        ws.fill_(fill)
+        got = [srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d, ws=ws),
+               *srl.adapters_backward(c.ad, plan, c.X_d, c.dY_d, base=c.bx_d, ws=ws)]
+        first = first or got
+        assert all((x == y).all() for x, y in zip(first, got))
+    c.check_forward(first[0])
+    c.check_backward(*first[1:])
+
+
+def test_captured_batches_with_other_ids():
+    """Plan, forward and backward captured once: each replay takes the ids and
+    inputs it finds."""
+    import torch
+
+    srl = _srl()
+    cases = [Case(M, 4, 24, 136, 72, "random", seed=s) for s, M in ((1, 90), (2, 90), (3, 90))]
+    c = cases[0]
+    ids, X, dY = c.ids_d.clone(), c.X_d.clone(), c.dY_d.clone()
+    ws = srl.adapters_workspace(c.ad, 90, backward=True)
+    plan = srl.adapters_plan(ids, 4)
+    Y, dX = torch.empty_like(c.by_d), torch.empty_like(c.bx_d)
+    dA, dB = torch.empty(c.ad.a.shape, device="cuda"), torch.empty(c.ad.b.shape, device="cuda")
+
+    def call():
+        srl.adapters_plan(ids, 4, plan=plan)
+        srl.adapters_forward(c.ad, plan, X, Y=Y, ws=ws)
+        srl.adapters_backward(c.ad, plan, X, dY, dX=dX, dA=dA, dB=dB, ws=ws)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for q in (1, 2, 0, 1):
+        for dst, src in ((ids, cases[q].ids_d), (X, cases[q].X_d), (dY, cases[q].dY_d)):
+            dst.copy_(src)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        p2 = srl.adapters_plan(cases[q].ids_d, 4)
+        want = [srl.adapters_forward(c.ad, p2, X), *srl.adapters_backward(c.ad, p2, X, dY)]
+        # (tokens without an adapter hold NaN inputs: their outputs are zeros)
+        assert all((x == y).all() for x, y in zip((Y, dX, dA, dB), want))
+
+
+def test_two_streams_with_their_own_workspaces():
+    import torch
+
+    srl = _srl()
+    c = Case(1200, 6, 32, 520, 264, "runs", seed=9)
+    plan = srl.adapters_plan(c.ids_d, 6)
+    want = srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(5):
+        for s in streams:
+            p = srl.adapters_plan(c.ids_d, 6, stream=s)
+            got.append(srl.adapters_forward(c.ad, p, c.X_d, base=c.by_d, stream=s))
+    torch.cuda.synchronize()
+    assert all((g == want).all() for g in got)
+
+
+def test_offsets_past_32_bits():
+    """X of more than 2^32 bytes and elements past 2^31."""
+    import torch
+
+    srl = _srl()
+    M, K, N, r = 270000, 8192, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ad = srl.SalrAdapters((torch.randn((2, r, K), generator=g, device="cuda") * 0.1).to(torch.bfloat16),
+                          torch.randn((2, N, r), generator=g, device="cuda").to(torch.bfloat16))
+    X = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, 131071, 262143, 262145, M - 2, M - 1], device="cuda")
+    X[at] = torch.randn((len(at), K), generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.arange(M, device="cuda", dtype=torch.int32) % 3          # (2: no adapter)
+    Y = srl.adapters_forward(ad, srl.adapters_plan(ids, 2), X)
+    some = torch.zeros(M, dtype=torch.bool, device="cuda")
+    some[at] = True
+    assert (Y[~some] == 0).all()
+    for t in at.tolist():
+        q = t % 3
+        if q == 2:
+            assert (Y[t] == 0).all()
+            continue
+        x, A, B = (v.double() for v in (X[t], ad.a[q], ad.b[q]))
+        T = A @ x
+        tol = (B.abs() @ ((K + 64) * U * (A.abs() @ x.abs()) + 2.0 ** -16 * T.abs())) * 1.1 + (B @ T).abs() * H
+        assert ((Y[t].double() - B @ T).abs() <= tol).all()
+
+
+def test_refusals_of_the_binding():
+    import torch
+
+    srl = _srl()
+    ad = srl.SalrAdapters.empty(2, 16, 24, 8)
+    ids = torch.zeros(5, dtype=torch.int32, device="cuda")
+    plan = srl.adapters_plan(ids, 2)
+    X = torch.zeros((5, 24), dtype=torch.bfloat16, device="cuda")
+    for bad in (X.float(), X[:4], X.cpu(), torch.zeros((24, 5), dtype=torch.bfloat16, device="cuda").t()):
+        with pytest.raises((TypeError, ValueError)):
+            srl.adapters_forward(ad, plan, bad)
+    with pytest.raises(srl.SalrError):
+        srl.adapters_forward(ad, srl.adapters_plan(ids, 3), X)           # a plan of other adapters
+    with pytest.raises(srl.SalrError):
+        srl.adapters_forward(ad, plan, X, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(srl.SalrError):
+        srl.adapters_plan(torch.zeros(5000, dtype=torch.int32, device="cuda"), 2, plan=plan)   # a longer batch
+    with pytest.raises(ValueError):
+        srl.SalrAdapters(ad.a, ad.b[:1])
+    with pytest.raises(TypeError):
+        srl.adapters_plan(ids.long(), 2)
+    assert plan.M == 5                                                    # (as it was)
+    assert (srl.adapters_forward(ad, plan, X) == 0).all()

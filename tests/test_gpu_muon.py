@@ -178,3 +178,163 @@ def test_arguments(steps, nesterov, momentum):
     grp = Group([(20, 300), (300, 150), (16, 16)], seed=steps)
     _srl().muon_step(grp.plan, 0.3, steps=steps, nesterov=nesterov, momentum=momentum)
     grp.check(0.3, steps=steps, nesterov=nesterov, momentum=momentum)
+
+
+def test_as_exact_as_float_steps():
+    """Not much further from the definition than Newton-Schulz steps on X
+    itself in float, also where singular values differ a hundredfold: ten
+    times their error and 2^-20 (the sums over A's small eigenvalues)."""
+    import torch
+
+    for kind in ("noise", "signal"):
+        grp = Group([(80, 2048), (1408, 80), (250, 900)], kind=kind, seed=11)
+        for p in grp.params:
+            p.zero_()
+        grp.keep()
+        _srl().muon_step(grp.plan, 1.0)
+        for i, (p0, g, m0) in enumerate(grp.before):
+            want = om.step(p0, g, m0, 1.0, lr_scale=grp.lr_scale[i])[0]
+            u = torch.from_numpy(g + 0.95 * (0.95 * m0 + g)).float().cuda()
+            x = u / (u.norm() + 1e-7)
+            x = x if x.shape[0] <= x.shape[1] else x.t().contiguous()
+            for _ in range(5):
+                A = x @ x.t()
+                x = om.COEFFICIENTS[0] * x + (om.COEFFICIENTS[1] * A + om.COEFFICIENTS[2] * (A @ A)) @ x
+            x = x if x.shape == u.shape else x.t()
+            norm = np.linalg.norm(want)
+            plain = np.linalg.norm(_f64(x) * -grp.lr_scale[i] - want) / norm
+            mine = np.linalg.norm(_f64(grp.params[i]) - want) / norm
+            say(f"  {kind} {p0.shape}: float steps {plain:.1e}, here {mine:.1e}")
+            assert mine <= 10 * plain + 2.0 ** -20
+
+
+def test_training_shrinks_a_residual():
+    """The step as an optimizer's: gradients of |A - W|^2 for a factored A."""
+    import torch
+
+    srl = _srl()
+    torch.manual_seed(0)
+    W = torch.randn(96, 16, device="cuda") @ torch.randn(16, 64, device="cuda")
+    P = [torch.randn(96, 16, device="cuda") * 0.1, torch.randn(16, 64, device="cuda") * 0.1]
+    G = [torch.empty_like(p) for p in P]
+    plan = srl.muon_plan(P, G, **srl.muon_states(P))
+    for _ in range(20):
+        R = P[0] @ P[1] - W
+        G[0].copy_(R @ P[1].t())
+        G[1].copy_(P[0].t() @ R)
+        srl.muon_step(plan, 0.05)
+        assert all(torch.isfinite(p).all() for p in P)
+
+
+def test_same_bits_every_time():
+    import torch
+
+    def once():
+        grp = Group([(80, 1000), (999, 33), (200, 300)], seed=4)
+        _srl().muon_step(grp.plan, 0.1)
+        return grp.params + grp.st["m"]
+
+    a = once()
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(a, once()))
+
+
+def test_nan_and_infinity_stay_in_their_matrix():
+    import torch
+
+    shapes = [(16, 300), (16, 300), (300, 80), (16, 300), (300, 80)]
+    grp, ref = Group(shapes, seed=7), Group(shapes, seed=7)
+    grp.grads[1][3, 200] = float("nan")
+    grp.grads[2][1, 1] = float("inf")
+    for x in (grp, ref):
+        _srl().muon_step(x.plan, 0.1)
+    for i in (0, 3, 4):
+        assert torch.equal(grp.params[i], ref.params[i])
+    for i in (1, 2):
+        assert torch.isnan(grp.params[i]).all()
+
+
+def test_matrices_end_where_they_end():
+    """Matrices of odd sizes side by side in one buffer (16-byte starts): what
+    lies between them stays."""
+    import torch
+
+    srl = _srl()
+    shapes = [(13, 77), (77, 13), (81, 333), (1, 5), (97, 101), (129, 131)]
+    room = [-(-r * c // 8) * 8 + 8 for r, c in shapes]
+    views = lambda buf: [buf[a:a + r * c].view(r, c) for a, (r, c) in zip(np.cumsum([8] + room), shapes)]
+    n = 8 + sum(room)
+    for pt, gt, master in ((torch.float32, torch.float32, False), (torch.bfloat16, torch.bfloat16, True),
+                           (torch.bfloat16, torch.float32, False)):
+        bufs = [torch.full((n,), 3.0, dtype=t, device="cuda") for t in (pt, gt, torch.float32, torch.float32)]
+        P, G, M, W = map(views, bufs)
+        for g in G:
+            g.copy_(torch.randn(g.shape, device="cuda"))
+        plan = srl.muon_plan(P, G, M, master=W if master else None)
+        srl.muon_step(plan, 0.1)
+        hole = torch.ones(n, dtype=torch.bool, device="cuda")
+        for h in views(hole):
+            h.fill_(False)
+        assert all((b[hole] == 3).all() for b in bufs)
+        assert all(not (p == 3).all() for p in P)
+
+
+def test_captured_step_with_dyn():
+    import torch
+
+    srl = _srl()
+    a, b = (Group([(80, 640), (500, 24), (300, 150)], seed=8) for _ in range(2))
+    dyn = torch.tensor([0.0, 1.0], device="cuda")
+    srl.muon_step(a.plan, 0.0, dyn=dyn)              # (a zero rate moves the momenta alone)
+    srl.muon_step(b.plan, 0.0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        srl.muon_step(a.plan, 123.0, weight_decay=0.1, dyn=dyn)
+    for lr, scale in ((0.1, 1.0), (0.02, 0.5), (0.3, 2.0)):
+        dyn.copy_(torch.tensor([lr, scale]))
+        torch.cuda.synchronize()
+        graph.replay()
+        srl.muon_step(b.plan, lr, weight_decay=0.1, grad_scale=scale)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(a.params + a.st["m"], b.params + b.st["m"]))
+    with pytest.raises(srl.SalrError):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            srl.muon_plan(a.params, a.grads, **a.st)
+
+
+def test_step_on_another_stream():
+    import torch
+
+    srl = _srl()
+    a, b = (Group([(80, 640), (500, 24)], seed=8) for _ in range(2))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    srl.muon_step(a.plan, 0.1, stream=s)
+    s.synchronize()
+    srl.muon_step(b.plan, 0.1)
+    assert all(torch.equal(x, y) for x, y in zip(a.params, b.params))
+
+
+def test_refusals_of_the_binding():
+    import torch
+
+    srl = _srl()
+    p = torch.zeros((16, 40), device="cuda")
+    st = srl.muon_states([p])
+    for bad in (dict(grads=[p.to(torch.float16)]), dict(grads=[p.t()]), dict(grads=[p[:8]]), dict(grads=[p.cpu()]),
+                dict(params=[p.view(-1)]), dict(grads=[]), dict(master=[p, p]), dict(lr_scale=[1.0, 2.0])):
+        with pytest.raises((TypeError, ValueError)):
+            srl.muon_plan(**{**dict(params=[p], grads=[p.clone()], m=st["m"]), **bad})
+    with pytest.raises(srl.SalrError):
+        srl.muon_plan([p], [p], st["m"])                                  # the gradient is what is written
+    with pytest.raises(srl.SalrError):
+        srl.muon_plan([p], [p.clone()], st["m"], master=[p.clone()])      # a master of a float parameter
+    big = torch.zeros((257, 300), device="cuda")
+    with pytest.raises(srl.SalrError):
+        srl.muon_plan([big], [big.clone()], srl.muon_states([big])["m"])
+    plan = srl.muon_plan([p], [p.clone()], st["m"])
+    for bad in (dict(lr=-1.0), dict(momentum=1.0), dict(eps=0.0), dict(steps=0), dict(steps=7),
+                dict(coefficients=(1.0, float("nan"), 0.0)), dict(grad_scale=float("inf"))):
+        with pytest.raises(srl.SalrError):
+            srl.muon_step(plan, **{**dict(lr=0.1), **bad})
