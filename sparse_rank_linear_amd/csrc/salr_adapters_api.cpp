@@ -42,19 +42,22 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
   p.max_tiles = (int32_t)most_pieces(M, count + 1, p.tile);
   p.max_chunks = (int32_t)most_pieces(M, count, p.chunk);
   p.max_parts = (int32_t)std::min<int64_t>(p.max_chunks, 2 * M / p.chunk);
-  char* at = static_cast<char*>(buffer);
+  size_t at = 0;
   const auto take = [&](size_t n) {
-    char* q = at;
+    const uintptr_t q = reinterpret_cast<uintptr_t>(buffer) + at;  // (the buffer may be null: sizes alone)
     at += align_up(n, 16);
-    return static_cast<void*>(q);
+    return reinterpret_cast<void*>(q);
   };
   p.head = static_cast<int32_t*>(take(16));
   p.offsets = static_cast<int32_t*>(take(((size_t)count + 2) * 4));
   p.parts = static_cast<int32_t*>(take(((size_t)count + 2) * 4));
   p.order = static_cast<int32_t*>(take((size_t)M * 4));
-  p.tiles = static_cast<salr::AdapterTile*>(take((size_t)p.max_tiles * sizeof(salr::AdapterTile)));
+  // (room for the small tiles of shorter batches, so that a buffer serves those too)
+  const int64_t room = std::max<int64_t>(p.max_tiles, most_pieces(std::min(M, salr::kAdapterSmallTokens), count + 1,
+                                                                  salr::kAdapterSmallTile));
+  p.tiles = static_cast<salr::AdapterTile*>(take((size_t)room * sizeof(salr::AdapterTile)));
   p.chunks = static_cast<salr::AdapterTile*>(take((size_t)p.max_chunks * sizeof(salr::AdapterTile)));
-  if (bytes) *bytes = (size_t)(at - static_cast<char*>(buffer));
+  if (bytes) *bytes = at;
   return p;
 }
 

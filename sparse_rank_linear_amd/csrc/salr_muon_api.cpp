@@ -156,7 +156,7 @@ int salr_muon_plan(const salr_muon_tensor_t* tensors, int32_t count, int32_t p_t
     size_t nw = 0, nr = 0, at = head;
     Range* read = ranges + (size_t)count * 3 + 1;
     const size_t pb = p_type == SALR_TYPE_F32 ? 4 : 2, gb = g_type == SALR_TYPE_F32 ? 4 : 2;
-    char* base = static_cast<char*>(table);
+    const uintptr_t base = reinterpret_cast<uintptr_t>(table);  // (may be null: refused below)
     int32_t k = 0;
     for (int cls = 0; cls < kMuonClasses && rc == SALR_OK; ++cls) {
       for (int32_t i = 0; i < count; ++i) {

@@ -231,6 +231,18 @@ def test_base_in_place_none_and_skipped_dx(M):
     z.check_backward(*srl.adapters_backward(z.ad, plan, z.X_d, z.dY_d))
 
 
+def test_a_buffer_serves_shorter_batches():
+    """A plan of 1100 tokens, whose tiles are large, used again for 1000, whose
+    tiles are small and more."""
+    import torch
+
+    srl = _srl()
+    plan = srl.adapters_plan(torch.zeros(1100, dtype=torch.int32, device="cuda"), 300)
+    c = Case(1000, 300, 8, 16, 8, "random", seed=2)
+    assert srl.adapters_plan(c.ids_d, 300, plan=plan) is plan
+    c.check_forward(srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d))
+
+
 def test_no_tokens():
     import torch
 
