@@ -741,8 +741,8 @@ typedef struct salr_adapters_plan {
   int32_t count;
 } salr_adapters_plan_t;
 
-/* Bytes of the buffer of a plan for M tokens and `count` adapters (`out` host;
- * 0 <= M < 2^31 - 65536).  Errors: INVALID_ARG. */
+/* Bytes of the buffer of a plan for up to M tokens and `count` adapters (`out`
+ * host; 0 <= M <= 2^27).  Errors: INVALID_ARG. */
 int salr_adapters_plan_bytes(int64_t M, int32_t count, size_t* out);
 
 /*
@@ -820,7 +820,8 @@ int salr_adapters_backward(const salr_adapters_t* A,
  * The steps run on the product of u with itself, summed and iterated in
  * double (float products of its pieces): X is as exact as by float steps on
  * X itself up to a few 1e-5 of it (its smallest singular values; 1e-6 where
- * they are of one size).  u's sum of squares has to fit a float.  A matrix
+ * they are of one size).  u's sum of squares has to fit a float, and elements
+ * below 1e-19, whose squares do not, may count as zeros in |u|.  A matrix
  * with a NaN or an infinity among its gradients gets NaN everywhere; others
  * do not see it.
  */
@@ -847,8 +848,8 @@ typedef struct salr_muon_plan {
   int32_t chunks[SALR_MUON_CLASSES];
 } salr_muon_plan_t;
 
-/* What one step uses.  lr, weight_decay >= 0, eps > 0, 0 <= momentum < 1, 1 <=
- * steps <= 6, all finite. */
+/* What one step uses.  lr, weight_decay >= 0, eps >= 1e-12, 0 <= momentum < 1,
+ * 1 <= steps <= 6, all finite floats. */
 typedef struct salr_muon_step_args {
   double lr, momentum, weight_decay, eps, grad_scale;
   double a, b, c;
@@ -859,7 +860,8 @@ typedef struct salr_muon_step_args {
 /* Bytes of the plan's device buffer for `count` matrices (`rows`, `cols` and
  * `out` host; count <= 2^20).  Errors: INVALID_ARG, UNSUPPORTED (a shorter
  * side above SALR_MUON_MAX_SIDE, a matrix of 2^29 elements or more; more than
- * 2^40 elements in all, or more pieces of matrices than one launch takes). */
+ * 65535 matrices of one class of shorter sides above 112, than 2^40 elements in
+ * all, or more pieces of matrices than one launch takes). */
 int salr_muon_plan_bytes(const int64_t* rows, const int64_t* cols,
                          int32_t count, size_t* out);
 

@@ -233,7 +233,7 @@ __global__ __launch_bounds__(IterShape<NT>::kThreads) void muon_iterate_kernel(M
 // [S][S] doubles in memory, 32 x 32 of a product a workgroup (the lower
 // blocks, mirrored), both operands read along their rows.
 struct MuonProduct {
-  // out = scale^x left right (+ ...) : which of the matrix's five
+  // out = left right: which of the matrix's six
   int left, right, out;
   bool poly;      // out = a I + b left + c left right
   int first;      // left and right are not scaled yet: poly: both; else: right

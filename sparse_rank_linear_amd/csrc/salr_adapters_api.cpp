@@ -11,7 +11,9 @@
 
 namespace {
 
-constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 65536;
+// (2^21 + 4097 tiles, times four groups of ranks, times 256 threads: the most
+// that a launch takes has 32 bits)
+constexpr int64_t kMaxTokens = int64_t(1) << 27;
 constexpr int64_t kMaxColumns = int64_t(1) << 20;
 constexpr int32_t kMaxRank = 256;
 using namespace salr;
@@ -52,11 +54,13 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
   p.offsets = static_cast<int32_t*>(take(((size_t)count + 2) * 4));
   p.parts = static_cast<int32_t*>(take(((size_t)count + 2) * 4));
   p.order = static_cast<int32_t*>(take((size_t)M * 4));
-  // (room for the small tiles of shorter batches, so that a buffer serves those too)
+  // (room for what shorter batches have more of, so that a buffer serves those
+  // too: small tiles, and chunks, which are M / 32 tokens long or more)
+  const int64_t chunk_room = std::min<int64_t>(32, M / salr::kAdapterMinChunk) + std::min<int64_t>(M, count);
   const int64_t room = std::max<int64_t>(p.max_tiles, most_pieces(std::min(M, salr::kAdapterSmallTokens), count + 1,
                                                                   salr::kAdapterSmallTile));
   p.tiles = static_cast<salr::AdapterTile*>(take((size_t)room * sizeof(salr::AdapterTile)));
-  p.chunks = static_cast<salr::AdapterTile*>(take((size_t)p.max_chunks * sizeof(salr::AdapterTile)));
+  p.chunks = static_cast<salr::AdapterTile*>(take((size_t)chunk_room * sizeof(salr::AdapterTile)));
   if (bytes) *bytes = at;
   return p;
 }

@@ -1,5 +1,5 @@
 // The orthogonalised step: what the C ABI (salr_muon_api.cpp) and the kernels
-// (muon.hip) share.
+// (muon_*.hip) share.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -20,7 +20,9 @@ constexpr int32_t kMaxMatrices = 1 << 20;
 constexpr int64_t kMaxSide = int64_t(1) << 30;
 constexpr int64_t kMaxMatrix = int64_t(1) << 29;   // elements of one: the kernels' byte offsets have 32 bits
 constexpr int64_t kMaxElements = int64_t(1) << 40;
-constexpr int64_t kMaxChunks = (int64_t(1) << 24) - 1;
+constexpr int64_t kMaxChunks = (int64_t(1) << 22) - 1;  // of up to 1024 threads: a launch takes 2^32
+constexpr int32_t kMaxLarge = 65535;  // matrices of a class that has a grid dimension for them
+constexpr double kMinEps = 1e-12;     // far above |u| of elements whose squares a float does not hold
 static_assert(SALR_MUON_CLASSES == kMuonClasses, "a plan counts every class");
 
 int class_of(int64_t s) {
@@ -59,7 +61,7 @@ Shape shape_of(int64_t rows, int64_t cols, const Cut& cut) {
 // workgroups for the CUs, then fewer and longer ones; from ten tiles on a CU
 // holds one workgroup at a time, and a few more than there are CUs would take
 // twice as long (253 x 67584 columns in 267 chunks 139 us, in 237 ones 85).
-// INVALID_ARG, UNSUPPORTED (a short side over the limit, too many chunks) or 0.
+// INVALID_ARG, UNSUPPORTED (a short side over the limit, too many pieces) or 0.
 constexpr int64_t kCus = 256;
 template <class R, class C>
 int survey(int32_t count, R rows, C cols, Cut* cut, int64_t* chunks) {
@@ -78,7 +80,13 @@ int survey(int32_t count, R rows, C cols, Cut* cut, int64_t* chunks) {
       n[q.cls] += q.chunks;
     }
   };
-  int64_t n[kMuonClasses];
+  int64_t n[kMuonClasses], matrices[kMuonClasses] = {};
+  for (int32_t i = 0; i < count; ++i) {
+    const Shape q = shape_of(rows(i), cols(i), *cut);
+    matrices[q.cls] += q.chunks > 0;
+  }
+  for (int cls = kMuonLdsClasses; cls < kMuonClasses; ++cls)
+    if (matrices[cls] > kMaxLarge) return SALR_ERR_UNSUPPORTED;
   chunks_of(n);
   for (int cls = 0; cls < kMuonClasses; ++cls)
     for (int k = 0; k < 16 && kMuonTiles[cls] >= 10 && n[cls] > kCus && n[cls] < 2 * kCus; ++k) {
@@ -164,7 +172,7 @@ int salr_muon_plan(const salr_muon_tensor_t* tensors, int32_t count, int32_t p_t
         if (q.chunks == 0 || q.cls != cls) continue;
         const salr_muon_tensor_t& t = tensors[i];
         const bool ok = t.p && t.g && t.m && aligned16(t.p) && aligned16(t.g) && aligned16(t.m) &&
-                        (t.master != nullptr) == master && aligned16(t.master) && std::isfinite(t.lr_scale);
+                        (t.master != nullptr) == master && aligned16(t.master) && std::isfinite((float)t.lr_scale);
         if (!ok) {
           rc = SALR_ERR_INVALID_ARG;
           break;
@@ -235,17 +243,18 @@ int salr_muon_step(const salr_muon_plan_t* plan, const salr_muon_step_args_t* ar
   int64_t matrices = 0, chunks = 0;
   for (int c = 0; c < kMuonClasses; ++c) {
     if (plan->matrices[c] < 0 || plan->chunks[c] < 0) return SALR_ERR_INVALID_ARG;
+    if (c >= kMuonLdsClasses && plan->matrices[c] > kMaxLarge) return SALR_ERR_INVALID_ARG;
     matrices += plan->matrices[c];
     chunks += plan->chunks[c];
   }
   if (matrices > plan->count || chunks > kMaxChunks) return SALR_ERR_INVALID_ARG;
-  const auto nonneg = [](double v) { return v >= 0 && std::isfinite(v); };
-  if (!nonneg(args->weight_decay) || !nonneg(args->eps) || args->eps == 0) return SALR_ERR_INVALID_ARG;
+  const auto nonneg = [](double v) { return v >= 0 && std::isfinite((float)v); };
+  if (!nonneg(args->weight_decay) || !nonneg(args->eps) || args->eps < kMinEps) return SALR_ERR_INVALID_ARG;
   if (!(args->momentum >= 0 && args->momentum < 1) || args->steps < 1 || args->steps > kMuonMaxSteps)
     return SALR_ERR_INVALID_ARG;
   for (double v : {args->a, args->b, args->c})
     if (!std::isfinite(v)) return SALR_ERR_INVALID_ARG;
-  if (!dyn && (!nonneg(args->lr) || !std::isfinite(args->grad_scale))) return SALR_ERR_INVALID_ARG;
+  if (!dyn && (!nonneg(args->lr) || !std::isfinite((float)args->grad_scale))) return SALR_ERR_INVALID_ARG;
   if (!aligned4(dyn)) return SALR_ERR_INVALID_ARG;
   MuonArgs a{};
   a.matrices = static_cast<const MuonMatrix*>(plan->table);

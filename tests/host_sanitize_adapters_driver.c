@@ -26,10 +26,10 @@ static void* at(uint64_t a) { return (void*)(uintptr_t)a; }
 
 static void adapters(void) {
   size_t n = 0;
-  EXPECT(salr_adapters_plan_bytes((INT64_C(1) << 31) - 65536, SALR_ADAPTERS_MAX, &n) == SALR_OK);
-  EXPECT(n >= (size_t)4 * ((INT64_C(1) << 31) - 65536));
+  EXPECT(salr_adapters_plan_bytes(INT64_C(1) << 27, SALR_ADAPTERS_MAX, &n) == SALR_OK);
+  EXPECT(n >= (size_t)(INT64_C(4) << 27));
   EXPECT(salr_adapters_plan_bytes(INT64_MAX, 1, &n) == SALR_ERR_INVALID_ARG);
-  EXPECT(salr_adapters_ws_bytes(SALR_ADAPTERS_MAX, 1 << 20, 1 << 20, 256, (INT64_C(1) << 31) - 65536, 1, &n) == SALR_OK);
+  EXPECT(salr_adapters_ws_bytes(SALR_ADAPTERS_MAX, 1 << 20, 1 << 20, 256, INT64_C(1) << 27, 1, &n) == SALR_OK);
   EXPECT(salr_adapters_ws_bytes(1, 1, 8, 8, 0, 0, &n) == SALR_OK && n > 0);
   salr_adapters_plan_t plan;
   memset(&plan, 0, sizeof plan);
@@ -37,7 +37,7 @@ static void adapters(void) {
   EXPECT(salr_adapters_plan(at(0x100000), 100, 4, at(0x100000), 1 << 20, &plan, NULL) == SALR_ERR_INVALID_ARG);
   EXPECT(plan.buffer == NULL);
   plan.buffer = at(0x200000);
-  plan.M = (INT64_C(1) << 31) - 65536;
+  plan.M = INT64_C(1) << 27;
   plan.count = 4096;
   salr_adapters_t a = {4096, 256, 1 << 20, 1 << 20, at(0x10000000000), at(0x20000000000), NULL, NULL};
   /* spans of many terabytes, and at the top of the address space */

@@ -40,6 +40,14 @@ def test_plan_refusals_and_sizes():
         assert sizes == sorted(sizes)                  # (a plan's buffer serves shorter batches)
         assert srl.adapters_plan_bytes(1024, count) <= srl.adapters_plan_bytes(1025, count)
         assert all(s >= 4 * M for M, s in zip(range(0, 200000, 701), sizes))
+        # chunks become longer from 32768 tokens on, by 64 every 2048
+        for M in (1024, 32768, 34816, 34817, 65536, 1 << 20, (1 << 20) + 2048):
+            assert srl.adapters_plan_bytes(M, count) <= srl.adapters_plan_bytes(M + 1, count), (count, M)
+    # as many tokens as every launch has room for
+    assert srl.adapters_plan_bytes(1 << 27, 4096) > 4 << 27
+    assert lib.salr_adapters_plan_bytes((1 << 27) + 1, 1, C.byref(n)) == -1
+    assert lib.salr_adapters_ws_bytes(1, 16, 24, 8, (1 << 27) + 1, 0, C.byref(n)) == -1
+    assert call(M=(1 << 27) + 1, n=1 << 40) == -1
 
 
 def _forward(A=None, plan=None, X=P + 0x100000, base=P + 0x200000, Y=P + 0x300000, ws=P + 0x400000, n=1 << 24):
@@ -139,6 +147,7 @@ def test_muon_plan_refusals():
     assert _muon_plan([a, a], **far) == -1                                  # written twice
     assert _muon_plan([_tensor(1, g=P + 0x100000 + 16)], **far) == -1        # a gradient that is written
     assert _muon_plan([a], table=P + 0x120000 + 256) == -1                   # the table on the momentum
+    assert _muon_plan([_tensor(1, lr_scale=1e39)], **far) == -1
     # empty matrices need nothing
     assert _muon_plan([_tensor(1, p=None, g=None, m=None, rows=0)], nbytes=0, **far) == -3
 
@@ -152,6 +161,9 @@ def test_muon_sizes_and_step_refusals():
     assert lib.salr_muon_plan_bytes(i64(-1), i64(40), 1, C.byref(out)) == -1
     assert lib.salr_muon_plan_bytes(i64(300), i64(300), 1, C.byref(out)) == -2
     assert lib.salr_muon_plan_bytes(None, None, 0, C.byref(out)) == 0
+    # shorter sides above 112 have launches with room for 65535 matrices; below, they need no more
+    for side, n, want in ((113, 65535, 0), (113, 65536, -2), (112, 65536, 0)):
+        assert lib.salr_muon_plan_bytes((C.c_int64 * n)(*[side] * n), (C.c_int64 * n)(*[200] * n), n, C.byref(out)) == want
     plan = B.salr_muon_plan_t(P, 1, 1, 1, 0)
     plan.matrices[0], plan.chunks[0] = 1, 1
     args = dict(lr=0.1, momentum=0.9, weight_decay=0.0, eps=1e-7, grad_scale=1.0, a=3.4, b=-4.7, c=2.0, steps=5,
@@ -162,6 +174,9 @@ def test_muon_sizes_and_step_refusals():
     for bad in (dict(lr=-1.0), dict(lr=nan), dict(momentum=1.0), dict(momentum=-0.1), dict(weight_decay=-1.0),
                 dict(eps=0.0), dict(eps=inf), dict(grad_scale=nan), dict(a=inf), dict(b=nan), dict(c=inf),
                 dict(steps=0), dict(steps=7), dict(dyn=P + 2)):
+        assert step(**bad) == -1, bad
+    # what no float holds, and an eps beside which squares that underflow would count
+    for bad in (dict(lr=1e39), dict(weight_decay=1e39), dict(grad_scale=-1e39), dict(eps=1e-13)):
         assert step(**bad) == -1, bad
     for field, v in (("table", None), ("table", P + 4), ("count", -1), ("p_type", 3), ("g_type", 3), ("has_master", 1),
                      ("count", 0)):
