@@ -1339,7 +1339,10 @@ class SalrAdapters:
                                      check(b, "b", torch.bfloat16, (self.count, self.N, self.r)),
                                      check(self.ranks, "ranks", torch.int32, (self.count,)),
                                      check(self.scales, "scales", torch.float32, (self.count,)))
-        self._held = (a, b, self.ranks, self.scales)   # what the descriptor points to
+        self._held = self._tensors()   # what the descriptor points to
+
+    def _tensors(self):
+        return [(t, None if t is None else t.data_ptr()) for t in (self.a, self.b, self.ranks, self.scales)]
 
     @classmethod
     def empty(cls, count, N, K, r, device="cuda"):
@@ -1349,8 +1352,8 @@ class SalrAdapters:
                    torch.zeros((count, N, r), dtype=torch.bfloat16, device=device))
 
     def descriptor(self) -> salr_adapters_t:
-        a, b, ranks, scales = self._held
-        if a is not self.a or b is not self.b or ranks is not self.ranks or scales is not self.scales:
+        # (a tensor may have been replaced, or its memory)
+        if any(t is not u or p != q for (t, p), (u, q) in zip(self._held, self._tensors())):
             self.__post_init__()
         return self._desc
 

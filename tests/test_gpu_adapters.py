@@ -243,6 +243,28 @@ def test_a_buffer_serves_shorter_batches():
     c.check_forward(srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d))
 
 
+def test_replaced_tensors_and_memory():
+    """What the adapters hold when a call is made is what it uses, though a
+    tensor, or the memory behind one, has been replaced since the last."""
+    srl = _srl()
+    c, d = (Case(40, 4, 16, 72, 48, "runs", mixed=False, seed=q) for q in (3, 3))
+    for q in (0, 1):
+        plan = srl.adapters_plan(c.ids_d, 4)
+        c.check_forward(srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d))
+        keep = c.ad.a.data, c.ad.b.data        # (alive: the new memory is elsewhere)
+        if q == 0:
+            c.ad.a.data, c.ad.b.data = d.ad.a.flip(0), d.ad.b.flip(0)
+        else:
+            c.ad.a, c.ad.b = d.ad.a.flip(0), d.ad.b.flip(0)
+            c.a, c.b = d.a, d.b
+        c.a, c.b = c.a[::-1], c.b[::-1]
+        c.check_forward(srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d))
+        del keep
+    c.ad.b.data = d.ad.b[:3].clone()
+    with pytest.raises(ValueError):
+        srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d)
+
+
 def test_no_tokens():
     import torch
 
