@@ -11,7 +11,14 @@ namespace {
 //
 // Wave w holds row tile w % NT of Q in registers and takes its share of the
 // stage's 16-column tiles; Q u goes through LDS to the threads that hold the
-// parameters.
+// parameters.  Bound by memory and the fp32 products one after the other, as
+// the waves of a workgroup do the same at a time: 192 pairs of 80 x 2048 and 80
+// x 1408, bf16 parameters and float gradients, 179 us (3.6 TB/s; the
+// products are a quarter of it), 64 of 112 x 4096 and 112 x 14336 with masters
+// 592 us (4.0 TB/s), three of 253 x 8191 and 253 x 14337 149 us (273 MB, 56 us,
+// and 8.9 GFLOP, 58).
+// Stores past the caches, loads ahead by two stages and stores spread over the
+// next stage's products were all slower.
 template <int NT>
 struct ApplyShape {
   static constexpr int KB = muon_stage(NT), S = 16 * NT;
@@ -113,7 +120,8 @@ __device__ __forceinline__ void apply(const MuonArgs& a, const MuonMatrix& M, in
 }
 
 template <int NT, bool GF, bool PF, bool MASTER>
-__global__ __launch_bounds__(ApplyShape<NT>::kWaves * 64, NT == 3 || NT > 5 ? 4 : 5) void muon_apply_kernel(MuonArgs a, int64_t c0, int sub) {
+__global__ __launch_bounds__(ApplyShape<NT>::kWaves * 64, NT == 3 || NT > 5 ? 4 : 5) void muon_apply_kernel(
+    MuonArgs a, int64_t c0, int sub) {
   extern __shared__ __attribute__((aligned(16))) float lds[];  // u, then Q u
   const MuonChunk ch = a.chunks[c0 + blockIdx.x / sub];
   const MuonMatrix& M = a.matrices[ch.matrix];

@@ -130,7 +130,8 @@ struct Stage {
       v[q] = FULL ? load4<F32>(element(p, q, k)) : Four<F32>::part(element(p, q, k), count(q, left));
   }
   template <bool FULL, bool F32>
-  __device__ __forceinline__ void store(global<typename Four<F32>::elem> p, int q, int64_t k, int left, f32x4_t x) const {
+  __device__ __forceinline__ void store(global<typename Four<F32>::elem> p, int q, int64_t k, int left,
+                                        f32x4_t x) const {
     if (FULL) {
       if (has(q)) *(global<typename Four<F32>::any>)element(p, q, k) = Four<F32>::pack(x);
     } else {

@@ -25,7 +25,9 @@ namespace {
 // which grow by a^2 = 12 a step, so what the later steps add counts for 1700
 // times less (an 80 x 2048 update whose singular values differ 200-fold: X is
 // 1e-5 off, after two such steps 5e-5, by float steps on X itself 4e-6; a step
-// in float takes 6 us, in double 9.5).  Q is float throughout.
+// in float takes 6 us, in double 9.5).  Q is float throughout.  Bound by the
+// chain of products of one matrix, each waiting for LDS: 53 us for rank 80,
+// alone or one matrix a CU; 159 for 128 matrices of rank 112.
 constexpr int kTileP = 17, kTileD = 16 * kTileP;  // (rows padded: columns lie on distinct banks)
 constexpr int kMuonDouble = 3;
 
@@ -223,15 +225,18 @@ __global__ __launch_bounds__(IterShape<NT>::kThreads) void muon_iterate_kernel(M
   constexpr int S = 16 * NT;
   for (int q = tid; q < S * S; q += kIterThreads) {
     const int r = q / S, c = q % S, hi = max(r, c), lo = min(r, c);
-    out[q] =
-        (float)((double)Q[((hi >> 4) * ((hi >> 4) + 1) / 2 + (lo >> 4)) * kTileD + (hi & 15) * kTileP + (lo & 15)] * inv);
+    const int tile = (hi >> 4) * ((hi >> 4) + 1) / 2 + (lo >> 4);
+    out[q] = (float)((double)Q[tile * kTileD + (hi & 15) * kTileP + (lo & 15)] * inv);
   }
 }
 
 // ---- iterate, larger matrices: one launch a product ----
 //
 // [S][S] doubles in memory, 32 x 32 of a product a workgroup (the lower
-// blocks, mirrored), both operands read along their rows.
+// blocks, mirrored), both operands read along their rows.  (Eight tiles' lower
+// halves in double take more than a CU's LDS.)  14 products for five steps, 12.4
+// us each for six matrices of 256 x 256: a launch, a trip through the caches for
+// operands that other dies wrote, 16 double products a wave one after another.
 struct MuonProduct {
   // out = left right: which of the matrix's six
   int left, right, out;
@@ -357,8 +362,8 @@ hipError_t launch_class(const MuonArgs& a, int32_t m0, int32_t n, hipStream_t s)
     // of the six: 0 the first product (which stays), 1 and 2 Q in turn, 3 P, 4 W; A_1 and on: in 5
     const unsigned blocks = (unsigned)muon_lower(S / 32);
     const auto product = [&](MuonProduct x, MuonProduct y, int jobs) {
-      hipLaunchKernelGGL(muon_product_kernel<NT>, dim3(blocks, (unsigned)n, (unsigned)jobs), dim3(kProductThreads), 0, s, a, m0, x,
-                         y);
+      hipLaunchKernelGGL(muon_product_kernel<NT>, dim3(blocks, (unsigned)n, (unsigned)jobs), dim3(kProductThreads), 0, s,
+                         a, m0, x, y);
     };
     int q = 1, A = 0;
     for (int step = 0; step < a.steps; ++step) {

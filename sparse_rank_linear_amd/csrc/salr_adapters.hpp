@@ -8,12 +8,18 @@
 
 namespace salr {
 
-// Tokens of a tile, all of one adapter: few tokens take small tiles (more
-// workgroups, leaner kernels), many take large ones (the adapter is read once
-// for four times the tokens).
+// Tokens of a tile, all of one adapter.  Few tokens take small tiles: more
+// workgroups, leaner kernels, and the pieces of T few enough to be summed where
+// they are used (256 tokens of 32 adapters, rank 16, 4096 x 14336: 13 us, with
+// large tiles 20; 64 tokens of 64 adapters, rank 64, 4096 x 4096: 20 and 28).
+// Many take large ones: the adapter is read once for four times the tokens
+// (8191 tokens, ranks 8 to 64, 4096 x 11008: 133 us, with small tiles 228).
 constexpr int kAdapterSmallTile = 16, kAdapterLargeTile = 64;
 constexpr int64_t kAdapterSmallTokens = 1024;  // the most with small tiles
-constexpr int kAdapterMinChunk = 1024;    // tokens that one workgroup sums a gradient over, at least
+// Tokens that one workgroup sums a gradient over, at least, and not more than 64
+// partial sums in all: products and sums take 54 us for 4099 tokens of 6
+// adapters, rank 80, 4096 x 11008, in chunks of 1024 tokens 65, of 256 62.
+constexpr int kAdapterMinChunk = 512;
 constexpr int kAdapterMaxSplits = 32;     // pieces of a contraction over K (or N)
 
 // One tile or chunk: tokens order[begin, end) of one adapter (`count`: tokens

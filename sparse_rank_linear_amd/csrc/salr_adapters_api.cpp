@@ -65,20 +65,26 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
   return p;
 }
 
-// A contraction over K columns in pieces: enough workgroups for the CUs.  Of M
-// tokens the pieces come to at most min(kAdapterMaxSplits M, M + 64 kGroups)
-// rows of T.
+// A contraction over K columns in pieces: enough workgroups for the CUs, fewer
+// where a token's sums are long (each piece writes them: 4099 tokens, rank 80:
+// down and finish 64 us, with twice the workgroups 73; rank 16: with half of
+// them 45 for 42) and for small tiles, whose pieces are summed by every
+// workgroup that uses them.  Of M tokens the pieces come to at most
+// min(kAdapterMaxSplits M, M + 64 kGroups) rows of T.
 constexpr int64_t kGroups = 1024;
+constexpr int32_t kFewRanks = 32;
 int64_t t_rows(int64_t M) { return std::min<int64_t>(salr::kAdapterMaxSplits * M, M + 64 * kGroups); }
 void cut(salr::AdapterDown* d, const salr::AdapterPlan& p, int32_t r) {
   const int64_t work = std::max<int64_t>(1, p.max_tiles * cdiv(r, 80));
-  const int64_t groups = p.tile == salr::kAdapterSmallTile ? kGroups / 2 : kGroups;
+  const int64_t groups = kGroups / (p.tile == salr::kAdapterSmallTile ? 2 : 1) / (r > kFewRanks ? 2 : 1);
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(salr::kAdapterMaxSplits, cdiv(groups, work)));
   d->cols = (int32_t)(cdiv(cdiv(d->K, want), 256) * 256);
   d->splits = (int32_t)cdiv(d->K, d->cols);
 }
-// Slices of N outputs: as many as 512 (small tiles) or 2048 workgroups take, in
-// eights where there are eight (one for each die, see adapter_down_kernel).
+// Slices of N outputs: as many as 512 (small tiles, whose workgroups sum T's
+// pieces first) or 2048 workgroups take, in eights where there are eight (one
+// for each die, see adapter_down_kernel).  With 1024 for both: 64 tokens of 64
+// adapters 12.9 us for 9.8, 8191 tokens 110 for 101.
 int32_t up_slices(int64_t N, const salr::AdapterPlan& p) {
   const int64_t groups = p.tile == salr::kAdapterSmallTile ? 512 : 2048;
   const int64_t steps = cdiv(N, 256), want = cdiv(groups, std::max<int64_t>(1, p.max_tiles));
@@ -116,7 +122,8 @@ Workspace lay_out(int64_t count, int64_t N, int64_t K, int32_t r, int64_t M, boo
 int check(const salr_adapters_t* A, const salr_adapters_plan_t* P) {
   if (!shape_ok(A) || !P || !plan_shape_ok(P->M, P->count) || P->count != A->count) return SALR_ERR_INVALID_ARG;
   if (!P->buffer || !aligned16(P->buffer) || !A->a || !A->b) return SALR_ERR_INVALID_ARG;
-  if (!aligned16(A->a) || !aligned16(A->b) || !aligned16(A->ranks) || !aligned16(A->scales)) return SALR_ERR_INVALID_ARG;
+  if (!aligned16(A->a) || !aligned16(A->b) || !aligned16(A->ranks) || !aligned16(A->scales))
+    return SALR_ERR_INVALID_ARG;
   return SALR_OK;
 }
 

@@ -60,7 +60,7 @@ Shape shape_of(int64_t rows, int64_t cols, const Cut& cut) {
 // How the matrices are cut, and the chunks that makes in all.  Enough
 // workgroups for the CUs, then fewer and longer ones; from ten tiles on a CU
 // holds one workgroup at a time, and a few more than there are CUs would take
-// twice as long (253 x 67584 columns in 267 chunks 139 us, in 237 ones 85).
+// half as long again (253 x 67584 columns in 267 chunks 139 us, in 237 ones 100).
 // INVALID_ARG, UNSUPPORTED (a short side over the limit, too many pieces) or 0.
 constexpr int64_t kCus = 256;
 template <class R, class C>

@@ -40,8 +40,8 @@ def test_plan_refusals_and_sizes():
         assert sizes == sorted(sizes)                  # (a plan's buffer serves shorter batches)
         assert srl.adapters_plan_bytes(1024, count) <= srl.adapters_plan_bytes(1025, count)
         assert all(s >= 4 * M for M, s in zip(range(0, 200000, 701), sizes))
-        # chunks become longer from 32768 tokens on, by 64 every 2048
-        for M in (1024, 32768, 34816, 34817, 65536, 1 << 20, (1 << 20) + 2048):
+        # chunks become longer from 16384 tokens on, by 64 every 2048
+        for M in (1024, 16384, 18432, 18433, 34816, 65536, 1 << 20, (1 << 20) + 2048):
             assert srl.adapters_plan_bytes(M, count) <= srl.adapters_plan_bytes(M + 1, count), (count, M)
     # as many tokens as every launch has room for
     assert srl.adapters_plan_bytes(1 << 27, 4096) > 4 << 27
