@@ -76,30 +76,42 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
   const int64_t t0 = min(M, wave * each), t1 = min(M, t0 + each);  // (no tokens from wave `waves` on)
   const uint64_t below = (1ull << lane) - 1ull;
   // f(token, its group, whether it exists, the lanes of the same group) for 64
-  // tokens at a time, in order; kAhead such batches are read together
-  const auto walk = [&](auto f) __attribute__((always_inline)) {
-    constexpr int kAhead = 8;
+  // tokens at a time, in order; kAhead such batches are read together, and kept
+  // for the second pass where there are no more
+  constexpr int kAhead = 8;
+  int group[kAhead];
+  uint64_t alike[kAhead];
+  const auto walk = [&](bool second, auto f) __attribute__((always_inline)) {
     for (int64_t b = t0; b < t1; b += 64 * kAhead) {
-      int g[kAhead];
+      if (!second || each > 64 * kAhead) {
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) g[q] = ids[min(b + 64 * q + lane, t1 - 1)];
+        for (int q = 0; q < kAhead; ++q) {
+          const int x = ids[min(b + 64 * q + lane, t1 - 1)];
+          group[q] = (uint32_t)x < (uint32_t)p.count ? x : p.count;
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+          if (b + 64 * q >= t1) break;
+          const bool live = b + 64 * q + lane < t1;
+          const int x = group[q];
+          uint64_t same = __ballot(live);
+          if (__ballot(live && x == __builtin_amdgcn_readfirstlane(x)) != same) {  // (a prompt's tokens are alike)
+            for (int k = 0; k < bits; ++k) {
+              const uint64_t set = __ballot((x >> k) & 1);
+              same &= (x >> k) & 1 ? set : ~set;
+            }
+          }
+          alike[q] = same;
+        }
+      }
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         if (b + 64 * q >= t1) break;
-        const bool live = b + 64 * q + lane < t1;
-        const int x = (uint32_t)g[q] < (uint32_t)p.count ? g[q] : p.count;
-        uint64_t same = __ballot(live);
-        if (__ballot(live && x == __builtin_amdgcn_readfirstlane(x)) != same) {  // (a prompt's tokens are alike)
-          for (int k = 0; k < bits; ++k) {
-            const uint64_t set = __ballot((x >> k) & 1);
-            same &= (x >> k) & 1 ? set : ~set;
-          }
-        }
-        f(b + 64 * q + lane, x, live, same);
+        f(b + 64 * q + lane, group[q], b + 64 * q + lane < t1, alike[q]);
       }
     }
   };
-  walk([&](int64_t, int g, bool live, uint64_t same) {
+  walk(false, [&](int64_t, int g, bool live, uint64_t same) {
     if (live && (same & below) == 0) cnt[wave * G + g] += (uint32_t)__popcll(same);
   });
   __syncthreads();
@@ -134,7 +146,9 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    for (int w = 0; w < wave; ++w) before[q] += wsum[q][w];
+    // (all read, as a loop to `wave` would wait for one after another)
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) before[q] += w < wave ? wsum[q][w] : 0u;
     n[q] = before[q];
   }
   for (int g = g0; g < g1; ++g) {
@@ -162,7 +176,7 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
     p.head[1] = (int32_t)chunk[G];
   }
   // place the tokens
-  walk([&](int64_t t, int g, bool live, uint64_t same) {
+  walk(true, [&](int64_t t, int g, bool live, uint64_t same) {
     if (!live) return;
     uint32_t* at = &cnt[wave * G + g];
     const uint32_t first = *at;
