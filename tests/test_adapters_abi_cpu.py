@@ -163,7 +163,8 @@ def test_muon_sizes_and_step_refusals():
     assert lib.salr_muon_plan_bytes(None, None, 0, C.byref(out)) == 0
     # shorter sides above 112 have launches with room for 65535 matrices; below, they need no more
     for side, n, want in ((113, 65535, 0), (113, 65536, -2), (112, 65536, 0)):
-        assert lib.salr_muon_plan_bytes((C.c_int64 * n)(*[side] * n), (C.c_int64 * n)(*[200] * n), n, C.byref(out)) == want
+        rows, cols = i64(*[side] * n), i64(*[200] * n)
+        assert lib.salr_muon_plan_bytes(rows, cols, n, C.byref(out)) == want
     plan = B.salr_muon_plan_t(P, 1, 1, 1, 0)
     plan.matrices[0], plan.chunks[0] = 1, 1
     args = dict(lr=0.1, momentum=0.9, weight_decay=0.0, eps=1e-7, grad_scale=1.0, a=3.4, b=-4.7, c=2.0, steps=5,

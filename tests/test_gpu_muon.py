@@ -85,7 +85,8 @@ class Group:
         up = lambda x, t: torch.from_numpy(np.ascontiguousarray(x)).cuda().to(t)
         self.params = [up(rng.standard_normal(s) * 0.02, pt) for s in shapes]
         kinds = kind if isinstance(kind, list) else [kind] * len(shapes)
-        self.grads = [up(_gradient(*s, k, rng) * 10.0 ** (-4 + i % 5), gt) for i, (s, k) in enumerate(zip(shapes, kinds))]
+        self.grads = [up(_gradient(*s, k, rng) * 10.0 ** (-4 + i % 5), gt)
+                      for i, (s, k) in enumerate(zip(shapes, kinds))]
         self.st = srl.muon_states(self.params, master=master)
         if not fresh:
             for i, (m, s, k) in enumerate(zip(self.st["m"], shapes, kinds)):
@@ -224,6 +225,49 @@ def test_training_shrinks_a_residual():
         G[1].copy_(P[0].t() @ R)
         srl.muon_step(plan, 0.05)
         assert all(torch.isfinite(p).all() for p in P)
+
+
+@pytest.mark.parametrize("rows,cols", [(256, 2097151), (2097151, 256), (3, 178956969), (536870911, 1)])
+def test_largest_matrices(rows, cols):
+    """Just below 2^29 elements, 2^31 bytes: against the definition in double,
+    a stretch of the long side at a time."""
+    import torch
+
+    srl = _srl()
+    s, L = min(rows, cols), max(rows, cols)
+    gen = torch.Generator(device="cuda").manual_seed(rows % 1000)
+    g = torch.randn((rows, cols), generator=gen, device="cuda")
+    p, m = torch.zeros_like(g), torch.zeros_like(g)
+    srl.muon_step(srl.muon_plan([p], [g], [m], lr_scale=[1.0]), 1.0, momentum=0.0)
+    assert torch.equal(m, g)
+
+    def pieces(x):
+        x = x if rows <= cols else x.T
+        each = (1 << 24) // s
+        return (x[:, k:k + each].double().contiguous() for k in range(0, L, each))
+
+    # (a library product over so long an axis with few rows takes seconds)
+    square = lambda x: x @ x.T.contiguous() if s > 3 else (x[:, None] * x[None]).sum(2)
+    gram, mags = (sum(square(f(x)) for x in pieces(g)) for f in (lambda x: x, torch.abs))
+    norm = float(gram.diagonal().sum().sqrt()) + 1e-7
+    sv, V = np.linalg.eigh((gram / norm ** 2).cpu().numpy())
+    sv = np.maximum(sv, 0.0)
+    q = om.growth(sv)
+    Q = torch.from_numpy((V * q) @ V.T).cuda()
+    # (as x_tolerance, for singular values far from zero: the slopes bound the quotients)
+    lo, hi = sv.min() * 0.999, sv.max() * 1.001
+    at = np.linspace(lo, hi, 20001)
+    K = np.abs(np.diff(om.growth(at)) / np.diff(at)).max() * 1.01 * np.sqrt(hi)
+    product = sum(float((Q.abs() @ (x.abs() / norm)).square().sum()) for x in pieces(g)) ** 0.5
+    tol = (K * (4 * U * 16 * float(mags.norm()) / norm ** 2 + 6 * U) + 5 * U * float(Q.norm()) + 3 * U * np.abs(q).max()
+           + 4 * U * 16 * product + 4 * U * s ** 0.5 * np.abs(q * np.sqrt(sv)).max())
+    off = sum(float((y + Q @ (x / norm)).square().sum()) for x, y in zip(pieces(g), pieces(p))) ** 0.5
+    say(f"  {rows} x {cols}: X off by {off:.2e}, allowed {tol:.2e}")
+    assert off <= tol
+    first, last = next(pieces(g)), (g if rows <= cols else g.T)[:, -5:].double()
+    for x, y in ((first[:, :5], next(pieces(p))[:, :5]), (last, (p if rows <= cols else p.T)[:, -5:].double())):
+        want = -(Q @ (x / norm))
+        assert ((y - want).abs() <= 1e-4 * want.abs().max()).all()        # (at either end, each value of its own size)
 
 
 def test_same_bits_every_time():
