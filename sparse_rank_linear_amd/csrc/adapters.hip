@@ -248,14 +248,15 @@ __device__ __forceinline__ f32x4_t sum_pieces(const float* at, int64_t plane, in
 // of 64 adapters 30 us for 20, one token 9.2 for 8.6.
 template <int RT, int NS>
 __global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterCommon c, AdapterDown j0, AdapterDown j1,
-                                                                int parts, int groups) {
+                                                                int parts0, int parts, int groups) {
   __shared__ f32x4_t sums[kWaves][RT][64];
   const AdapterPlan& p = c.plan;
-  const int ti = blockIdx.x / parts, part = blockIdx.x % parts;
-  const AdapterTile t = p.tiles[ti];  // (past the last: whatever was there)
+  const int ti = blockIdx.x / parts, any = blockIdx.x % parts;  // (parts: those of both contractions)
+  const AdapterTile t = p.tiles[ti];                           // (past the last: whatever was there)
   if (ti >= p.head[0] || t.adapter >= p.count) return;
-  const AdapterDown j = blockIdx.y ? j1 : j0;
-  const int split = part / groups, rank0 = (part % groups) * RT * 16;
+  const bool first = any < parts0;
+  const AdapterDown j = first ? j0 : j1;
+  const int part = first ? any : any - parts0, split = part / groups, rank0 = (part % groups) * RT * 16;
   const int live = live_ranks(c, t.adapter);
   if (split >= j.splits || rank0 >= live) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
@@ -729,17 +730,17 @@ hipError_t launch_adapter_plan(const int32_t* ids, const AdapterPlan& p, hipStre
 
 hipError_t launch_adapter_down(const AdapterCommon& c, const AdapterDown* jobs, int n_jobs, hipStream_t s) {
   int splits = 0;
-  for (int q = 0; q < n_jobs; ++q) splits = std::max(splits, jobs[q].splits);
+  for (int q = 0; q < n_jobs; ++q) splits += jobs[q].splits;
   with_rank_tiles(c.r, [&](auto rt, int groups) {
     constexpr int RT = decltype(rt)::value;
-    const int parts = splits * groups;
-    const dim3 grid((unsigned)c.plan.max_tiles * parts, (unsigned)n_jobs);
+    const int parts0 = jobs[0].splits * groups, parts = splits * groups;
+    const dim3 grid((unsigned)c.plan.max_tiles * parts);
     if (c.plan.tile == kAdapterSmallTile)
-      hipLaunchKernelGGL((adapter_down_kernel<RT, 1>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], parts,
-                         groups);
+      hipLaunchKernelGGL((adapter_down_kernel<RT, 1>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], parts0,
+                         parts, groups);
     else
-      hipLaunchKernelGGL((adapter_down_kernel<RT, 4>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], parts,
-                         groups);
+      hipLaunchKernelGGL((adapter_down_kernel<RT, 4>), grid, dim3(kThreads), 0, s, c, jobs[0], jobs[n_jobs - 1], parts0,
+                         parts, groups);
   });
   return hipGetLastError();
 }

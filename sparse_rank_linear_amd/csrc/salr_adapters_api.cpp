@@ -65,21 +65,32 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
   return p;
 }
 
-// A contraction over K columns in pieces: enough workgroups for the CUs, fewer
-// where a token's sums are long (each piece writes them: 4099 tokens, rank 80:
-// down and finish 64 us, with twice the workgroups 73; rank 16: with half of
-// them 45 for 42) and for small tiles, whose pieces are summed by every
-// workgroup that uses them.  Of M tokens the pieces come to at most
-// min(kAdapterMaxSplits M, M + 64 kGroups) rows of T.
-constexpr int64_t kGroups = 1024;
+// Contractions over their columns in pieces: enough workgroups for the CUs, and
+// fewer for small tiles, whose pieces are summed by every workgroup that uses
+// them, and where a token's sums are long (each piece writes them).  Above
+// kFewRanks a CU holds three workgroups of large tiles: pieces as long for one
+// contraction as for the other, as many as one round of workgroups takes, in
+// eights where there are eight (4099 tokens, rank 80, 4096 and 11008 columns:
+// 51 us in 8 pieces; in 10 56, in 16 of unequal lengths and two rounds 56).  Up
+// to kFewRanks, two rounds are better than one (8192 tokens, rank 16: 37 us for
+// 40).  Of M tokens the pieces of one come to at most min(kAdapterMaxSplits M, M + 64
+// kGroups) rows of T.
+constexpr int64_t kGroups = 1024, kRound = 768;
 constexpr int32_t kFewRanks = 32;
 int64_t t_rows(int64_t M) { return std::min<int64_t>(salr::kAdapterMaxSplits * M, M + 64 * kGroups); }
-void cut(salr::AdapterDown* d, const salr::AdapterPlan& p, int32_t r) {
+void cut(salr::AdapterDown* d, int n, const salr::AdapterPlan& p, int32_t r) {
   const int64_t work = std::max<int64_t>(1, p.max_tiles * cdiv(r, 80));
-  const int64_t groups = kGroups / (p.tile == salr::kAdapterSmallTile ? 2 : 1) / (r > kFewRanks ? 2 : 1);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(salr::kAdapterMaxSplits, cdiv(groups, work)));
-  d->cols = (int32_t)(cdiv(cdiv(d->K, want), 256) * 256);
-  d->splits = (int32_t)cdiv(d->K, d->cols);
+  const bool small = p.tile == salr::kAdapterSmallTile, few = r <= kFewRanks;
+  int64_t all = 0, round = std::max<int64_t>(n, kRound / work);
+  if (round >= 8) round -= round % 8;
+  for (int q = 0; q < n; ++q) all += d[q].K;
+  for (int q = 0; q < n; ++q) {
+    const int64_t each = small || few ? cdiv(kGroups / (small ? 2 : 1) / (few ? 1 : 2), work)
+                                      : cdiv(d[q].K * round, all);
+    const int64_t want = std::min<int64_t>(salr::kAdapterMaxSplits, each);
+    d[q].cols = (int32_t)(cdiv(cdiv(d[q].K, want), 256) * 256);
+    d[q].splits = (int32_t)cdiv(d[q].K, d[q].cols);
+  }
 }
 // Slices of N outputs: as many as 512 (small tiles, whose workgroups sum T's
 // pieces first) or 2048 workgroups take, in eights where there are eight (one
@@ -185,7 +196,7 @@ int salr_adapters_forward(const salr_adapters_t* A, const salr_adapters_plan_t* 
   const salr::AdapterCommon c{p, A->ranks, A->scales, A->r};
   char* at = static_cast<char*>(ws);
   salr::AdapterDown d{X, A->a, reinterpret_cast<float*>(at + w.t), A->K, 0, 0};
-  cut(&d, p, A->r);
+  cut(&d, 1, p, A->r);
   if (const int e = status(salr::launch_adapter_down(c, &d, 1, s))) return e;
   uint16_t* planes = nullptr;
   if (p.tile == salr::kAdapterLargeTile) {
@@ -226,7 +237,7 @@ int salr_adapters_backward(const salr_adapters_t* A, const salr_adapters_plan_t*
     uint16_t *a_t = halves(w.a), *b_t = halves(w.b);
     if (const int e = status(salr::launch_adapter_transpose(c, A->a, a_t, A->K, A->b, b_t, A->N, s))) return e;
     salr::AdapterDown d[2] = {{X, A->a, floats(w.t), A->K, 0, 0}, {dY, b_t, floats(w.t + w.t_bytes), A->N, 0, 0}};
-    for (salr::AdapterDown& q : d) cut(&q, p, A->r);
+    cut(d, 2, p, A->r);
     if (const int e = status(salr::launch_adapter_down(c, d, 2, s))) return e;
     const salr::AdapterFinish f[2] = {{d[0].T, t_planes, d[0].splits}, {d[1].T, g_planes, d[1].splits}};
     if (const int e = status(salr::launch_adapter_finish(c, f, 2, s))) return e;
