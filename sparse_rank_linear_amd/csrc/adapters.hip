@@ -239,7 +239,8 @@ __device__ __forceinline__ f32x4_t sum_pieces(const float* at, int64_t plane, in
 // from memory, 16 bytes a lane.  Each wave takes every kWaves-th 64 columns of
 // the piece; the waves' sums meet in LDS, in wave order.  Neighbouring
 // workgroups take a tile's pieces (they run on different dies: a die then sees
-// the same pieces of the adapters again and again, in its own cache).  Bound by
+// the same pieces of the adapters again and again, in its own cache; empty
+// workgroups between them would leave some dies less to do).  Bound by
 // the reads of X and dY: 8192 tokens x 4096, rank 16, both sides 37 us, 3.6
 // TB/s (and 8 MB of pieces written); 8191 prompt tokens 25.4, 2.6
 // TB/s (ranks 8 to 64: a tile of 64 ranks holds 132 registers).  One token: a

@@ -20,7 +20,7 @@ constexpr int64_t kAdapterSmallTokens = 1024;  // the most with small tiles
 // partial sums in all: products and sums take 54 us for 4099 tokens of 6
 // adapters, rank 80, 4096 x 11008, in chunks of 1024 tokens 65, of 256 62.
 constexpr int kAdapterMinChunk = 512;
-constexpr int kAdapterMaxSplits = 32;     // pieces of a contraction over K (or N)
+constexpr int kAdapterMaxSplits = 32;  // pieces of a contraction over K (or N)
 
 // One tile or chunk: tokens order[begin, end) of one adapter (`count`: tokens
 // without any).  part: a chunk's place among the partial sums, -1 where its

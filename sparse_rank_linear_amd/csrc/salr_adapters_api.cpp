@@ -71,22 +71,23 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
 // kFewRanks a CU holds three workgroups of large tiles: pieces as long for one
 // contraction as for the other, as many as one round of workgroups takes, in
 // eights where there are eight (4099 tokens, rank 80, 4096 and 11008 columns:
-// 51 us in 8 pieces; in 10 56, in 16 of unequal lengths and two rounds 56).  Up
-// to kFewRanks, two rounds are better than one (8192 tokens, rank 16: 37 us for
-// 40).  Of M tokens the pieces of one come to at most min(kAdapterMaxSplits M, M + 64
-// kGroups) rows of T.
+// 51 us in 8 pieces; in 10 or 11 56, in 16 and two rounds 55).  Up to kFewRanks,
+// two rounds are better than one (8192 tokens, rank 16: 37 us for 40).
+//   Each of `work` tiles has at most 64 tokens, so that one piece, or up to
+// (kGroups + work) / work, or up to kRound / work, come to at most M + 64
+// kGroups rows of T, and as many as kAdapterMaxSplits M.
 constexpr int64_t kGroups = 1024, kRound = 768;
 constexpr int32_t kFewRanks = 32;
 int64_t t_rows(int64_t M) { return std::min<int64_t>(salr::kAdapterMaxSplits * M, M + 64 * kGroups); }
 void cut(salr::AdapterDown* d, int n, const salr::AdapterPlan& p, int32_t r) {
   const int64_t work = std::max<int64_t>(1, p.max_tiles * cdiv(r, 80));
   const bool small = p.tile == salr::kAdapterSmallTile, few = r <= kFewRanks;
-  int64_t all = 0, round = std::max<int64_t>(n, kRound / work);
+  int64_t all = 0, round = kRound / work;
   if (round >= 8) round -= round % 8;
   for (int q = 0; q < n; ++q) all += d[q].K;
   for (int q = 0; q < n; ++q) {
     const int64_t each = small || few ? cdiv(kGroups / (small ? 2 : 1) / (few ? 1 : 2), work)
-                                      : cdiv(d[q].K * round, all);
+                                      : std::max<int64_t>(1, (2 * d[q].K * round + all) / (2 * all));
     const int64_t want = std::min<int64_t>(salr::kAdapterMaxSplits, each);
     d[q].cols = (int32_t)(cdiv(cdiv(d[q].K, want), 256) * 256);
     d[q].splits = (int32_t)cdiv(d[q].K, d[q].cols);

@@ -321,6 +321,50 @@ def test_same_bits_every_time_and_any_workspace(M):
     c.check_backward(*first[1:])
 
 
+@pytest.mark.parametrize("M,r,K,N,backward", [(140000, 40, 512, 16, True), (140000, 40, 16, 512, True),
+                                              (70000, 16, 512, 16, True), (5000, 88, 1024, 64, True),
+                                              (1025, 40, 8192, 16, True), (1024, 256, 4096, 16, True),
+                                              (90000, 64, 1024, 8, False), (1025, 256, 8192, 8, False)])
+def test_workspace_ends_where_it_ends(M, r, K, N, backward):
+    """One side much longer than the other, few and many tiles: nothing is
+    written behind the workspace, and the pieces make the product."""
+    import torch
+
+    srl = _srl()
+    g = torch.Generator(device="cuda").manual_seed(M + r)
+    draw = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    ad = srl.SalrAdapters(draw(2, r, K), draw(2, N, r))
+    X, dY = draw(M, K), draw(M, N)
+    ids = torch.arange(M, device="cuda", dtype=torch.int32) % 2
+    plan = srl.adapters_plan(ids, 2)
+    need = srl.adapters_ws_bytes(2, N, K, r, M, backward)
+    buf = torch.full((need + (64 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = buf[:need]
+    d = lambda t: t.double()
+    if backward:
+        dX, dA, dB = srl.adapters_backward(ad, plan, X, dY, ws=ws)
+    else:
+        Y = srl.adapters_forward(ad, plan, X, ws=ws)
+    assert (buf[need:] == 0xA5).all()
+    for q in (0, 1):
+        x, y, A, B = d(X[q::2]), d(dY[q::2]), d(ad.a[q]), d(ad.b[q])
+        if not backward:
+            got, want, left, right = Y[q::2], x @ A.T.contiguous() @ B.T.contiguous(), x @ A.T.contiguous(), B
+            size = x.abs() @ A.abs().T.contiguous() @ B.abs().T.contiguous()
+            tol = want.abs() * H + ((K + r + 64) * U) * size + 2.0 ** -16 * (left.abs() @ right.abs().T.contiguous())
+            assert ((d(got) - want).abs() <= tol * 1.1).all()
+            continue
+        G, T = y @ B, x @ A.T.contiguous()
+        mag = y.abs() @ B.abs() @ A.abs()
+        tol = (G @ A).abs() * H + (N + r + 64) * U * mag + 2.0 ** -16 * (G.abs() @ A.abs())
+        assert ((d(dX[q::2]) - G @ A).abs() <= tol * 1.1).all()
+        # (sums of M / 2 products of either side, whose own sums are K or N long)
+        t = lambda v: v.T.contiguous()
+        bound = (3 * (M // 2) + K + N + 64) * U
+        assert ((d(dA[q]) - t(G) @ x).abs() <= bound * (t(y.abs() @ B.abs()) @ x.abs())).all()
+        assert ((d(dB[q]) - t(y) @ T).abs() <= bound * (t(y.abs()) @ (x.abs() @ t(A.abs())))).all()
+
+
 def test_captured_batches_with_other_ids():
     """Plan, forward and backward captured once: each replay takes the ids and
     inputs it finds."""
