@@ -245,6 +245,8 @@ struct MuonProduct {
   bool final;     // to M.q, times 1 / (|u| + eps)
 };
 
+// The pieces' sum, both halves.  (Six matrices in 237 pieces of 278 KB: 66 MB in
+// 12 us, most of them from the caches.)
 template <int NT>
 __global__ __launch_bounds__(256) void muon_sum_kernel(MuonArgs a, int32_t m0) {
   constexpr int kTiles = muon_lower(NT), S = 16 * NT;
