@@ -1331,18 +1331,20 @@ class SalrAdapters:
         a, b = self.a, self.b
         if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
             raise ValueError("a must be [count][r][K] and b [count][N][r]")
-        (self.count, self.r, self.K), self.N = a.shape, b.shape[1]
+        (count, r, K), N = a.shape, b.shape[1]
         index = a.get_device()
         check = lambda t, name, dtype, shape: None if t is None else _ptr(t, name, dtype, shape, index)
-        self._desc = salr_adapters_t(self.count, self.r, self.N, self.K,
-                                     check(a, "a", torch.bfloat16, (self.count, self.r, self.K)),
-                                     check(b, "b", torch.bfloat16, (self.count, self.N, self.r)),
-                                     check(self.ranks, "ranks", torch.int32, (self.count,)),
-                                     check(self.scales, "scales", torch.float32, (self.count,)))
+        self._desc = salr_adapters_t(count, r, N, K, check(a, "a", torch.bfloat16, (count, r, K)),
+                                     check(b, "b", torch.bfloat16, (count, N, r)),
+                                     check(self.ranks, "ranks", torch.int32, (count,)),
+                                     check(self.scales, "scales", torch.float32, (count,)))
+        self.count, self.r, self.K, self.N = count, r, K, N
         self._held = self._tensors()   # what the descriptor points to
 
     def _tensors(self):
-        return [(t, None if t is None else t.data_ptr()) for t in (self.a, self.b, self.ranks, self.scales)]
+        # (an address is one device's)
+        return [t if t is None else (t.data_ptr(), t.shape, t.dtype, t.is_contiguous())
+                for t in (self.a, self.b, self.ranks, self.scales)]
 
     @classmethod
     def empty(cls, count, N, K, r, device="cuda"):
@@ -1352,8 +1354,8 @@ class SalrAdapters:
                    torch.zeros((count, N, r), dtype=torch.bfloat16, device=device))
 
     def descriptor(self) -> salr_adapters_t:
-        # (a tensor may have been replaced, or its memory)
-        if any(t is not u or p != q for (t, p), (u, q) in zip(self._held, self._tensors())):
+        # (a tensor may have been replaced, its memory, or how it lies there)
+        if self._held != self._tensors():
             self.__post_init__()
         return self._desc
 
@@ -1416,8 +1418,9 @@ def adapters_workspace(adapters: SalrAdapters, M_max: int, backward: bool = Fals
     """A workspace for adapters_forward (or adapters_backward) of at most M_max
     tokens."""
     torch = _torch()
-    return torch.empty(adapters_ws_bytes(adapters.count, adapters.N, adapters.K, adapters.r, M_max, backward),
-                       dtype=torch.uint8, device=adapters.a.device)
+    d = adapters.descriptor()
+    return torch.empty(adapters_ws_bytes(d.count, d.N, d.K, d.r, M_max, backward), dtype=torch.uint8,
+                       device=adapters.a.device)
 
 
 def _adapters_ws(ws, adapters, M, backward, index):
@@ -1475,17 +1478,18 @@ def adapters_backward(adapters: SalrAdapters, plan: AdaptersPlan, X, dY, base=No
         dX = base = None
     elif dX is None:
         dX = torch.empty(inp, dtype=bf16, device=dev)
+    a_shape, b_shape = (d.count, d.r, d.K), (d.count, d.N, d.r)
     if dA is None:
-        dA = torch.empty(adapters.a.shape, dtype=f32, device=dev)
+        dA = torch.empty(a_shape, dtype=f32, device=dev)
     if dB is None:
-        dB = torch.empty(adapters.b.shape, dtype=f32, device=dev)
+        dB = torch.empty(b_shape, dtype=f32, device=dev)
     ws = _adapters_ws(ws, adapters, M, True, index)
     _check(_lib().salr_adapters_backward(
         C.byref(d), C.byref(plan.desc), _ptr(X, "X", bf16, inp, index),
         _ptr(dY, "dY", bf16, (M, adapters.N), index),
         None if base is None else _ptr(base, "base", bf16, inp, index),
-        None if dX is None else _ptr(dX, "dX", bf16, inp, index), _ptr(dA, "dA", f32, adapters.a.shape, index),
-        _ptr(dB, "dB", f32, adapters.b.shape, index), ws.data_ptr(), ws.numel() * ws.element_size(), at),
+        None if dX is None else _ptr(dX, "dX", bf16, inp, index), _ptr(dA, "dA", f32, a_shape, index),
+        _ptr(dB, "dB", f32, b_shape, index), ws.data_ptr(), ws.numel() * ws.element_size(), at),
         "salr_adapters_backward")
     return dX, dA, dB
 

@@ -5,6 +5,7 @@ work, so these calls are safe without a GPU."""
 import ctypes as C
 
 import pytest
+import torch
 
 import sparse_rank_linear_amd as srl
 from sparse_rank_linear_amd import binding as B
@@ -190,3 +191,48 @@ def test_muon_sizes_and_step_refusals():
     assert lib.salr_muon_step(None, C.byref(B.salr_muon_step_args_t(*args.values())), None, None) == -1
     empty = B.salr_muon_plan_t(P, 0, 1, 1, 0)
     assert step(plan=empty) == 0
+
+
+def _held(count=4, r=16, K=16, N=16):
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    return srl.SalrAdapters(z(count, r, K), z(count, N, r), ranks=torch.full((count,), 5, dtype=torch.int32),
+                            scales=torch.ones(count))
+
+
+def test_descriptor_follows_the_tensors():
+    """Another shape, order or type at the same address is seen: the kernels
+    write as much as the descriptor says."""
+    ad = _held()
+    d = ad.descriptor()
+    assert (d.count, d.r, d.N, d.K) == (4, 16, 16, 16) and d.a == ad.a.data_ptr() and d.ranks == ad.ranks.data_ptr()
+    assert ad.descriptor() is d                                  # (nothing changed)
+    for t in ("a", "b", "ranks", "scales"):                      # two of four adapters
+        getattr(ad, t).data = getattr(ad, t).data[:2]
+    assert ad.descriptor().count == ad.count == 2 and ad.descriptor().a == d.a
+    assert srl.adapters_workspace(ad, 5, backward=True).numel() == srl.adapters_ws_bytes(2, 16, 16, 16, 5, True)
+    # fewer ranks of as many values: [count][8][32] and [count][32][8] at the same addresses
+    ad.a.data, ad.b.data = ad.a.data.view(2, 8, 32), ad.b.data.view(2, 32, 8)
+    # (the workspace is sized before anything else has looked at the tensors)
+    assert srl.adapters_workspace(ad, 5, backward=True).numel() == srl.adapters_ws_bytes(2, 32, 32, 8, 5, True)
+    d = ad.descriptor()
+    assert (d.r, d.N, d.K) == (ad.r, ad.N, ad.K) == (8, 32, 32)
+
+
+@pytest.mark.parametrize("name,change,error", [
+    ("a", lambda t: t[:2], ValueError), ("b", lambda t: t[:3], ValueError),
+    ("a", lambda t: t.transpose(1, 2), ValueError), ("b", lambda t: t.transpose(1, 2), ValueError),
+    ("a", lambda t: t[:, :, ::2], ValueError),
+    ("a", lambda t: t.view(dtype=torch.float16), TypeError),
+    ("b", lambda t: t.view(dtype=torch.int16), TypeError), ("ranks", lambda t: t[:2], ValueError),
+    ("ranks", lambda t: t.view(dtype=torch.float32), TypeError), ("scales", lambda t: t[1:], ValueError),
+    ("scales", lambda t: t[::2], ValueError)])
+def test_descriptor_refuses_what_no_longer_fits(name, change, error):
+    ad = _held()
+    ad.descriptor()
+    t = getattr(ad, name)
+    t.data = change(t.data)
+    for _ in range(2):                                           # (each time it is asked)
+        with pytest.raises(error):
+            ad.descriptor()
+        with pytest.raises(error):
+            srl.adapters_workspace(ad, 5)

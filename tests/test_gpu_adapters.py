@@ -265,6 +265,30 @@ def test_replaced_tensors_and_memory():
         srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d)
 
 
+def test_shrunk_at_the_same_address():
+    """Fewer adapters in the memory of more: the calls work on, and write the
+    gradients of, as many as there are now."""
+    import torch
+
+    srl = _srl()
+    c = Case(90, 4, 24, 136, 72, "runs", seed=6)
+    plan = srl.adapters_plan(c.ids_d, 4)
+    c.check_forward(srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d))
+    for t in (c.ad.a, c.ad.b, c.ad.ranks, c.ad.scales):
+        t.data = t.data[:2]
+    c.count, c.a, c.b, c.ranks, c.scales = 2, c.a[:2], c.b[:2], c.ranks[:2], c.scales[:2]
+    with pytest.raises(srl.SalrError):                                   # (a plan of four)
+        srl.adapters_backward(c.ad, plan, c.X_d, c.dY_d)
+    srl.adapters_plan(c.ids_d, 2, plan=plan)
+    c.check_forward(srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d))
+    dA, a_ok = _zeros_like_guarded((2, 24, 136), torch.float32, 4 * 24 * 136)
+    dB, b_ok = _zeros_like_guarded((2, 72, 24), torch.float32, 4 * 24 * 136)
+    c.check_backward(*srl.adapters_backward(c.ad, plan, c.X_d, c.dY_d, base=c.bx_d, dA=dA, dB=dB))
+    assert a_ok() and b_ok()
+    got = srl.adapters_backward(c.ad, plan, c.X_d, c.dY_d, need_dx=False)[1:]
+    assert torch.equal(got[0], dA) and torch.equal(got[1], dB)
+
+
 def test_no_tokens():
     import torch
 
