@@ -1339,12 +1339,15 @@ class SalrAdapters:
                                      check(self.ranks, "ranks", torch.int32, (count,)),
                                      check(self.scales, "scales", torch.float32, (count,)))
         self.count, self.r, self.K, self.N = count, r, K, N
+        self._index = index
         self._held = self._tensors()   # what the descriptor points to
 
     def _tensors(self):
         # (an address is one device's)
-        return [t if t is None else (t.data_ptr(), t.shape, t.dtype, t.is_contiguous())
-                for t in (self.a, self.b, self.ranks, self.scales)]
+        a, b, r, s = self.a, self.b, self.ranks, self.scales
+        return (a.data_ptr(), a.shape, a.dtype, a.is_contiguous(), b.data_ptr(), b.shape, b.dtype, b.is_contiguous(),
+                r if r is None else (r.data_ptr(), r.shape, r.dtype, r.is_contiguous()),
+                s if s is None else (s.data_ptr(), s.shape, s.dtype, s.is_contiguous()))
 
     @classmethod
     def empty(cls, count, N, K, r, device="cuda"):
@@ -1418,9 +1421,9 @@ def adapters_workspace(adapters: SalrAdapters, M_max: int, backward: bool = Fals
     """A workspace for adapters_forward (or adapters_backward) of at most M_max
     tokens."""
     torch = _torch()
-    d = adapters.descriptor()
-    return torch.empty(adapters_ws_bytes(d.count, d.N, d.K, d.r, M_max, backward), dtype=torch.uint8,
-                       device=adapters.a.device)
+    adapters.descriptor()              # (the sizes below are the tensors' own)
+    return torch.empty(adapters_ws_bytes(adapters.count, adapters.N, adapters.K, adapters.r, M_max, backward),
+                       dtype=torch.uint8, device=adapters.a.device)
 
 
 def _adapters_ws(ws, adapters, M, backward, index):
@@ -1445,7 +1448,7 @@ def adapters_forward(adapters: SalrAdapters, plan: AdaptersPlan, X, base=None, Y
         with _Place(dev, stream):
             return adapters_forward(adapters, plan, X, base, Y, ws)
     d, bf16, out = adapters.descriptor(), torch.bfloat16, (M, adapters.N)
-    if adapters.a.get_device() != index or plan.buffer.get_device() != index:
+    if adapters._index != index or plan.buffer.get_device() != index:
         raise ValueError(f"adapters and plan must be on cuda:{index}")
     if Y is None:
         Y = torch.empty(out, dtype=bf16, device=dev)
@@ -1472,13 +1475,13 @@ def adapters_backward(adapters: SalrAdapters, plan: AdaptersPlan, X, dY, base=No
         with _Place(dev, stream):
             return adapters_backward(adapters, plan, X, dY, base, dX, dA, dB, need_dx, ws)
     d, bf16, f32, inp = adapters.descriptor(), torch.bfloat16, torch.float32, (M, adapters.K)
-    if adapters.a.get_device() != index or plan.buffer.get_device() != index:
+    if adapters._index != index or plan.buffer.get_device() != index:
         raise ValueError(f"adapters and plan must be on cuda:{index}")
     if not need_dx:
         dX = base = None
     elif dX is None:
         dX = torch.empty(inp, dtype=bf16, device=dev)
-    a_shape, b_shape = (d.count, d.r, d.K), (d.count, d.N, d.r)
+    a_shape, b_shape = (adapters.count, adapters.r, adapters.K), (adapters.count, adapters.N, adapters.r)
     if dA is None:
         dA = torch.empty(a_shape, dtype=f32, device=dev)
     if dB is None:
