@@ -664,7 +664,9 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
       }
     }
   }
-  // dA: the lane holds four columns of rank i; dB: four ranks of column i
+  // dA: the lane holds four columns of rank i; dB: four ranks of column i.
+  // (Ranks past the live ones take zeros, whatever their planes' zeros met: 0
+  // times an infinity or a NaN is none.)
   float* out = t.part < 0 ? j.out + (int64_t)t.adapter * c.r * j.C : j.parts + (int64_t)t.part * c.r * j.C;
 #pragma unroll
   for (int a = 0; a < RT; ++a)
@@ -672,8 +674,11 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
     for (int h = 0; h < CT; ++h) {
       const int64_t cc = c0 + 16 * (CT * wave + h) + (is_a ? 4 * g : i);
       const int rr = rank0 + 16 * a + (is_a ? i : 4 * g);
+      f32x4_t v = acc[a][h];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = rr + (is_a ? 0 : e) < live ? v[e] : 0.f;
       if (cc < j.C && rr < c.r)
-        *reinterpret_cast<f32x4_t*>(is_a ? out + (int64_t)rr * j.C + cc : out + cc * c.r + rr) = acc[a][h];
+        *reinterpret_cast<f32x4_t*>(is_a ? out + (int64_t)rr * j.C + cc : out + cc * c.r + rr) = v;
     }
 }
 

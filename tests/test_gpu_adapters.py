@@ -323,6 +323,53 @@ def test_infinite_values_reach_their_own_outputs_only():
     assert (Y[[t for t in range(20) if t not in (3, 7)]] == 2.0).all()
 
 
+class NotFinite:
+    """A backward call with one value of X or dY infinite or NaN, beside the
+    same call with zero there (checked against the oracle): adapters of
+    `ranks` ranks, the value in a token of the middle one."""
+
+    def __init__(self, M, r, ranks, where, value):
+        import torch
+
+        srl = _srl()
+        c = Case(M, len(ranks), r, 136, 72, "runs", mixed=False, seed=M + r)
+        c.ranks = np.array(ranks)
+        c.ad.ranks = torch.tensor(ranks, dtype=torch.int32, device="cuda")
+        plan = srl.adapters_plan(c.ids_d, len(ranks))
+        mine = np.flatnonzero(c.ids == len(ranks) // 2)
+        at = (int(mine[2 * len(mine) // 3]), 41)
+        host, dev = (c.X, c.X_d) if where == "X" else (c.dY, c.dY_d)
+        call = lambda: srl.adapters_backward(c.ad, plan, c.X_d, c.dY_d, base=c.bx_d)
+        host[at] = dev[at] = 0.0
+        clean = call()
+        c.check_backward(*clean)
+        host[at] = dev[at] = value
+        got = call()
+        with np.errstate(invalid="ignore"):
+            self.want = oa.backward(c.a, c.b, c.ids, c.ranks, c.scales, c.X, c.dY, c.bx)
+        self.got, self.clean = ([t.double().cpu().numpy() for t in x] for x in (got, clean))
+        self.ranks = ranks
+
+
+NOT_FINITE = [(M, r, ranks, where, value) for M, r, ranks in ((200, 32, (24, 5, 12)), (200, 32, (5, 24, 12)),
+                                                             (4000, 32, (24, 12, 5)), (3000, 96, (5, 85, 90)))
+              for where in ("X", "dY") for value in (float("inf"), -float("inf"), NAN)]
+
+
+@pytest.mark.parametrize("M,r,ranks,where,value", NOT_FINITE)
+def test_unused_ranks_get_zeros_beside_values_that_are_not_finite(M, r, ranks, where, value):
+    """One chunk of an adapter's tokens, and several.  What the formula gives
+    as finite is what the call without that value gives, to the bit."""
+    q = NotFinite(M, r, ranks, where, value)
+    for i, n in enumerate(ranks):
+        assert (q.got[1][i, n:] == 0).all() and (q.got[2][i, :, n:] == 0).all()
+    for name, got, want, clean in zip(("dX", "dA", "dB"), q.got, q.want, q.clean):
+        finite = np.isfinite(want)
+        assert (np.isfinite(got) == finite).all(), name
+        assert (got[finite] == clean[finite]).all(), name
+    assert not np.isfinite(q.want[1]).all() and not np.isfinite(q.want[2]).all()
+
+
 @pytest.mark.parametrize("M", [40, 1500])
 def test_same_bits_every_time_and_any_workspace(M):
     """Results do not depend on timing, on what the workspace held, or on the
