@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
-constexpr int kThreads = 256;
+constexpr int kThreads = kAdapterThreads;
 constexpr int kWaves = kThreads / 64;
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -701,11 +701,9 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_sum_kernel(AdapterCommo
   *reinterpret_cast<f32x4_t*>(j.out + (int64_t)adapter * size + e) = v;
 }
 
-// The rank tiles of 16 in groups of up to five, as even as they go.
-inline int rank_groups(int r) { return ((r + 15) / 16 + 4) / 5; }
 template <class F>
 void with_rank_tiles(int r, F f) {
-  const int groups = rank_groups(r), rt = ((r + 15) / 16 + groups - 1) / groups;
+  const int groups = adapter_rank_groups(r), rt = ((r + 15) / 16 + groups - 1) / groups;
   if (rt == 1) f(std::integral_constant<int, 1>{}, groups);
   else if (rt == 2) f(std::integral_constant<int, 2>{}, groups);
   else if (rt == 3) f(std::integral_constant<int, 3>{}, groups);

@@ -21,6 +21,10 @@ constexpr int64_t kAdapterSmallTokens = 1024;  // the most with small tiles
 // adapters, rank 80, 4096 x 11008, in chunks of 1024 tokens 65, of 256 62.
 constexpr int kAdapterMinChunk = 512;
 constexpr int kAdapterMaxSplits = 32;  // pieces of a contraction over K (or N)
+constexpr int kAdapterThreads = 256;   // of a workgroup, all kernels but the plan's
+
+// The rank tiles of 16 go in groups of up to five, as even as they go.
+inline int adapter_rank_groups(int r) { return ((r + 15) / 16 + 4) / 5; }
 
 // One tile or chunk: tokens order[begin, end) of one adapter (`count`: tokens
 // without any).  part: a chunk's place among the partial sums, -1 where its

@@ -11,9 +11,10 @@
 
 namespace {
 
-// (2^21 + 4097 tiles, times four groups of ranks, times 256 threads: the most
-// that a launch takes has 32 bits)
+// The most tokens: 2^21 + 4097 tiles, whose contraction of up to four groups of
+// ranks is one launch still (launch_down).
 constexpr int64_t kMaxTokens = int64_t(1) << 27;
+constexpr int64_t kLaunchThreads = int64_t(1) << 32;  // a launch has fewer
 constexpr int64_t kMaxColumns = int64_t(1) << 20;
 constexpr int32_t kMaxRank = 256;
 using namespace salr;
@@ -80,7 +81,7 @@ constexpr int64_t kGroups = 1024, kRound = 768;
 constexpr int32_t kFewRanks = 32;
 int64_t t_rows(int64_t M) { return std::min<int64_t>(salr::kAdapterMaxSplits * M, M + 64 * kGroups); }
 void cut(salr::AdapterDown* d, int n, const salr::AdapterPlan& p, int32_t r) {
-  const int64_t work = std::max<int64_t>(1, p.max_tiles * cdiv(r, 80));
+  const int64_t work = std::max<int64_t>(1, (int64_t)p.max_tiles * adapter_rank_groups(r));
   const bool small = p.tile == salr::kAdapterSmallTile, few = r <= kFewRanks;
   int64_t all = 0, round = kRound / work;
   if (round >= 8) round -= round % 8;
@@ -92,6 +93,18 @@ void cut(salr::AdapterDown* d, int n, const salr::AdapterPlan& p, int32_t r) {
     d[q].cols = (int32_t)(cdiv(cdiv(d[q].K, want), 256) * 256);
     d[q].splits = (int32_t)cdiv(d[q].K, d[q].cols);
   }
+}
+// The contractions in one launch, or where that would have too many threads (both
+// of a backward call whose tiles times groups of ranks are 2^23 or more) in one
+// each.
+hipError_t launch_down(const salr::AdapterCommon& c, const salr::AdapterDown* d, int n, hipStream_t s) {
+  int64_t pieces = 0;
+  for (int q = 0; q < n; ++q) pieces += d[q].splits;
+  if (c.plan.max_tiles * adapter_rank_groups(c.r) * pieces * salr::kAdapterThreads < kLaunchThreads)
+    return salr::launch_adapter_down(c, d, n, s);
+  for (int q = 0; q < n; ++q)
+    if (const hipError_t e = salr::launch_adapter_down(c, d + q, 1, s)) return e;
+  return hipSuccess;
 }
 // Slices of N outputs: as many as 512 (small tiles, whose workgroups sum T's
 // pieces first) or 2048 workgroups take, in eights where there are eight (one
@@ -198,7 +211,7 @@ int salr_adapters_forward(const salr_adapters_t* A, const salr_adapters_plan_t* 
   char* at = static_cast<char*>(ws);
   salr::AdapterDown d{X, A->a, reinterpret_cast<float*>(at + w.t), A->K, 0, 0};
   cut(&d, 1, p, A->r);
-  if (const int e = status(salr::launch_adapter_down(c, &d, 1, s))) return e;
+  if (const int e = status(launch_down(c, &d, 1, s))) return e;
   uint16_t* planes = nullptr;
   if (p.tile == salr::kAdapterLargeTile) {
     planes = reinterpret_cast<uint16_t*>(at + w.planes);
@@ -239,7 +252,7 @@ int salr_adapters_backward(const salr_adapters_t* A, const salr_adapters_plan_t*
     if (const int e = status(salr::launch_adapter_transpose(c, A->a, a_t, A->K, A->b, b_t, A->N, s))) return e;
     salr::AdapterDown d[2] = {{X, A->a, floats(w.t), A->K, 0, 0}, {dY, b_t, floats(w.t + w.t_bytes), A->N, 0, 0}};
     cut(d, 2, p, A->r);
-    if (const int e = status(salr::launch_adapter_down(c, d, 2, s))) return e;
+    if (const int e = status(launch_down(c, d, 2, s))) return e;
     const salr::AdapterFinish f[2] = {{d[0].T, t_planes, d[0].splits}, {d[1].T, g_planes, d[1].splits}};
     if (const int e = status(salr::launch_adapter_finish(c, f, 2, s))) return e;
     if (dX) {
