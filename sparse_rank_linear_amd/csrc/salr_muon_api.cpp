@@ -253,7 +253,7 @@ int salr_muon_step(const salr_muon_plan_t* plan, const salr_muon_step_args_t* ar
   if (!(args->momentum >= 0 && args->momentum < 1) || args->steps < 1 || args->steps > kMuonMaxSteps)
     return SALR_ERR_INVALID_ARG;
   for (double v : {args->a, args->b, args->c})
-    if (!std::isfinite(v)) return SALR_ERR_INVALID_ARG;
+    if (!std::isfinite((float)v)) return SALR_ERR_INVALID_ARG;
   if (!dyn && (!nonneg(args->lr) || !std::isfinite((float)args->grad_scale))) return SALR_ERR_INVALID_ARG;
   if (!aligned4(dyn)) return SALR_ERR_INVALID_ARG;
   MuonArgs a{};

@@ -236,3 +236,18 @@ def test_descriptor_refuses_what_no_longer_fits(name, change, error):
             ad.descriptor()
         with pytest.raises(error):
             srl.adapters_workspace(ad, 5)
+
+
+@pytest.mark.parametrize("name", ["a", "b", "c"])
+def test_muon_coefficients_are_floats(name):
+    """The later steps use them as floats: what no float holds is refused, and
+    the largest floats are not."""
+    plan = B.salr_muon_plan_t(P, 0, 1, 1, 0)             # (no matrices: nothing is launched)
+    args = dict(lr=0.1, momentum=0.9, weight_decay=0.0, eps=1e-7, grad_scale=1.0, a=3.4, b=-4.7, c=2.0, steps=5,
+                nesterov=1)
+    step = lambda v: srl.lib().salr_muon_step(
+        C.byref(plan), C.byref(B.salr_muon_step_args_t(*{**args, name: v}.values())), None, None)
+    for v in (1e39, -1e39, 1e308, float("inf"), float("nan")):
+        assert step(v) == -1, v
+    for v in (3.4e38, -3.4e38, 0.0):
+        assert step(v) == 0, v
