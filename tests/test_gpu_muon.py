@@ -227,6 +227,30 @@ def test_training_shrinks_a_residual():
         assert all(torch.isfinite(p).all() for p in P)
 
 
+def test_training_steps_follow_the_definition():
+    """Twenty steps with fresh gradients and carried momenta, of |P0 P1 - W|^2
+    for a factored matrix: parameters and momenta after each, against the
+    definition's step from the state and the gradients that it found
+    (tests/test_oracle_muon.py: how far a step in a wrong direction or without
+    its momentum would be off)."""
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(0)
+    draw = lambda *s: torch.randn(s, generator=g, device="cuda")
+    W = draw(96, 16) @ draw(16, 64)
+    grp = Group([(96, 16), (16, 64)], fresh=True)
+    for p in grp.params:
+        p.copy_(draw(*p.shape) * 0.1)
+    P = grp.params
+    for _ in range(20):
+        R = P[0] @ P[1] - W
+        grp.grads[0].copy_(R @ P[1].t())
+        grp.grads[1].copy_(P[0].t() @ R)
+        grp.keep()
+        _srl().muon_step(grp.plan, 0.05)
+        grp.check(0.05)
+
+
 @pytest.mark.parametrize("rows,cols", [(256, 2097151), (2097151, 256), (3, 178956969), (536870911, 1)])
 def test_largest_matrices(rows, cols):
     """Just below 2^29 elements, 2^31 bytes: against the definition in double,

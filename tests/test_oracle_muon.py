@@ -55,3 +55,37 @@ def test_planted_mistakes_are_seen():
     for other in ((a, b, -c), (a, c, b), (a, b, 0.9 * c)):
         assert np.abs(om.orthogonalise(u, coefficients=other) - base).max() > 1e-3
     assert np.abs(om.orthogonalise(u, steps=4) - base).max() > 1e-3
+
+
+def test_training_steps_tell_mistakes_apart():
+    """The training of tests/test_gpu_muon.py's
+    test_training_steps_follow_the_definition with mistakes planted in a step:
+    a wrong direction or rate is ten times what that test allows at every step;
+    a momentum that is not carried or not looked ahead with is seen at most
+    steps by the parameters, and the first at every step by the momentum."""
+    from tests.test_gpu_muon import U, x_tolerance
+
+    rng = np.random.default_rng(0)
+    W = rng.standard_normal((96, 16)) @ rng.standard_normal((16, 64))
+    P = [rng.standard_normal((96, 16)) * 0.1, rng.standard_normal((16, 64)) * 0.1]
+    M, lr, scales, seen = [np.zeros_like(p) for p in P], 0.05, (1.0, 1.5), {}
+    for k in range(20):
+        R = P[0] @ P[1] - W
+        G = [R @ P[1].T, P[0].T @ R]
+        for i in (0, 1):
+            go = lambda g, m, **kw: om.step(P[i], g, m, lr, lr_scale=scales[i], **kw)
+            p, m, u = go(G[i], M[i])
+            bound = lr * scales[i] * x_tolerance(u) + 4 * U * np.linalg.norm(np.abs(P[i]) + np.abs(p - P[i]))
+            wrong = {"the other direction": go(-G[i], -M[i]), "the gradient's sign": go(-G[i], M[i]),
+                     "half the rate": om.step(P[i], G[i], M[i], lr / 2, lr_scale=scales[i])}
+            for name, (q, _, _) in wrong.items():
+                if k == 0 or name != "the gradient's sign":      # (later the momentum outweighs it)
+                    assert np.linalg.norm(q - p) > 10 * bound, (k, i, name)
+                seen.setdefault(name, []).append(np.linalg.norm(q - p) > bound)
+            if k > 0:
+                lost = go(G[i], 0 * M[i])
+                assert (np.abs(lost[1] - m) > 10 * 3 * U * (np.abs(0.95 * M[i]) + np.abs(G[i]))).any()
+                for name, q in (("no momentum", lost[0]), ("no Nesterov", go(G[i], M[i], nesterov=False)[0])):
+                    seen.setdefault(name, []).append(np.linalg.norm(q - p) > bound)
+            P[i], M[i] = p, m
+    assert all(np.mean(v) > 0.8 for v in seen.values()), {n: np.mean(v) for n, v in seen.items()}
