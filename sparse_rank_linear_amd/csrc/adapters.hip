@@ -613,56 +613,83 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterCommon c,
   for (int a = 0; a < RT; ++a)
 #pragma unroll
     for (int h = 0; h < CT; ++h) acc[a][h] = zero4();
-  // staging: 16 bytes of CT rows' columns, and 8 ranks of a plane's row a pass
-  constexpr int kRowThreads = kCols / 8, kRows = kThreads / kRowThreads, kPasses = 32 / kRows;
-  const int row = tid / kRowThreads, col = 8 * (tid % kRowThreads);
-  const bool col_in = c0 + col < j.C;
-  constexpr int kRankPieces = 3 * 32 * RT * 2, kRankPasses = (kRankPieces + kThreads - 1) / kThreads;
-  u32x4_t vc[kPasses], vr[kRankPasses];
-  int tok[kPasses];  // the tokens of the next stage
-  const auto next_tokens = [&](int b) __attribute__((always_inline)) {
+  // A token whose columns hold an infinity or a NaN has one in the other product
+  // of its row too, at every rank.
+  bool odd = false;
+  for (int b = t.begin + tid; b < t.end; b += kThreads)
+    odd |= (j.other[(int64_t)b * c.r] & 0x7F80u) == 0x7F80u;
+  // Sums over the chunk.  With APART, what is not finite among the columns meets
+  // the first plane alone, which is infinite or NaN where T or G is, and zero
+  // where it is: the others would make inf - inf or 0 * inf of it.  Otherwise the
+  // same sums, in the same order.
+  const auto sums = [&](int tid, auto apart) __attribute__((always_inline)) {
+    constexpr bool APART = decltype(apart)::value;
+    const int lane = tid & 63, wave = tid >> 6;
+    // staging: 16 bytes of CT rows' columns, and 8 ranks of a plane's row a pass
+    constexpr int kRowThreads = kCols / 8, kRows = kThreads / kRowThreads, kPasses = 32 / kRows;
+    const int row = tid / kRowThreads, col = 8 * (tid % kRowThreads);
+    const bool col_in = c0 + col < j.C;
+    constexpr int kRankPieces = 3 * 32 * RT * 2, kRankPasses = (kRankPieces + kThreads - 1) / kThreads;
+    u32x4_t vc[kPasses], vr[kRankPasses];
+    int tok[kPasses];  // the tokens of the next stage
+    const auto next_tokens = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < kPasses; ++h) tok[h] = p.order[min(b + row + kRows * h, t.end - 1)];
-  };
-  const auto load = [&](int b) __attribute__((always_inline)) {
+      for (int h = 0; h < kPasses; ++h) tok[h] = p.order[min(b + row + kRows * h, t.end - 1)];
+    };
+    const auto load = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < kPasses; ++h)
-      vc[h] = b + row + kRows * h < t.end && col_in ? load16(j.cols + (int64_t)tok[h] * j.C + c0 + col) : zero_u4();
-    if (b + 32 < t.end) next_tokens(b + 32);
+      for (int h = 0; h < kPasses; ++h)
+        vc[h] = b + row + kRows * h < t.end && col_in ? load16(j.cols + (int64_t)tok[h] * j.C + c0 + col) : zero_u4();
+      if (b + 32 < t.end) next_tokens(b + 32);
 #pragma unroll
-    for (int q = 0; q < kRankPasses; ++q) {
-      const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = rank0 + x % (RT * 2) * 8;
-      vr[q] = x < kRankPieces && b + y < t.end && z < live ? load16(j.planes + l * plane + (int64_t)(b + y) * c.r + z)
-                                                          : zero_u4();
-    }
-  };
-  next_tokens(t.begin);
-  load(t.begin);
-  for (int b = t.begin; b < t.end; b += 32) {
-    lds_barrier();
+      for (int q = 0; q < kRankPasses; ++q) {
+        const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = rank0 + x % (RT * 2) * 8;
+        vr[q] = x < kRankPieces && b + y < t.end && z < live
+                    ? load16(j.planes + l * plane + (int64_t)(b + y) * c.r + z)
+                    : zero_u4();
+      }
+    };
+    next_tokens(t.begin);
+    load(t.begin);
+    for (int b = t.begin; b < t.end; b += 32) {
+      lds_barrier();
 #pragma unroll
-    for (int h = 0; h < kPasses; ++h) *reinterpret_cast<u32x4_t*>(&cols[(row + kRows * h) * kColPitch + col]) = vc[h];
+      for (int h = 0; h < kPasses; ++h) *reinterpret_cast<u32x4_t*>(&cols[(row + kRows * h) * kColPitch + col]) = vc[h];
 #pragma unroll
-    for (int q = 0; q < kRankPasses; ++q) {
-      const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = x % (RT * 2) * 8;
-      if (x < kRankPieces) *reinterpret_cast<u32x4_t*>(&rank[l][y * kRankPitch + z]) = vr[q];
-    }
-    lds_barrier();
-    if (b + 32 < t.end) load(b + 32);
-    u32x4_t x[CT];
+      for (int q = 0; q < kRankPasses; ++q) {
+        const int x = tid + q * kThreads, l = x / (32 * RT * 2), y = x / (RT * 2) % 32, z = x % (RT * 2) * 8;
+        if (x < kRankPieces) *reinterpret_cast<u32x4_t*>(&rank[l][y * kRankPitch + z]) = vr[q];
+      }
+      lds_barrier();
+      if (b + 32 < t.end) load(b + 32);
+      u32x4_t x[CT];
 #pragma unroll
-    for (int h = 0; h < CT; ++h) x[h] = read_transposed(cols + 16 * (CT * wave + h), kColPitch, lane);
+      for (int h = 0; h < CT; ++h) x[h] = read_transposed(cols + 16 * (CT * wave + h), kColPitch, lane);
 #pragma unroll
-    for (int a = 0; a < RT; ++a) {
-      if (rank0 + 16 * a >= live) break;  // (zeros from here on)
+      for (int a = 0; a < RT; ++a) {
+        if (rank0 + 16 * a >= live) break;  // (zeros from here on)
 #pragma unroll
-      for (int l = 0; l < 3; ++l) {
-        const u32x4_t y = read_transposed(rank[l] + 16 * a, kRankPitch, lane);
+        for (int l = 0; l < 3; ++l) {
+          const u32x4_t y = read_transposed(rank[l] + 16 * a, kRankPitch, lane);
 #pragma unroll
-        for (int h = 0; h < CT; ++h)
-          acc[a][h] = is_a ? mfma_16x16x32(x[h], y, acc[a][h]) : mfma_16x16x32(y, x[h], acc[a][h]);
+          for (int h = 0; h < CT; ++h) {
+            u32x4_t v = x[h];
+            if (APART && l > 0)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] &= ~(((((v[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xFFFFu);
+            acc[a][h] = is_a ? mfma_16x16x32(v, y, acc[a][h]) : mfma_16x16x32(y, v, acc[a][h]);
+          }
+        }
       }
     }
+  };
+  if (!__syncthreads_or(odd)) {
+    sums(tid, std::false_type{});
+  } else {
+    int again = tid;  // (one that shares no addresses with the loop above: they would stay in registers)
+    asm volatile("" : "+v"(again));
+    sums(again, std::true_type{});
   }
   // dA: the lane holds four columns of rank i; dB: four ranks of column i.
   // (Ranks past the live ones take zeros, whatever their planes' zeros met: 0

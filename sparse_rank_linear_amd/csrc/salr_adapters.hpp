@@ -77,10 +77,11 @@ struct AdapterUp {
 };
 
 // grad[a] = sum over a's tokens of cols[t][c] planes[t][j], stored [r][C]
-// (rank_major) or [C][r].
+// (rank_major) or [C][r].  other: the planes of what cols gave.
 struct AdapterGrad {
   const uint16_t* cols;
   const uint16_t* planes;
+  const uint16_t* other;
   float* out;
   float* parts;
   int64_t C;

@@ -260,8 +260,8 @@ int salr_adapters_backward(const salr_adapters_t* A, const salr_adapters_plan_t*
       if (const int e = status(salr::launch_adapter_up(c, u, s))) return e;
     }
   }
-  return status(salr::launch_adapter_grads(c, {X, g_planes, dA, floats(w.parts_a), A->K},
-                                           {dY, t_planes, dB, floats(w.parts_b), A->N}, s));
+  return status(salr::launch_adapter_grads(c, {X, g_planes, t_planes, dA, floats(w.parts_a), A->K},
+                                           {dY, t_planes, g_planes, dB, floats(w.parts_b), A->N}, s));
 }
 
 }  // extern "C"

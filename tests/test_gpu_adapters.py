@@ -328,12 +328,17 @@ class NotFinite:
     same call with zero there (checked against the oracle): adapters of
     `ranks` ranks, the value in a token of the middle one."""
 
-    def __init__(self, M, r, ranks, where, value):
+    def __init__(self, M, r, ranks, where, value, fresh=False):
         import torch
 
         srl = _srl()
         c = Case(M, len(ranks), r, 136, 72, "runs", mixed=False, seed=M + r)
         c.ranks = np.array(ranks)
+        if fresh:                    # the first rank of A and B zeros
+            for x in (c.a, c.ad.a):
+                x[:, 0] = 0.0
+            for x in (c.b, c.ad.b):
+                x[:, :, 0] = 0.0
         c.ad.ranks = torch.tensor(ranks, dtype=torch.int32, device="cuda")
         plan = srl.adapters_plan(c.ids_d, len(ranks))
         mine = np.flatnonzero(c.ids == len(ranks) // 2)
@@ -368,6 +373,16 @@ def test_unused_ranks_get_zeros_beside_values_that_are_not_finite(M, r, ranks, w
         assert (np.isfinite(got) == finite).all(), name
         assert (got[finite] == clean[finite]).all(), name
     assert not np.isfinite(q.want[1]).all() and not np.isfinite(q.want[2]).all()
+
+
+@pytest.mark.parametrize("fresh", [False, True])
+@pytest.mark.parametrize("M,r,ranks,where,value", NOT_FINITE)
+def test_gradients_of_infinite_values_follow_the_formula(M, r, ranks, where, value, fresh):
+    """Infinite, with its sign, where the formula is, and NaN where it is."""
+    q = NotFinite(M, r, ranks, where, value, fresh)
+    for name, got, want in zip(("dX", "dA", "dB"), q.got, q.want):
+        bad = ~np.isfinite(want) & ~((got == want) | (np.isnan(got) & np.isnan(want)))
+        assert not bad.any(), (name, np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
 
 
 @pytest.mark.parametrize("M", [40, 1500])
