@@ -208,12 +208,15 @@ __device__ __forceinline__ float scale_of(const AdapterCommon& c, int adapter) {
   return c.scales ? c.scales[adapter] : 1.f;
 }
 
-// x as a sum of bf16 values, the first the nearest to it: two of them hold 16
-// of a float's 24 bits, three all of them.  An infinite first one is all.
+// x as a sum of bf16 values, the first the nearest to it (of those that are
+// finite, where x is): two of them hold 16 of a float's 24 bits, three all of
+// them.  An infinite first one is all.
 __device__ __forceinline__ void limbs(float x, uint16_t* w, int n) {
+  constexpr uint32_t kExp = 0x7F800000u;
+  const bool finite = (__float_as_uint(x) & kExp) != kExp;
   w[0] = f32_to_bf16(x);
-  float rest = x - bf16_to_f32(w[0]);
-  if ((w[0] & 0x7F80u) == 0x7F80u) rest = 0.f;
+  if (finite && (w[0] & 0x7FFFu) == 0x7F80u) w[0] -= 1;
+  float rest = finite ? x - bf16_to_f32(w[0]) : 0.f;
   for (int i = 1; i < n; ++i) {
     w[i] = f32_to_bf16(rest);
     rest -= bf16_to_f32(w[i]);

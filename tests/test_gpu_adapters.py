@@ -385,6 +385,34 @@ def test_gradients_of_infinite_values_follow_the_formula(M, r, ranks, where, val
         assert not bad.any(), (name, np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("M", [1, 1100])
+def test_sums_that_bf16_would_round_to_infinity(M, sign):
+    """T (and G) of 2^128 - 2^119 + 2^112: a float holds it, its nearest bf16
+    would be infinite."""
+    import torch
+
+    srl = _srl()
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    plan = srl.adapters_plan(torch.zeros(M, dtype=torch.int32, device="cuda"), 1)
+    big, rest = sign * (2.0 ** 128 - 2.0 ** 120), sign * (2.0 ** 119 + 2.0 ** 112)
+    a, b, X, dY = z(1, 8, 72), z(1, 72, 8), z(M, 72), z(M, 72)
+    a[0, 0, 3] = a[0, 0, 40] = 1.0
+    b[0, 5, 0] = 2.0 ** -10
+    X[:, 3], X[:, 40] = big, rest
+    dY[0, 7] = 2.0 ** -10
+    ad = srl.SalrAdapters(a, b)
+    Y = srl.adapters_forward(ad, plan, X)
+    assert (Y[:, 5] == sign * 2.0 ** 118).all() and Y.count_nonzero() == M
+    dB = srl.adapters_backward(ad, plan, X, dY)[2]
+    assert dB[0, 7, 0].item() == (big + rest) * 2.0 ** -10 and dB.count_nonzero() == 1
+    # the other way round: G
+    ad = srl.SalrAdapters(b.transpose(1, 2).contiguous(), a.transpose(1, 2).contiguous())
+    dX, dA, _ = srl.adapters_backward(ad, plan, dY, X)
+    assert (dX[:, 5] == sign * 2.0 ** 118).all() and dX.count_nonzero() == M
+    assert dA[0, 0, 7].item() == (big + rest) * 2.0 ** -10 and dA.count_nonzero() == 1
+
+
 @pytest.mark.parametrize("M", [40, 1500])
 def test_same_bits_every_time_and_any_workspace(M):
     """Results do not depend on timing, on what the workspace held, or on the
