@@ -1339,7 +1339,7 @@ class SalrAdapters:
                                      check(self.ranks, "ranks", torch.int32, (count,)),
                                      check(self.scales, "scales", torch.float32, (count,)))
         self.count, self.r, self.K, self.N = count, r, K, N
-        self._index = index
+        self._index, self._ref = index, C.byref(self._desc)
         self._held = self._tensors()   # what the descriptor points to
 
     def _tensors(self):
@@ -1447,16 +1447,17 @@ def adapters_forward(adapters: SalrAdapters, plan: AdaptersPlan, X, base=None, Y
     if at is None:
         with _Place(dev, stream):
             return adapters_forward(adapters, plan, X, base, Y, ws)
-    d, bf16, out = adapters.descriptor(), torch.bfloat16, (M, adapters.N)
+    adapters.descriptor()
+    bf16, out = torch.bfloat16, (M, adapters.N)
     if adapters._index != index or plan.buffer.get_device() != index:
         raise ValueError(f"adapters and plan must be on cuda:{index}")
     if Y is None:
         Y = torch.empty(out, dtype=bf16, device=dev)
     ws = _adapters_ws(ws, adapters, M, False, index)
     _check(_lib().salr_adapters_forward(
-        C.byref(d), C.byref(plan.desc), _ptr(X, "X", bf16, (M, adapters.K), index),
+        adapters._ref, C.byref(plan.desc), _ptr(X, "X", bf16, (M, adapters.K), index),
         None if base is None else _ptr(base, "base", bf16, out, index), _ptr(Y, "Y", bf16, out, index),
-        ws.data_ptr(), ws.numel() * ws.element_size(), at), "salr_adapters_forward")
+        ws.data_ptr(), ws.nbytes, at), "salr_adapters_forward")
     return Y
 
 
@@ -1474,7 +1475,8 @@ def adapters_backward(adapters: SalrAdapters, plan: AdaptersPlan, X, dY, base=No
     if at is None:
         with _Place(dev, stream):
             return adapters_backward(adapters, plan, X, dY, base, dX, dA, dB, need_dx, ws)
-    d, bf16, f32, inp = adapters.descriptor(), torch.bfloat16, torch.float32, (M, adapters.K)
+    adapters.descriptor()
+    bf16, f32, inp = torch.bfloat16, torch.float32, (M, adapters.K)
     if adapters._index != index or plan.buffer.get_device() != index:
         raise ValueError(f"adapters and plan must be on cuda:{index}")
     if not need_dx:
@@ -1488,11 +1490,11 @@ def adapters_backward(adapters: SalrAdapters, plan: AdaptersPlan, X, dY, base=No
         dB = torch.empty(b_shape, dtype=f32, device=dev)
     ws = _adapters_ws(ws, adapters, M, True, index)
     _check(_lib().salr_adapters_backward(
-        C.byref(d), C.byref(plan.desc), _ptr(X, "X", bf16, inp, index),
+        adapters._ref, C.byref(plan.desc), _ptr(X, "X", bf16, inp, index),
         _ptr(dY, "dY", bf16, (M, adapters.N), index),
         None if base is None else _ptr(base, "base", bf16, inp, index),
         None if dX is None else _ptr(dX, "dX", bf16, inp, index), _ptr(dA, "dA", f32, a_shape, index),
-        _ptr(dB, "dB", f32, b_shape, index), ws.data_ptr(), ws.numel() * ws.element_size(), at),
+        _ptr(dB, "dB", f32, b_shape, index), ws.data_ptr(), ws.nbytes, at),
         "salr_adapters_backward")
     return dX, dA, dB
 
