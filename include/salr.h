@@ -715,8 +715,9 @@ int salr_adamw_step_random(const salr_adamw_plan_t* plan,
  * count) has no adapter: its output is base, and its inputs are not used.
  * Products accumulate in fp32 and every output is rounded once: X A and G meet
  * the next product as sums of bf16 values that hold 16 bits of them (24 for the
- * float gradients).  Results do not depend on timing: no sums by
- * floating-point atomics.
+ * float gradients).  Infinities and NaN in X and dY follow the formulas; an
+ * infinity in an adapter makes what it reaches infinite or NaN.  Results do not
+ * depend on timing: no sums by floating-point atomics.
  */
 #define SALR_ADAPTERS_MAX 4096
 

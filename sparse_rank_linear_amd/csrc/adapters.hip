@@ -58,7 +58,9 @@ __device__ __forceinline__ int group_of(const uint32_t* start, int n, uint32_t x
 // ballot for each bit of its number.  Then the lists of tiles and chunks.
 // Bound by its chain of barriers and LDS and memory round trips (64 tokens 6.0
 // us, 8192 tokens of 16 adapters 10.2; with the ids read and matched twice 6.6
-// and 10.8): once for all projections of a batch.
+// and 10.8): once for all projections of a batch.  From some 16384 tokens on one
+// workgroup is too few (65536 tokens of 16 adapters in 64 runs 43 us, in any
+// order 83; 2^20 tokens 592 and 1246).
 __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_t* ids, AdapterPlan p, int waves,
                                                                     int bits) {
   extern __shared__ uint32_t sm[];
@@ -244,9 +246,14 @@ __device__ __forceinline__ f32x4_t sum_pieces(const float* at, int64_t plane, in
 // workgroups take a tile's pieces (they run on different dies: a die then sees
 // the same pieces of the adapters again and again, in its own cache; empty
 // workgroups between them would leave some dies less to do).  Bound by
-// the reads of X and dY: 8192 tokens x 4096, rank 16, both sides 37 us, 3.6
-// TB/s (and 8 MB of pieces written); 8191 prompt tokens 25.4, 2.6
-// TB/s (ranks 8 to 64: a tile of 64 ranks holds 132 registers).  One token: a
+// the reads of X and dY, and above 32 ranks by how few waves have them in flight:
+// 8192 tokens x 4096, rank 16, both sides 37.5 us, 3.6 TB/s (and 8 MB of pieces
+// written; 122 + 36 registers and accumulators a lane, three waves a SIMD); 8191
+// prompt tokens 25, 2.7 TB/s (ranks 8 to 64: 132 + 88, two waves); rank 80, 4099
+// tokens, 4096 + 11008 columns 51, 2.4 TB/s (150 + 116, ten more than two waves
+// would leave each, so one, without loads ahead); ranks 128 and 256 run as two
+// and four groups of 64, each of which reads the tokens again (8192 tokens x
+// 4096, both sides: 105 and 162 us).  One token: a
 // wait for memory, 3.3 us.  One launch with the outputs' kernel, each workgroup
 // of a small tile contracting for itself, takes longer than the two: 64 tokens
 // of 64 adapters 30 us for 20, one token 9.2 for 8.6.
@@ -388,7 +395,11 @@ __global__ __launch_bounds__(kThreads) void adapter_finish_kernel(AdapterCommon 
 // ends up with twice 8 consecutive outputs of one token, and four lanes with 64
 // bytes that lie together.  Bound by memory, reads and writes in equal parts:
 // 8191 tokens x 11008 outputs 101 us, 3.6 TB/s (a copy of that size: 74); 8192 x
-// 4096 32 us, 4.2.  Stores past the caches are slower.
+// 4096 32 us, 4.2.  Stores past the caches are slower.  Above 96 ranks
+// (large tiles: 128) the weights of 64 outputs leave room for one wave a SIMD (64
+// tokens, 4096 outputs, rank 128 6.4 us, 256 10.8; 8192 tokens 67 and 142 to 157).
+// An adapter of fewer ranks than are stored is read whole, as its ranks share
+// their lines (64 adapters of 64 to 8 ranks: 34.6 MB for 16).
 template <int RC, int NS, bool PLANES>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, AdapterUp u) {
   constexpr int kPitch = RC * 32 + 8;
@@ -537,7 +548,8 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterCommon c, A
 }
 
 // ---- the adapters transposed (for the gradients): [R][C] -> [C][R], those
-// with tokens only, 64 x 64 at a time; their bytes twice, 3 to 9 us ----
+// with tokens only, 64 x 64 at a time; their bytes twice, 3 to 9 us, and 25 for
+// 16 adapters of rank 256 ----
 __global__ __launch_bounds__(kThreads) void adapter_transpose_kernel(AdapterCommon c, const uint16_t* a, uint16_t* at,
                                                                      int64_t K, const uint16_t* b, uint16_t* bt,
                                                                      int64_t N) {
@@ -575,9 +587,10 @@ __global__ __launch_bounds__(kThreads) void adapter_transpose_kernel(AdapterComm
 // 32 tokens at a time go to LDS as they are and come back transposed (4 x 16
 // values a 16 lanes).  T and G are three bf16 planes each: the float sums see
 // all their bits.  Bound by the reads of X and dY, once for each group of up to
-// 80 ranks: 8192 tokens, rank 16, 4096 x 4096 32 us, 4.2 TB/s; rank 80, 4099
-// tokens, 4096 x 11008 46 us, 2.7 TB/s, three products a pair and 40
-// accumulators a lane.
+// 80 ranks: 8192 tokens, rank 16, 4096 x 4096 33.5 us, 4.0 TB/s; rank 80, 4099
+// tokens, 4096 x 11008 48 us, 2.6 TB/s, three products a pair and 40
+// accumulators a lane.  A look at one value a token first, for what is not
+// finite, takes 1 us of each; at the columns themselves, stage by stage, up to 13.
 
 __device__ __forceinline__ u32x4_t read_transposed(const uint16_t* tile, int pitch, int lane) {
   // lane (i, g) gets column i of rows 4g..4g+3 and 16+4g..16+4g+3

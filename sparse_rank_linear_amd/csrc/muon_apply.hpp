@@ -16,7 +16,9 @@ namespace {
 // x 1408, bf16 parameters and float gradients, 179 us (3.6 TB/s; the
 // products are a quarter of it), 64 of 112 x 4096 and 112 x 14336 with masters
 // 592 us (4.0 TB/s), three of 253 x 8191 and 253 x 14337 149 us (273 MB, 56 us,
-// and 8.9 GFLOP, 58).
+// and 8.9 GFLOP, 58).  The forms of 3, 6, 7 and 16 tiles, and of 5 and 12 with
+// masters (5 also floats with bf16 gradients), spill up to 27 registers under the
+// bounds below.
 // Stores past the caches, loads ahead by two stages and stores spread over the
 // next stage's products were all slower.
 template <int NT>

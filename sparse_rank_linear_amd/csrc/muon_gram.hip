@@ -11,13 +11,15 @@ namespace {
 // such groups take every kParts-th 16 columns of a stage.  Sixteen columns'
 // sums are float, then join a double: the smallest eigenvalues decide how fast
 // their directions grow, and longer float sums drown them (an 80 x 2048 update
-// whose singular values differ 200-fold: X is 2e-5 off; summed in float over
+// whose singular values differ 250-fold: X is 1.5e-5 off; summed in float over
 // 64 columns 6e-5, and over all of them some 1e-3).  The next stage's loads are
 // under way while one is multiplied.  Bound by memory (g and m read, m written)
 // up to the ranks of ordinary adapters: 192 pairs of 80 x 2048 and 80 x 1408 in
 // 120 us, 5.3 TB/s; 64 of 112 x 4096 and 112 x 14336 381 us, 4.2; above those by
 // a CU's one workgroup, whose loads, LDS reads and products follow each other:
-// three of 253 x 8191 and 253 x 14337 in 114 us (205 MB, 42 us, and 4.7 GFLOP, 31).
+// three of 253 x 8191 and 253 x 14337 in 114 us (205 MB, 42 us, and 4.7 GFLOP, 31;
+// 16 waves leave 128 registers a lane, and the 16 tiles' form spills 88: a wait
+// for one of those waits for the loads that are to stay in flight too).
 template <int NT>
 struct GramShape {
   static constexpr int KB = muon_stage(NT), S = 16 * NT;

@@ -23,11 +23,12 @@ namespace {
 // wave.  The first kMuonDouble steps in double (see gram): products of float
 // matrices put noise of 2^-24 of the largest eigenvalue on the smallest ones,
 // which grow by a^2 = 12 a step, so what the later steps add counts for 1700
-// times less (an 80 x 2048 update whose singular values differ 200-fold: X is
-// 1e-5 off, after two such steps 5e-5, by float steps on X itself 4e-6; a step
+// times less (an 80 x 2048 update whose singular values differ 250-fold: X is
+// 1.5e-5 off, after two such steps 5e-5, by float steps on X itself 4e-6; a step
 // in float takes 6 us, in double 9.5).  Q is float throughout.  Bound by the
 // chain of products of one matrix, each waiting for LDS: 53 us for rank 80,
-// alone or one matrix a CU; 159 for 128 matrices of rank 112.
+// alone or one matrix a CU, of which nine products in double are 19 on the matrix
+// cores and eight in float some 8; 159 for 128 matrices of rank 112.
 constexpr int kTileP = 17, kTileD = 16 * kTileP;  // (rows padded: columns lie on distinct banks)
 constexpr int kMuonDouble = 3;
 
@@ -237,6 +238,8 @@ __global__ __launch_bounds__(IterShape<NT>::kThreads) void muon_iterate_kernel(M
 // halves in double take more than a CU's LDS.)  14 products for five steps, 12.4
 // us each for six matrices of 256 x 256: a launch, a trip through the caches for
 // operands that other dies wrote, 16 double products a wave one after another.
+// Hundreds of matrices are bound by those trips: 380 of 256 x 256, 8.7 ms a step
+// (256 x 411, bf16), of which a plain step in float takes 6.3.
 struct MuonProduct {
   // out = left right: which of the matrix's six
   int left, right, out;

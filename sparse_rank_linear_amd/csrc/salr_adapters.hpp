@@ -16,9 +16,10 @@ namespace salr {
 // (8191 tokens, ranks 8 to 64, 4096 x 11008: 133 us, with small tiles 228).
 constexpr int kAdapterSmallTile = 16, kAdapterLargeTile = 64;
 constexpr int64_t kAdapterSmallTokens = 1024;  // the most with small tiles
-// Tokens that one workgroup sums a gradient over, at least, and not more than 64
-// partial sums in all: products and sums take 54 us for 4099 tokens of 6
-// adapters, rank 80, 4096 x 11008, in chunks of 1024 tokens 65, of 256 62.
+// Tokens that one workgroup sums a gradient over, at least (more from 16384
+// tokens on, a 32nd of them), and so not more than 64 partial sums in all:
+// products and sums take 56 us for 4099 tokens of 6 adapters, rank 80, 4096 x
+// 11008, in chunks of 1024 tokens 64, of 256 63.
 constexpr int kAdapterMinChunk = 512;
 constexpr int kAdapterMaxSplits = 32;  // pieces of a contraction over K (or N)
 constexpr int kAdapterThreads = 256;   // of a workgroup, all kernels but the plan's
@@ -43,7 +44,7 @@ struct AdapterPlan {
   AdapterTile* chunks;
   int64_t M;
   int32_t count, tile, chunk;
-  int32_t max_tiles, max_chunks, max_parts;
+  int32_t max_tiles, max_chunks;
 };
 
 // One contraction T[t][j] = sum_k X[t][k] W[a][j][k], in `splits` pieces of
@@ -76,8 +77,8 @@ struct AdapterUp {
   int32_t splits, slices;
 };
 
-// grad[a] = sum over a's tokens of cols[t][c] planes[t][j], stored [r][C]
-// (rank_major) or [C][r].  other: the planes of what cols gave.
+// The sum over an adapter's tokens of cols[t][c] planes[t][j], stored [r][C] (dA)
+// or [C][r] (dB).  other: the planes of what cols gave (dA: T, dB: G).
 struct AdapterGrad {
   const uint16_t* cols;
   const uint16_t* planes;

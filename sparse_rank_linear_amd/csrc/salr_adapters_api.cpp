@@ -44,7 +44,6 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
   p.tile = M <= salr::kAdapterSmallTokens ? salr::kAdapterSmallTile : salr::kAdapterLargeTile;
   p.max_tiles = (int32_t)most_pieces(M, count + 1, p.tile);
   p.max_chunks = (int32_t)most_pieces(M, count, p.chunk);
-  p.max_parts = (int32_t)std::min<int64_t>(p.max_chunks, 2 * M / p.chunk);
   size_t at = 0;
   const auto take = [&](size_t n) {
     const uintptr_t q = reinterpret_cast<uintptr_t>(buffer) + at;  // (the buffer may be null: sizes alone)
@@ -69,11 +68,17 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
 // Contractions over their columns in pieces: enough workgroups for the CUs, and
 // fewer for small tiles, whose pieces are summed by every workgroup that uses
 // them, and where a token's sums are long (each piece writes them).  Above
-// kFewRanks a CU holds three workgroups of large tiles: pieces as long for one
-// contraction as for the other, as many as one round of workgroups takes, in
-// eights where there are eight (4099 tokens, rank 80, 4096 and 11008 columns:
-// 51 us in 8 pieces; in 10 or 11 56, in 16 and two rounds 55).  Up to kFewRanks,
-// two rounds are better than one (8192 tokens, rank 16: 37 us for 40).
+// kFewRanks, pieces as long for one contraction as for the other and kRound
+// workgroups in all, in eights where there are eight (4099 tokens, rank 80, 4096
+// and 11008 columns: 51 us in 8 pieces; in 10 or 11 56, in 16 55).  A CU holds
+// one workgroup of large tiles at a time at rank 80 (266 registers a lane), two
+// at 48 and 64; with 256, 512, 768 and 1024 workgroups that batch takes 67, 53,
+// 51 and 50 us, and 8192 tokens with 4096 columns on both sides 79, 64, 60 and
+// 56 at rank 64 and 73, 58, 55 and 51 at rank 48: more pieces are better there,
+// while their sums take up to 2 us more.  Up to kFewRanks kGroups workgroups or
+// more for each contraction (rank 16: 37.5 us, cut as above 43.5; 24: 41.5 and
+// 47; 32: 44.5 and 48.5).  The two, their sums added, come together at rank 64
+// (40: 58 and 60 us, 48: 60 and 62, 64: 68 and 68).
 //   Each of `work` tiles has at most 64 tokens, so that one piece, or up to
 // (kGroups + work) / work, or up to kRound / work, come to at most M + 64
 // kGroups rows of T, and as many as kAdapterMaxSplits M.
