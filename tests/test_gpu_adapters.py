@@ -385,6 +385,30 @@ def test_gradients_of_infinite_values_follow_the_formula(M, r, ranks, where, val
         assert not bad.any(), (name, np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
 
 
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), NAN])
+@pytest.mark.parametrize("M,r", [(1, 8), (200, 40), (3000, 96)])
+def test_outputs_of_infinite_values_follow_the_formula(M, r, value):
+    """One value of X, then one of the base as well: what the formula gives, and
+    other tokens as without them."""
+    srl = _srl()
+    c = Case(M, 2, r, 136, 72, M % 2, mixed=False, seed=M)
+    plan = srl.adapters_plan(c.ids_d, 2)
+    c.X[M // 2, 77] = c.X_d[M // 2, 77] = 0.0
+    clean = srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d)
+    c.check_forward(clean)
+    for base in (False, True):
+        c.X[M // 2, 77] = c.X_d[M // 2, 77] = value
+        if base:
+            c.by[M // 2, 5] = c.by_d[M // 2, 5] = float("inf")
+        got = srl.adapters_forward(c.ad, plan, c.X_d, base=c.by_d).double().cpu().numpy()
+        with np.errstate(invalid="ignore"):
+            want = oa.forward(c.a, c.b, c.ids, c.ranks, c.scales, c.X, c.by)
+        assert not np.isfinite(want[M // 2]).any()
+        np.testing.assert_array_equal(got[M // 2], want[M // 2])
+        others = np.arange(M) != M // 2
+        assert (got[others] == clean.double().cpu().numpy()[others]).all()
+
+
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("M", [1, 1100])
 def test_sums_that_bf16_would_round_to_infinity(M, sign):
