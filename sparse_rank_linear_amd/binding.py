@@ -1319,7 +1319,9 @@ class SalrAdapters:
     """`count` low-rank adapters of one layer, stacked as include/salr.h lays
     them out (salr_adapters_t): a bf16 [count][r][K], b bf16 [count][N][r];
     optionally how many ranks each uses (ranks, device int32 [count]) and its
-    scale (scales, device float [count])."""
+    scale (scales, device float [count]).  A call uses the tensors as they are
+    when it is made: they, their memory and their shapes may change between
+    calls."""
 
     a: object
     b: object
