@@ -74,8 +74,8 @@ salr::AdapterPlan lay_out_plan(void* buffer, int64_t M, int32_t count, size_t* b
 // one workgroup of large tiles at a time at rank 80 (266 registers a lane), two
 // at 48 and 64; with 256, 512, 768 and 1024 workgroups that batch takes 67, 53,
 // 51 and 50 us, and 8192 tokens with 4096 columns on both sides 79, 64, 60 and
-// 56 at rank 64 and 73, 58, 55 and 51 at rank 48: more pieces are better there,
-// while their sums take up to 2 us more.  Up to kFewRanks kGroups workgroups or
+// 56 at rank 64 and 73, 58, 55 and 51 at rank 48, their sums 0.2 more: there more
+// pieces would be better.  Up to kFewRanks kGroups workgroups or
 // more for each contraction (rank 16: 37.5 us, cut as above 43.5; 24: 41.5 and
 // 47; 32: 44.5 and 48.5).  The two, their sums added, come together at rank 64
 // (40: 58 and 60 us, 48: 60 and 62, 64: 68 and 68).
